@@ -34,7 +34,9 @@ EXPORTS = ("glu_fwd", "glu_bwd", "glu_fwd_host", "glu_bwd_host", "glu_fwd_host_n
            "glu_status_string", "glu_last_cuda_error", "glu_version", "glu_last_launch",
            "glu_set_tuning", "glu_get_tuning", "glu_wait_timeouts", "glu_wait_selftest", "glu_gemm_fwd",
            "glu_gemm_nt", "glu_mlp_fwd", "glu_mlp_workspace_bytes",
-           "glu_add_rmsnorm_fwd", "glu_add_rmsnorm_bwd")
+           "glu_add_rmsnorm_fwd", "glu_add_rmsnorm_bwd",
+           "glu_quantize", "glu_add_rmsnorm_q", "glu_gemm_q_nt", "glu_gemm_q_fwd", "glu_gemm_q_grouped_nt",
+           "glu_gemm_q_grouped_fwd")
 
 
 class GluError(RuntimeError):
@@ -124,6 +126,22 @@ def lib() -> ctypes.CDLL:
             L.glu_add_rmsnorm_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, i64,
                                               ci, vp]
             L.glu_add_rmsnorm_bwd.restype = ci
+            L.glu_quantize.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, ci, ci, vp]
+            L.glu_quantize.restype = ci
+            L.glu_add_rmsnorm_q.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp, i64, i64,
+                                            ctypes.c_float, ci, vp]
+            L.glu_add_rmsnorm_q.restype = ci
+            L.glu_gemm_q_nt.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, ci, vp]
+            L.glu_gemm_q_nt.restype = ci
+            L.glu_gemm_q_fwd.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, i64, i64, i64, i64,
+                                         ci, vp]
+            L.glu_gemm_q_fwd.restype = ci
+            L.glu_gemm_q_grouped_nt.argtypes = [vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp, i64, i64, i64, i64,
+                                                vp, i64, ci, vp]
+            L.glu_gemm_q_grouped_nt.restype = ci
+            L.glu_gemm_q_grouped_fwd.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, vp, vp, i64, i64, vp, i64, vp,
+                                                 i64, i64, i64, i64, vp, i64, ci, vp]
+            L.glu_gemm_q_grouped_fwd.restype = ci
             _lib = L
     return _lib
 
@@ -238,6 +256,43 @@ def glu_add_rmsnorm_bwd(dy, dy_stride, h, h_stride, rstd, gamma, dh, dh_stride, 
                         dgamma, n_rows, n_cols, dtype, stream) -> int:
     return lib().glu_add_rmsnorm_bwd(dy, dy_stride, h, h_stride, rstd, gamma, dh, dh_stride, dx, dx_stride, dres,
                                      dres_stride, dgamma, n_rows, n_cols, dtype, stream)
+
+
+def glu_quantize(x, x_stride, q, q_stride, scale, scale_stride, n_rows, n_cols, block_rows, dtype, stream) -> int:
+    return lib().glu_quantize(x, x_stride, q, q_stride, scale, scale_stride, n_rows, n_cols, block_rows, dtype, stream)
+
+
+def glu_add_rmsnorm_q(x, x_stride, residual, res_stride, gamma, h, h_stride, q, q_stride, scale, scale_stride, rstd,
+                      n_rows, n_cols, eps, dtype, stream) -> int:
+    return lib().glu_add_rmsnorm_q(x, x_stride, residual, res_stride, gamma, h, h_stride, q, q_stride, scale,
+                                   scale_stride, rstd, n_rows, n_cols, eps, dtype, stream)
+
+
+def glu_gemm_q_nt(a, a_stride, a_scale, a_scale_stride, b, b_stride, b_scale, b_scale_stride, d, d_stride, M, K, N,
+                  dtype, stream) -> int:
+    return lib().glu_gemm_q_nt(a, a_stride, a_scale, a_scale_stride, b, b_stride, b_scale, b_scale_stride, d,
+                               d_stride, M, K, N, dtype, stream)
+
+
+def glu_gemm_q_fwd(x, x_stride, x_scale, x_scale_stride, w_gate, w_up, w_stride, gate_scale, up_scale, w_scale_stride,
+                   y, y_stride, y_scale, y_scale_stride, M, K, I, act, stream) -> int:
+    return lib().glu_gemm_q_fwd(x, x_stride, x_scale, x_scale_stride, w_gate, w_up, w_stride, gate_scale, up_scale,
+                                w_scale_stride, y, y_stride, y_scale, y_scale_stride, M, K, I, act, stream)
+
+
+def glu_gemm_q_grouped_nt(a, a_stride, a_scale, a_scale_stride, b, b_stride, b_group, b_scale, b_scale_stride,
+                          b_scale_group, d, d_stride, M, K, N, offsets, n_groups, dtype, stream) -> int:
+    return lib().glu_gemm_q_grouped_nt(a, a_stride, a_scale, a_scale_stride, b, b_stride, b_group, b_scale,
+                                       b_scale_stride, b_scale_group, d, d_stride, M, K, N, offsets, n_groups, dtype,
+                                       stream)
+
+
+def glu_gemm_q_grouped_fwd(x, x_stride, x_scale, x_scale_stride, w_gate, w_up, w_stride, w_group, gate_scale,
+                           up_scale, w_scale_stride, w_scale_group, y, y_stride, y_scale, y_scale_stride, M, K, I,
+                           offsets, n_groups, act, stream) -> int:
+    return lib().glu_gemm_q_grouped_fwd(x, x_stride, x_scale, x_scale_stride, w_gate, w_up, w_stride, w_group,
+                                        gate_scale, up_scale, w_scale_stride, w_scale_group, y, y_stride, y_scale,
+                                        y_scale_stride, M, K, I, offsets, n_groups, act, stream)
 
 
 def glu_get_tuning() -> dict:
@@ -509,6 +564,213 @@ def add_rmsnorm_bwd(dy, h, rstd, gamma, *, dh=None, dx=None, dres=None, dgamma=N
     if st:
         raise GluError(st, "glu_add_rmsnorm_bwd")
     return (dx, dgamma) if want_dg else dx
+
+
+# ---- 8-bit floating point ----------------------------------------------------------
+
+def _same_device(x, *others):
+    """Every tensor on x's device, which is the current one (the device the
+    library launches on)."""
+    import torch
+    dev = x.device
+    if not x.is_cuda or dev.index != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current CUDA device")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on one device")
+
+
+def _groups(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _empty_q(shape, device):
+    """An e4m3 tensor whose rows start on 16-byte boundaries (the products'
+    rule): the last dimension of a wider tensor where it is no multiple of 16."""
+    import torch
+    n = shape[-1]
+    if n % 16 == 0:
+        return torch.empty(shape, dtype=torch.float8_e4m3fn, device=device)
+    return torch.empty((*shape[:-1], n + -n % 16), dtype=torch.float8_e4m3fn, device=device)[..., :n]
+
+
+def _check_q(q, scale, name):
+    import torch
+    if q.dtype != torch.float8_e4m3fn or scale.dtype != torch.float32:
+        raise TypeError(f"{name} must be float8_e4m3fn with float32 scales")
+
+
+def _scale_rows(scale, shape, name):
+    """Row stride of a scale matrix of the given shape."""
+    if tuple(scale.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(scale.shape)}")
+    return _rows(scale, name)[1]
+
+
+def _weight(w, s, K, name, grouped):
+    """(N, row stride, expert stride, scale's row stride, scale's expert stride) of (N, K) or (E, N, K) weights."""
+    _check_q(w, s, name)
+    if w.dim() != (3 if grouped else 2) or w.shape[-1] != K:
+        raise ValueError(f"{name} must be {'(E, N, K)' if grouped else '(N, K)'} with K = {K}")
+    N = w.shape[-2]
+    want = (*w.shape[:-2], _groups(N), _groups(K))
+    if tuple(s.shape) != want:
+        raise ValueError(f"{name}'s scales must have shape {want}, not {tuple(s.shape)}")
+    if (w.stride(-1) != 1 and K > 1) or (s.stride(-1) != 1 and s.shape[-1] > 1):
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return (N, w.stride(-2), w.stride(0) if grouped else 0, s.stride(-2), s.stride(0) if grouped else 0)
+
+
+def _offsets(offsets, w):
+    import torch
+    if offsets.dtype != torch.int32 or not offsets.is_contiguous() or offsets.shape != (w.shape[0] + 1,):
+        raise ValueError("offsets must be a contiguous int32 tensor of one entry more than there are experts")
+
+
+def quantize(x, *, block_rows: int = 1, q=None, scale=None, stream=None):
+    """(q, scale) of x in e4m3 with a float32 scale for each block of 128
+    columns: of one row (``block_rows`` = 1, activations; x is (..., K) and
+    scale (..., ceil(K / 128))), or of 128 rows (128, weights; x is (N, K), or
+    (E, N, K) for the weights of E experts, and scale (.., ceil(N / 128),
+    ceil(K / 128)))."""
+    import torch
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    code = _dtype_code(x)
+    if block_rows == 128:
+        if x.dim() not in (2, 3):
+            raise ValueError("x must be (N, K) or (E, N, K) for 128 x 128 blocks")
+        shape = (*x.shape[:-2], _groups(x.shape[-2]), _groups(x.shape[-1]))
+    else:
+        shape = (*x.shape[:-1], _groups(x.shape[-1]))
+    _same_device(x, q, scale)
+    q = _empty_q(x.shape, x.device) if q is None else q
+    scale = torch.empty(shape, dtype=torch.float32, device=x.device) if scale is None else scale
+    _check_q(q, scale, "q")
+    if q.shape != x.shape or tuple(scale.shape) != tuple(shape):
+        raise ValueError("q and scale must have the shapes of x and of its blocks")
+    st = 0
+    parts = [(x, q, scale)] if x.dim() < 3 or block_rows == 1 else list(zip(x, q, scale))
+    for xe, qe, se in parts:
+        n_rows, x_stride = _rows(xe, "x")
+        st = st or glu_quantize(xe.data_ptr(), x_stride, qe.data_ptr(), _rows(qe, "q")[1], se.data_ptr(),
+                                _rows(se, "scale")[1], n_rows, xe.shape[-1], block_rows, code, _stream(stream))
+    if st:
+        raise GluError(st, "glu_quantize")
+    return q, scale
+
+
+def add_rmsnorm_q(x, residual, gamma, eps: float = 1e-5, *, h=None, q=None, scale=None, rstd=None, stream=None):
+    """h = x + residual, and rmsnorm(h) * gamma over the last dimension as
+    (q, scale): e4m3 with a float32 scale for each 128 columns of a row, in one
+    pass.  ``h`` may be x or residual; ``rstd`` as in add_rmsnorm.  Returns
+    (h, q, scale) or (h, q, scale, rstd)."""
+    import torch
+    _same_device(x, residual, gamma, h, q, scale)
+    n_rows, x_stride = _rows(x, "x")
+    _, r_stride = _rows(residual, "residual")
+    if residual.shape != x.shape or residual.dtype != x.dtype:
+        raise ValueError("residual must match x in shape and dtype")
+    H = x.shape[-1]
+    if gamma.shape != (H,) or gamma.dtype != x.dtype or not gamma.is_contiguous():
+        raise ValueError("gamma must be a contiguous (H,) tensor of x's dtype")
+    h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if h is None else h
+    if h.shape != x.shape or h.dtype != x.dtype:
+        raise ValueError("h must match x in shape and dtype")
+    shape = (*x.shape[:-1], _groups(H))
+    q = _empty_q(x.shape, x.device) if q is None else q
+    scale = torch.empty(shape, dtype=torch.float32, device=x.device) if scale is None else scale
+    _check_q(q, scale, "q")
+    if q.shape != x.shape:
+        raise ValueError("q must match x in shape")
+    s_stride = _scale_rows(scale, shape, "scale")
+    want_rstd = rstd is not None and rstd is not False
+    if rstd is True:
+        rstd = torch.empty(n_rows, dtype=torch.float32, device=x.device)
+    if want_rstd and (rstd.dtype != torch.float32 or rstd.numel() != n_rows or not rstd.is_contiguous() or
+                      rstd.device != x.device):
+        raise ValueError("rstd must be a contiguous float32 tensor with one entry per row")
+    st = glu_add_rmsnorm_q(x.data_ptr(), x_stride, residual.data_ptr(), r_stride, gamma.data_ptr(), h.data_ptr(),
+                           _rows(h, "h")[1], q.data_ptr(), _rows(q, "q")[1], scale.data_ptr(), s_stride,
+                           rstd.data_ptr() if want_rstd else None, n_rows, H, float(eps), _dtype_code(x),
+                           _stream(stream))
+    if st:
+        raise GluError(st, "glu_add_rmsnorm_q")
+    return (h, q, scale, rstd) if want_rstd else (h, q, scale)
+
+
+def gemm_q_nt(a, a_scale, b, b_scale, *, d=None, dtype=None, offsets=None, stream=None):
+    """d = a @ b^T of quantised matrices on the tensor cores, in ``dtype``
+    (float16 or bfloat16, the default; d's when d is given).  a is (..., K) with
+    scales by rows, b (N, K) with scales by 128 x 128 blocks.  With ``offsets``
+    (int32, E + 1 entries, on the device) b is (E, N, K) and a's rows offsets[e]
+    .. offsets[e + 1] are multiplied by b[e]; rows of d that no expert has are
+    left as they were."""
+    import torch
+    _same_device(a, a_scale, b, b_scale, d, offsets)
+    _check_q(a, a_scale, "a")
+    n_rows, a_stride = _rows(a, "a")
+    K = a.shape[-1]
+    as_stride = _scale_rows(a_scale, (*a.shape[:-1], _groups(K)), "a_scale")
+    grouped = offsets is not None
+    N, b_stride, b_group, bs_stride, bs_group = _weight(b, b_scale, K, "b", grouped)
+    if d is None:
+        d = torch.empty((*a.shape[:-1], N), dtype=dtype or torch.bfloat16, device=a.device)
+    if tuple(d.shape) != (*a.shape[:-1], N) or (dtype is not None and d.dtype != dtype):
+        raise ValueError("d has the wrong shape or dtype")
+    _, d_stride = _rows(d, "d")
+    code = _dtype_code(d)
+    if grouped:
+        _offsets(offsets, b)
+        st = glu_gemm_q_grouped_nt(a.data_ptr(), a_stride, a_scale.data_ptr(), as_stride, b.data_ptr(), b_stride,
+                                   b_group, b_scale.data_ptr(), bs_stride, bs_group, d.data_ptr(), d_stride, n_rows,
+                                   K, N, offsets.data_ptr(), b.shape[0], code, _stream(stream))
+    else:
+        st = glu_gemm_q_nt(a.data_ptr(), a_stride, a_scale.data_ptr(), as_stride, b.data_ptr(), b_stride,
+                           b_scale.data_ptr(), bs_stride, d.data_ptr(), d_stride, n_rows, K, N, code, _stream(stream))
+    if st:
+        raise GluError(st, "glu_gemm_q_grouped_nt" if grouped else "glu_gemm_q_nt")
+    return d
+
+
+def gemm_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, y=None, y_scale=None, act: str = "silu",
+               offsets=None, stream=None):
+    """(y, y_scale): act(x @ w_gate^T) * (x @ w_up^T) of quantised matrices, on
+    the tensor cores, quantised by rows in the epilogue.  x is (..., K), the
+    weights (I, K) with one row stride, or (E, I, K) with ``offsets`` (see
+    gemm_q_nt)."""
+    import torch
+    _same_device(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, y_scale, offsets)
+    _check_q(x, x_scale, "x")
+    n_rows, x_stride = _rows(x, "x")
+    K = x.shape[-1]
+    xs_stride = _scale_rows(x_scale, (*x.shape[:-1], _groups(K)), "x_scale")
+    grouped = offsets is not None
+    N, *gate = _weight(w_gate, gate_scale, K, "w_gate", grouped)
+    if w_up.shape != w_gate.shape or _weight(w_up, up_scale, K, "w_up", grouped)[1:] != tuple(gate):
+        raise ValueError("w_gate and w_up (and their scales) must have one shape and one stride")
+    w_stride, w_group, s_stride, s_group = gate
+    y = _empty_q((*x.shape[:-1], N), x.device) if y is None else y
+    shape = (*x.shape[:-1], _groups(N))
+    y_scale = torch.empty(shape, dtype=torch.float32, device=x.device) if y_scale is None else y_scale
+    _check_q(y, y_scale, "y")
+    if tuple(y.shape) != (*x.shape[:-1], N):
+        raise ValueError("y has the wrong shape")
+    ys_stride = _scale_rows(y_scale, shape, "y_scale")
+    _, y_stride = _rows(y, "y")
+    if grouped:
+        _offsets(offsets, w_gate)
+        st = glu_gemm_q_grouped_fwd(x.data_ptr(), x_stride, x_scale.data_ptr(), xs_stride, w_gate.data_ptr(),
+                                    w_up.data_ptr(), w_stride, w_group, gate_scale.data_ptr(), up_scale.data_ptr(),
+                                    s_stride, s_group, y.data_ptr(), y_stride, y_scale.data_ptr(), ys_stride, n_rows,
+                                    K, N, offsets.data_ptr(), w_gate.shape[0], ACT[act], _stream(stream))
+    else:
+        st = glu_gemm_q_fwd(x.data_ptr(), x_stride, x_scale.data_ptr(), xs_stride, w_gate.data_ptr(), w_up.data_ptr(),
+                            w_stride, gate_scale.data_ptr(), up_scale.data_ptr(), s_stride, y.data_ptr(), y_stride,
+                            y_scale.data_ptr(), ys_stride, n_rows, K, N, ACT[act], _stream(stream))
+    if st:
+        raise GluError(st, "glu_gemm_q_grouped_fwd" if grouped else "glu_gemm_q_fwd")
+    return y, y_scale
 
 
 # ---- host tensors ---------------------------------------------------------------

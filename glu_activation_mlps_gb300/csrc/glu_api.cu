@@ -485,9 +485,10 @@ int validate_fwd(const void *a, int64_t a_stride, const void *b, int64_t b_strid
     return GLU_OK;
 }
 
-int validate_add_rmsnorm(const void *x, int64_t x_stride, const void *res, int64_t res_stride,
-                         const void *gamma, const void *h, int64_t h_stride, const void *y, int64_t y_stride,
-                         const float *rstd, int64_t n_rows, int64_t n_cols, float eps, int dtype, bool *empty)
+// The argument rules of the residual add + RMSNorm, with y or without.
+static int validate_rms(const void *x, int64_t x_stride, const void *res, int64_t res_stride, const void *gamma,
+                        const void *h, int64_t h_stride, bool has_y, const void *y, int64_t y_stride,
+                        const float *rstd, int64_t n_rows, int64_t n_cols, float eps, int dtype, bool *empty)
 {
     *empty = false;
     if (!(dtype == GLU_F32 || dtype == GLU_F16 || dtype == GLU_BF16)) return GLU_ERR_ENUM;
@@ -495,7 +496,11 @@ int validate_add_rmsnorm(const void *x, int64_t x_stride, const void *res, int64
     if (!(eps > 0.0f) || !(eps < INFINITY)) return GLU_ERR_VALUE;
     if (n_rows == 0 || n_cols == 0) { *empty = true; return GLU_OK; }
     if (n_cols > kRmsMaxCols) return GLU_ERR_SHAPE;
-    if (!x || !res || !gamma || !h || !y) return GLU_ERR_NULL;
+    if (!x || !res || !gamma || !h || (has_y && !y)) return GLU_ERR_NULL;
+    if (!has_y) {           // h stands for both outputs below
+        y = h;
+        y_stride = h_stride;
+    }
     if (n_rows == 1) x_stride = res_stride = h_stride = y_stride = n_cols;
     if (x_stride < n_cols || res_stride < n_cols || h_stride < n_cols || y_stride < n_cols)
         return GLU_ERR_STRIDE;
@@ -507,7 +512,7 @@ int validate_add_rmsnorm(const void *x, int64_t x_stride, const void *res, int64
         extent_bytes(my, n_rows, E) < 0 || extent_bytes(mg, 1, E) < 0)
         return GLU_ERR_SHAPE;
     const Mat ins[2] = {mx, mr}, outs[2] = {mh, my};
-    if (int st = check_aliasing(ins, 2, outs, 2, n_rows, E)) return st;
+    if (int st = check_aliasing(ins, 2, outs, has_y ? 2 : 1, n_rows, E)) return st;
     // gamma is read by every row: no output element may lie on it
     for (const Mat &o : outs)
         if (rows_hit_range(o, n_rows, E, mg.p, uint64_t(n_cols) * E)) return GLU_ERR_ALIAS;
@@ -521,6 +526,22 @@ int validate_add_rmsnorm(const void *x, int64_t x_stride, const void *res, int64
         }
     }
     return GLU_OK;
+}
+
+int validate_add_rmsnorm(const void *x, int64_t x_stride, const void *res, int64_t res_stride,
+                         const void *gamma, const void *h, int64_t h_stride, const void *y, int64_t y_stride,
+                         const float *rstd, int64_t n_rows, int64_t n_cols, float eps, int dtype, bool *empty)
+{
+    return validate_rms(x, x_stride, res, res_stride, gamma, h, h_stride, true, y, y_stride, rstd, n_rows, n_cols,
+                        eps, dtype, empty);
+}
+
+int validate_add_rmsnorm_inputs(const void *x, int64_t x_stride, const void *res, int64_t res_stride,
+                                const void *gamma, const void *h, int64_t h_stride, const float *rstd,
+                                int64_t n_rows, int64_t n_cols, float eps, int dtype, bool *empty)
+{
+    return validate_rms(x, x_stride, res, res_stride, gamma, h, h_stride, false, nullptr, 0, rstd, n_rows, n_cols,
+                        eps, dtype, empty);
 }
 
 int validate_add_rmsnorm_bwd(const void *dy, int64_t dy_stride, const void *h, int64_t h_stride, const float *rstd,
@@ -712,9 +733,10 @@ int glu_version(void) { return GLU_VERSION; }
 int glu_wait_timeouts(unsigned int *count, int reset)
 {
     if (!count) return GLU_ERR_NULL;
-    unsigned int bulk = 0, gemm = 0, rms = 0, self = 0;
+    unsigned int bulk = 0, gemm = 0, gemm_q = 0, rms = 0, self = 0;
     cudaError_t e = glu::bulk_timeouts(&bulk, reset != 0);
     if (e == cudaSuccess) e = glu::gemm::timeouts(&gemm, reset != 0);
+    if (e == cudaSuccess) e = glu::gemmq::timeouts(&gemm_q, reset != 0);
     if (e == cudaSuccess) e = glu::rms::timeouts(&rms, reset != 0);
     if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&self, glu::g_selftest_timeouts, sizeof(unsigned int));
     if (e == cudaSuccess && reset) {
@@ -722,7 +744,7 @@ int glu_wait_timeouts(unsigned int *count, int reset)
         e = cudaMemcpyToSymbol(glu::g_selftest_timeouts, &zero, sizeof(unsigned int));
     }
     if (e != cudaSuccess) return cuda_fail(e);
-    *count = bulk + gemm + rms + self;
+    *count = bulk + gemm + gemm_q + rms + self;
     return GLU_OK;
 }
 

@@ -47,6 +47,7 @@
 #include "glu.h"
 #include "glu_kernels.cuh"
 #include "glu_internal.h"
+#include "glu_tensor.cuh"
 
 namespace glu {
 namespace gemm {
@@ -57,7 +58,6 @@ constexpr int kThreads = 192;            // warp 0 loads, warp 1 issues MMAs, wa
 constexpr int kEpiWarps = 4;
 constexpr int kRingBytes = 192 * 1024;   // shared memory given to the stage ring
 constexpr int kYBox = 32;                // y leaves through 32 x 32 boxes (64-byte rows, 64-byte swizzle)
-constexpr long long kBudget = 2000000000LL;   // ~1 s at 2 GHz
 
 template <int BN, int CTAS>
 struct Shape {
@@ -93,221 +93,6 @@ struct Params {
 };
 
 static __device__ unsigned int g_gemm_timeouts;
-
-__device__ __forceinline__ uint32_t saddr(const void *p)
-{
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-// Waits for the phase with the given parity to complete: spinning on
-// try_wait, for the producer and MMA threads that must react at once; false
-// once the clock budget has run out (checked every 16 tries).
-__device__ __forceinline__ bool wait_parity(uint32_t bar, uint32_t parity)
-{
-    const long long t0 = clock64();
-    for (uint32_t n = 1;; ++n) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (done) return true;
-        if ((n & 15) == 0 && clock64() - t0 > kBudget) return false;
-    }
-}
-
-// The same for the epilogue warps, which wait for a whole tile's MMAs: each
-// try_wait may suspend the warp until the phase completes (200 us at most), so
-// the waiting warps take no issue slots from the producer and MMA threads on
-// their sub-partitions (measured 1-3 % faster than spinning).
-__device__ __forceinline__ bool wait_parity_sleep(uint32_t bar, uint32_t parity)
-{
-    const long long t0 = clock64();
-    while (true) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity), "r"(200000u)
-            : "memory");
-        if (done) return true;
-        if (clock64() - t0 > kBudget) return false;
-    }
-}
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// Shared::cluster address of the same shared variable in block `rank` of the cluster.
-__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-__device__ __forceinline__ void arrive_local(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void arrive_cluster(uint32_t bar_cluster)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
-
-__device__ __forceinline__ void arrive_expect_tx_local(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-// Shared-memory matrix descriptor of a K-major tile stored as 128-byte rows
-// with the 128-byte swizzle: start address, leading byte offset (unused for
-// swizzled K-major tiles, encoded 1), stride byte offset 1024 (eight rows form
-// one swizzle atom), the fixed version bits 0b001 at 46, swizzle mode 2 at 61.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr)
-{
-    uint64_t d = 0;
-    d |= uint64_t((addr & 0x3FFFF) >> 4);
-    d |= uint64_t(1) << 16;
-    d |= uint64_t(1024 >> 4) << 32;
-    d |= uint64_t(1) << 46;
-    d |= uint64_t(2) << 61;
-    return d;
-}
-
-// Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator (bits
-// 4-5 = 1), A and B formats (bits 7-9, 10-12: 0 = f16, 1 = bf16), both
-// K-major (bits 15, 16 = 0), N >> 3 at bits 17-22, M >> 4 at bits 24-28.
-__host__ __device__ constexpr uint32_t idesc_f16(int ab_format, int M, int N)
-{
-    return (1u << 4) | (uint32_t(ab_format) << 7) | (uint32_t(ab_format) << 10) |
-           (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
-}
-
-// 2-D tiled copy into this block's shared memory; the barrier may belong to
-// the partner block when CTAS == 2.
-template <int CTAS>
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
-{
-    if constexpr (CTAS == 1)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-            "[%4];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
-            "{%2, %3}], [%4];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-            : "memory");
-}
-
-template <int CTAS>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    if constexpr (CTAS == 1)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(acc)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(acc)
-            : "memory");
-}
-
-// Arrive on `bar` (same offset in every block of the pair) once all MMAs this
-// thread issued so far are done.
-template <int CTAS>
-__device__ __forceinline__ void mma_commit(uint32_t bar)
-{
-    if constexpr (CTAS == 1)
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                     : "memory");
-    else
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                bar),
-            "h"(uint16_t(3))
-            : "memory");
-}
-
-template <int CTAS>
-__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols)
-{
-    if constexpr (CTAS == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    } else {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    }
-}
-
-template <int CTAS>
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols)
-{
-    if constexpr (CTAS == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
-    else
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
-}
-
-// 32 consecutive fp32 columns of this warp's 32 tensor-memory lanes.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
-
-// A 32 x 32 box of y from shared memory (64-byte swizzle) to global memory;
-// the tensor-memory accelerator drops rows and columns outside y.
-__device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int x, int y)
-{
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(src)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
-__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
-}
 
 // Tile t of the grouped order: group_m row blocks side by side walk the column blocks.
 __device__ __forceinline__ void tile_origin(const Params &p, int t, int &mb, int &ib)
@@ -618,27 +403,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 namespace glu {
 namespace gemm {
 namespace {
-
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn()
-{
-    static std::once_flag once;
-    static EncodeFn fn = nullptr;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeFn>(p);
-        else
-            (void)cudaGetLastError();
-    });
-    return fn;
-}
 
 // A rows x cols row-major matrix (row stride in bytes) as a 2-D tensor map
 // with a box of box_cols x box_rows; loads read zeros outside the matrix and

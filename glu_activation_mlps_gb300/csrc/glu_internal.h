@@ -31,6 +31,9 @@ cudaError_t timeouts(unsigned int *count, bool reset);   // glu_gemm.cu
 namespace rms {
 cudaError_t timeouts(unsigned int *count, bool reset);   // glu_rmsnorm.cu
 }
+namespace gemmq {
+cudaError_t timeouts(unsigned int *count, bool reset);   // glu_gemm_q.cu
+}
 void record_launch(const glu_launch_info_t &info);       // this thread's glu_last_launch
 // Whether p points into device memory (not pinned host or managed memory):
 // the tensor-memory accelerator and the bulk-copy engine are given device
@@ -42,11 +45,35 @@ constexpr int64_t kRmsMaxCols = 32768;
 int validate_add_rmsnorm(const void *x, int64_t x_stride, const void *res, int64_t res_stride,
                          const void *gamma, const void *h, int64_t h_stride, const void *y, int64_t y_stride,
                          const float *rstd, int64_t n_rows, int64_t n_cols, float eps, int dtype, bool *empty);
+// The same without y (glu_add_rmsnorm_q, whose result is quantised).
+int validate_add_rmsnorm_inputs(const void *x, int64_t x_stride, const void *res, int64_t res_stride,
+                                const void *gamma, const void *h, int64_t h_stride, const float *rstd,
+                                int64_t n_rows, int64_t n_cols, float eps, int dtype, bool *empty);
 constexpr int64_t kRmsBwdMaxCols = 16384;
 int validate_add_rmsnorm_bwd(const void *dy, int64_t dy_stride, const void *h, int64_t h_stride, const float *rstd,
                              const void *gamma, const void *dh, int64_t dh_stride, const void *dx, int64_t dx_stride,
                              const void *dres, int64_t dres_stride, const float *dgamma, int64_t n_rows,
                              int64_t n_cols, int dtype, bool *empty);
+
+// The bytes from a matrix's first to its last element (strides in elements of
+// E bytes); empty for zero rows.  False if they do not fit the address space.
+struct Span {
+    uint64_t lo, hi;
+};
+inline bool span(const void *p, int64_t rows, int64_t stride, int64_t cols, int E, Span *s)
+{
+    s->lo = s->hi = uint64_t(uintptr_t(p));
+    if (rows <= 0 || cols <= 0) return true;
+    int64_t n;
+    if (__builtin_mul_overflow(rows - 1, stride, &n) || __builtin_add_overflow(n, cols, &n) ||
+        __builtin_mul_overflow(n, int64_t(E), &n))
+        return false;
+    return !__builtin_add_overflow(s->lo, uint64_t(n), &s->hi);
+}
+inline bool overlap(const Span &a, const Span &b)
+{
+    return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi;
+}
 
 // One validated call: what the planner needs.  Strides are in elements.
 struct Call {

@@ -1,0 +1,513 @@
+// Quantisation to e4m3 with a scale for each block of 128 (glu_quant.cuh),
+// alone and fused with the residual add + RMSNorm before it:
+//
+//     glu_quantize        q, scale of x by rows (1 x 128) or blocks (128 x 128)
+//     glu_add_rmsnorm_q   s = x + residual, h = round(s),
+//                         y = s / sqrt(mean(s^2) + eps) * gamma,  q, scale of y by rows
+//
+// Both are bound by HBM: a value is read once and written once.  A thread owns
+// 16 bytes of a row (V = 8 values of a 16-bit type, 4 of f32), so a block of
+// 128 columns is 128 / V neighbouring lanes of one warp and its largest
+// magnitude a few shuffles; the values stay in registers between the load and
+// the store.  Rows that are not 16-byte multiples take the same code with V = 4
+// values at stride 32 (element accesses, coalesced), a block being one warp.
+// y is quantised from fp32: it is never rounded to the input's type.
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "glu.h"
+#include "glu_internal.h"
+#include "glu_kernels.cuh"
+#include "glu_quant.cuh"
+
+namespace glu {
+namespace quant {
+
+// How a thread's V values of one 128-column block lie in a row: contiguous
+// with 16-byte accesses (VEC), or at stride 32 with element accesses.
+template <class T, bool VEC>
+struct Lanes {
+    static constexpr int V = VEC ? 16 / int(sizeof(T)) : 4;
+    static constexpr int kPer = kBlock / V;         // lanes that share a block
+    using C = Codec<T>;
+    // first column of the piece number `piece` (counted over the row)
+    __device__ __forceinline__ static int col(int piece)
+    {
+        return VEC ? piece * V : (piece / 32) * kBlock + piece % 32;
+    }
+    static constexpr int kStep = VEC ? 1 : 32;      // distance of a thread's columns
+
+    struct Raw {
+        uint32_t w[VEC ? 4 : V];
+    };
+    __device__ __forceinline__ static Raw load(const char *row, int col, int H)
+    {
+        Raw r;
+        if constexpr (VEC) {
+            if (col < H)
+                Access<16>::load(row + int64_t(col) * sizeof(T), r.w);
+            else
+                r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0;      // zeros in every type
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                r.w[i] = col + 32 * i < H
+                             ? __float_as_uint(C::load1(row + int64_t(col + 32 * i) * sizeof(T)))
+                             : 0u;
+        }
+        return r;
+    }
+    __device__ __forceinline__ static float get(const Raw &r, int i)
+    {
+        if constexpr (VEC)
+            return C::get(r.w[i / C::kPerWord], i % C::kPerWord);
+        else
+            return __uint_as_float(r.w[i]);
+    }
+    __device__ __forceinline__ static void store(char *row, int col, int H, const float (&f)[V])
+    {
+        if constexpr (VEC) {
+            if (col < H) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = C::put(f + j * C::kPerWord);
+                Access<16>::store(row + int64_t(col) * sizeof(T), w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (col + 32 * i < H) C::store1(row + int64_t(col + 32 * i) * sizeof(T), f[i]);
+        }
+    }
+    // V e4m3 values of one row
+    __device__ __forceinline__ static void store_q(char *row, int col, int H, const float (&f)[V])
+    {
+        if constexpr (VEC) {
+            if (col < H) {
+                if constexpr (V == 8)
+                    asm volatile("st.global.L1::no_allocate.v2.b32 [%0], {%1, %2};" ::"l"(row + col),
+                                 "r"(pack4(f[0], f[1], f[2], f[3])), "r"(pack4(f[4], f[5], f[6], f[7]))
+                                 : "memory");
+                else
+                    asm volatile("st.global.L1::no_allocate.b32 [%0], %1;" ::"l"(row + col),
+                                 "r"(pack4(f[0], f[1], f[2], f[3]))
+                                 : "memory");
+            }
+        } else {
+            const uint32_t w = pack4(f[0], f[1], f[2], f[3]);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (col + 32 * i < H) row[col + 32 * i] = char((w >> (8 * i)) & 0xFFu);
+        }
+    }
+    __device__ __forceinline__ static float block_max(float v)
+    {
+#pragma unroll
+        for (int o = kPer / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+        return v;
+    }
+};
+
+__device__ __forceinline__ float sum32(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// ---------------------------------------------------------------- add + RMSNorm
+
+struct NormParams {
+    const char *x, *res, *gamma;
+    char *h, *q;
+    float *scale, *rstd;
+    int64_t sx, sr, sh, sq;     // row strides in bytes
+    int64_t ss;                 // scale's row stride in floats
+    int64_t rows;
+    int H;
+    int tpr;                    // threads per row, a multiple of 32; the block holds blockDim.x / tpr rows
+    float eps;
+};
+
+// One row per team of tpr threads, NV pieces per thread, its values kept in
+// fp32 registers between the sum of squares and the quantisation: x and the
+// residual are read once, h, q and the scales written once.  The sum of squares
+// is formed with fused multiply-adds in two chains per thread, then over the
+// warp by shuffles and over the row's warps through shared memory.
+template <class T, int NV, bool VEC>
+__global__ void __launch_bounds__(1024) add_rmsnorm_q_kernel(const NormParams p)
+{
+    using L = Lanes<T, VEC>;
+    constexpr int V = L::V;
+    __shared__ float red[32];
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const int team = threadIdx.x / p.tpr, t = threadIdx.x - team * p.tpr;
+    const int64_t row = int64_t(blockIdx.x) * (blockDim.x / p.tpr) + team;
+    const bool on = row < p.rows;               // whole teams, so whole warps
+    const int H = on ? p.H : 0;                 // a team without a row loads and stores nothing
+    const char *xr = p.x + row * p.sx, *rr = p.res + row * p.sr;
+    typename L::Raw a[NV], b[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = L::col(t + k * p.tpr);
+        a[k] = L::load(xr, c, H);
+        b[k] = L::load(rr, c, H);
+    }
+    float s[NV][V], ss[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s[k][i] = L::get(a[k], i) + L::get(b[k], i);
+            ss[i & 1] = fmaf(s[k][i], s[k][i], ss[i & 1]);
+        }
+        L::store(p.h + row * p.sh, L::col(t + k * p.tpr), H, s[k]);
+    }
+    float total = sum32(ss[0] + ss[1]);
+    if (p.tpr > 32) {
+        const int lane = threadIdx.x & 31, nw = p.tpr >> 5;
+        if (lane == 0) red[threadIdx.x >> 5] = total;
+        __syncthreads();
+        total = sum32(lane < nw ? red[team * nw + lane] : 0.0f);
+    }
+    const float rstd = 1.0f / sqrtf(total / float(p.H) + p.eps);
+    if (on && t == 0 && p.rstd) p.rstd[row] = rstd;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int piece = t + k * p.tpr, c = L::col(piece);
+        const typename L::Raw g = L::load(p.gamma, c, H);
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s[k][i] = s[k][i] * rstd * L::get(g, i);
+            m = fmaxf(m, fabsf(s[k][i]));
+        }
+        const Divider d(L::block_max(m));
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[k][i] = d(s[k][i]);
+        L::store_q(p.q + row * p.sq, c, H, s[k]);
+        if (piece % L::kPer == 0 && c < H) p.scale[row * p.ss + piece / L::kPer] = d.scale();
+    }
+}
+
+// ---------------------------------------------------------------- quantisation
+
+struct QuantParams {
+    const char *x;
+    char *q;
+    float *scale;
+    int64_t sx, sq;             // row strides in bytes
+    int64_t ss;                 // scale's row stride in floats
+    int64_t rows;
+    int H;
+    int tpr;                    // rows form: threads per row (the block holds blockDim.x / tpr rows)
+};
+
+// By rows: a team of tpr threads (a multiple of 32) takes NV pieces each of one
+// row; blockIdx.y counts stretches of NV * tpr pieces along wide rows.
+template <class T, int NV, bool VEC>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
+{
+    using L = Lanes<T, VEC>;
+    constexpr int V = L::V;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int team = threadIdx.x / p.tpr, t = threadIdx.x - team * p.tpr;
+    const int64_t row = int64_t(blockIdx.x) * (blockDim.x / p.tpr) + team;
+    if (row >= p.rows) return;                  // whole teams, so whole warps
+    const int first = blockIdx.y * p.tpr * NV + t;
+    const char *xr = p.x + row * p.sx;
+    typename L::Raw a[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) a[k] = L::load(xr, L::col(first + k * p.tpr), p.H);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int piece = first + k * p.tpr, c = L::col(piece);
+        float f[V], m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            f[i] = L::get(a[k], i);
+            m = fmaxf(m, fabsf(f[i]));
+        }
+        const Divider d(L::block_max(m));
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = d(f[i]);
+        L::store_q(p.q + row * p.sq, c, p.H, f);
+        if (piece % L::kPer == 0 && c < p.H) p.scale[row * p.ss + piece / L::kPer] = d.scale();
+    }
+}
+
+// By blocks: 256 threads hold one 128 x 128 block in registers.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) quantize_blocks_kernel(const QuantParams p)
+{
+    using L = Lanes<T, VEC>;
+    constexpr int V = L::V;
+    constexpr int kRows = 256 / L::kPer;        // rows of the block loaded at once
+    constexpr int NV = kBlock / kRows;
+    __shared__ float red[8];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = int(blockIdx.x) * kBlock + L::col(int(threadIdx.x) % L::kPer);
+    const int64_t r0 = int64_t(blockIdx.y) * kBlock + threadIdx.x / L::kPer;
+    typename L::Raw a[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t row = r0 + k * kRows;
+        a[k] = L::load(p.x + row * p.sx, c, row < p.rows ? p.H : 0);
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(L::get(a[k], i)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
+    const Divider d(m);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t row = r0 + k * kRows;
+        float f[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = d(L::get(a[k], i));
+        L::store_q(p.q + row * p.sq, c, row < p.rows ? p.H : 0, f);
+    }
+    if (threadIdx.x == 0) p.scale[int64_t(blockIdx.y) * p.ss + blockIdx.x] = d.scale();
+}
+
+// ---------------------------------------------------------------- host side
+
+namespace {
+
+using NormFn = void (*)(NormParams);
+using QuantFn = void (*)(QuantParams);
+
+template <class T>
+NormFn norm_kernel(int nv, bool vec)
+{
+    if (vec) {
+        switch (nv) {
+        case 1: return add_rmsnorm_q_kernel<T, 1, true>;
+        case 2: return add_rmsnorm_q_kernel<T, 2, true>;
+        case 4: return add_rmsnorm_q_kernel<T, 4, true>;
+        default: return sizeof(T) == 4 ? add_rmsnorm_q_kernel<T, sizeof(T) == 4 ? 8 : 4, true> : nullptr;
+        }
+    }
+    switch (nv) {
+    case 1: return add_rmsnorm_q_kernel<T, 1, false>;
+    case 2: return add_rmsnorm_q_kernel<T, 2, false>;
+    case 4: return add_rmsnorm_q_kernel<T, 4, false>;
+    default: return add_rmsnorm_q_kernel<T, 8, false>;
+    }
+}
+
+template <class T>
+QuantFn quant_kernel(bool blocks, int nv, bool vec)
+{
+    if (blocks) return vec ? quantize_blocks_kernel<T, true> : quantize_blocks_kernel<T, false>;
+    if (nv == 1) return vec ? quantize_rows_kernel<T, 1, true> : quantize_rows_kernel<T, 1, false>;
+    return vec ? quantize_rows_kernel<T, 4, true> : quantize_rows_kernel<T, 4, false>;
+}
+
+bool a16(const void *p) { return uintptr_t(p) % 16 == 0; }
+
+// Launches with the programmatic dependency of every kernel here (the kernel
+// waits for the previous grid itself), or without where that is refused.
+template <class P>
+int launch(void (*fn)(P), dim3 grid, int threads, const P &p, glu_stream_t stream)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    P copy = p;
+    void *args[] = {&copy};
+    cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(fn), args);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        cfg.attrs = nullptr;
+        cfg.numAttrs = 0;
+        e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(fn), args);
+    }
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return glu::cuda_fail(e);
+    }
+    return GLU_OK;
+}
+
+}  // namespace
+}  // namespace quant
+}  // namespace glu
+
+extern "C" int glu_add_rmsnorm_q(const void *x, int64_t x_stride, const void *residual, int64_t res_stride,
+                                 const void *gamma, void *h, int64_t h_stride, void *q, int64_t q_stride,
+                                 float *scale, int64_t scale_stride, float *rstd, int64_t n_rows, int64_t n_cols,
+                                 float eps, glu_dtype_t dtype, glu_stream_t stream)
+{
+    using namespace glu::quant;
+    bool empty = false;
+    // x, residual, gamma, h and rstd under the rules of glu_add_rmsnorm_fwd (h
+    // standing in for its y, which has no counterpart here)
+    if (int st = glu::validate_add_rmsnorm_inputs(x, x_stride, residual, res_stride, gamma, h, h_stride, rstd, n_rows,
+                                                  n_cols, eps, dtype, &empty))
+        return st;
+    if (empty) {
+        glu::record_launch(glu_launch_info_t{});
+        return GLU_OK;
+    }
+    const int E = dtype == GLU_F32 ? 4 : 2;
+    const int64_t groups = (n_cols + kBlock - 1) / kBlock;
+    if (!q || !scale) return GLU_ERR_NULL;
+    if (n_rows == 1) {
+        x_stride = res_stride = h_stride = q_stride = n_cols;
+        scale_stride = groups;
+    }
+    if (q_stride < n_cols || scale_stride < groups) return GLU_ERR_STRIDE;
+    glu::Span all[7] = {};
+    const bool fits = glu::span(x, n_rows, x_stride, n_cols, E, &all[0]) &&
+                      glu::span(residual, n_rows, res_stride, n_cols, E, &all[1]) &&
+                      glu::span(gamma, 1, n_cols, n_cols, E, &all[2]) &&
+                      glu::span(h, n_rows, h_stride, n_cols, E, &all[3]) &&
+                      glu::span(rstd, rstd ? n_rows : 0, 1, 1, 4, &all[4]) &&
+                      glu::span(q, n_rows, q_stride, n_cols, 1, &all[5]) &&
+                      glu::span(scale, n_rows, scale_stride, groups, 4, &all[6]);
+    if (!fits) return GLU_ERR_SHAPE;
+    for (int o = 5; o < 7; ++o)
+        for (int i = 0; i < o; ++i)
+            if (glu::overlap(all[i], all[o])) return GLU_ERR_ALIAS;
+    if (uintptr_t(scale) % 4 || (rstd && uintptr_t(rstd) % 4)) return GLU_ERR_STRIDE;
+
+    const int V = 16 / E;
+    const bool vec = a16(x) && a16(residual) && a16(gamma) && a16(h) && (n_cols * E) % 16 == 0 &&
+                     (x_stride * E) % 16 == 0 && (res_stride * E) % 16 == 0 && (h_stride * E) % 16 == 0 &&
+                     uintptr_t(q) % V == 0 && q_stride % V == 0;
+    // pieces (16 bytes, or 4 elements) a row has, and pieces per thread: two up
+    // to 1024 threads, more only beyond
+    const int64_t pieces = vec ? n_cols / V : groups * 32;
+    int nv = pieces <= 128 ? 1 : 2;
+    while (pieces > int64_t(1024) * nv) nv *= 2;
+    int tpr = int((pieces + nv - 1) / nv);
+    tpr = (tpr + 31) / 32 * 32;
+    const int teams = tpr >= 128 ? 1 : 128 / tpr;
+    NormParams p{};
+    p.x = static_cast<const char *>(x);
+    p.res = static_cast<const char *>(residual);
+    p.gamma = static_cast<const char *>(gamma);
+    p.h = static_cast<char *>(h);
+    p.q = static_cast<char *>(q);
+    p.scale = scale;
+    p.rstd = rstd;
+    p.sx = x_stride * E;
+    p.sr = res_stride * E;
+    p.sh = h_stride * E;
+    p.sq = q_stride;
+    p.ss = scale_stride;
+    p.rows = n_rows;
+    p.H = int(n_cols);
+    p.tpr = tpr;
+    p.eps = eps;
+    const int64_t blocks = (n_rows + teams - 1) / teams;
+    if (blocks > INT32_MAX) return GLU_ERR_SHAPE;
+    const NormFn fn = dtype == GLU_F32   ? norm_kernel<float>(nv, vec)
+                      : dtype == GLU_F16 ? norm_kernel<__half>(nv, vec)
+                                         : norm_kernel<__nv_bfloat16>(nv, vec);
+    if (int st = launch(fn, dim3(unsigned(blocks)), tpr * teams, p, stream)) return st;
+    glu_launch_info_t info{};
+    info.launched = 1;
+    info.vec_bytes = vec ? 16 : E;
+    info.unroll = nv * (vec ? V : 4);
+    info.threads = tpr * teams;
+    info.grid = int32_t(blocks);
+    info.path = 9;
+    info.vector_units = n_rows;
+    glu::record_launch(info);
+    return GLU_OK;
+}
+
+extern "C" int glu_quantize(const void *x, int64_t x_stride, void *q, int64_t q_stride, float *scale,
+                            int64_t scale_stride, int64_t n_rows, int64_t n_cols, int block_rows, glu_dtype_t dtype,
+                            glu_stream_t stream)
+{
+    using namespace glu::quant;
+    if (!(dtype == GLU_F32 || dtype == GLU_F16 || dtype == GLU_BF16)) return GLU_ERR_ENUM;
+    if (block_rows != 1 && block_rows != kBlock) return GLU_ERR_VALUE;
+    if (n_rows < 0 || n_cols < 0 || n_cols > INT32_MAX - 4096) return GLU_ERR_SHAPE;
+    if (n_rows == 0 || n_cols == 0) {
+        glu::record_launch(glu_launch_info_t{});
+        return GLU_OK;
+    }
+    if (!x || !q || !scale) return GLU_ERR_NULL;
+    const int E = dtype == GLU_F32 ? 4 : 2, V = 16 / E;
+    const bool by_block = block_rows == kBlock;
+    const int64_t groups = (n_cols + kBlock - 1) / kBlock;
+    const int64_t srows = by_block ? (n_rows - 1) / kBlock + 1 : n_rows;
+    if (n_rows == 1) x_stride = q_stride = n_cols;
+    if (srows == 1) scale_stride = groups;
+    if (x_stride < n_cols || q_stride < n_cols || scale_stride < groups) return GLU_ERR_STRIDE;
+    glu::Span sx{}, sq{}, ss{};
+    if (!glu::span(x, n_rows, x_stride, n_cols, E, &sx) || !glu::span(q, n_rows, q_stride, n_cols, 1, &sq) ||
+        !glu::span(scale, srows, scale_stride, groups, 4, &ss))
+        return GLU_ERR_SHAPE;
+    if (glu::overlap(sx, sq) || glu::overlap(sx, ss) || glu::overlap(sq, ss)) return GLU_ERR_ALIAS;
+    if (uintptr_t(scale) % 4) return GLU_ERR_STRIDE;
+    const bool vec = a16(x) && (n_cols * E) % 16 == 0 && (x_stride * E) % 16 == 0 && uintptr_t(q) % V == 0 &&
+                     q_stride % V == 0;
+    QuantParams p{};
+    p.x = static_cast<const char *>(x);
+    p.q = static_cast<char *>(q);
+    p.scale = scale;
+    p.sx = x_stride * E;
+    p.sq = q_stride;
+    p.ss = scale_stride;
+    p.rows = n_rows;
+    p.H = int(n_cols);
+    dim3 grid;
+    int nv = 1;
+    if (by_block) {
+        if (srows > 65535 || groups > INT32_MAX) return GLU_ERR_SHAPE;
+        grid = dim3(unsigned(groups), unsigned(srows));
+    } else {
+        // four pieces per thread in rows that fill a block with them, else one
+        const int64_t pieces = vec ? n_cols / V : groups * 32;
+        nv = pieces >= 1024 ? 4 : 1;
+        int64_t tpr = (pieces + nv - 1) / nv;
+        tpr = tpr > 256 ? 256 : (tpr + 31) / 32 * 32;
+        p.tpr = int(tpr);
+        const int64_t teams = 256 / tpr;
+        const int64_t blocks = (n_rows + teams - 1) / teams;
+        const int64_t spans = (pieces + tpr * nv - 1) / (tpr * nv);
+        if (blocks > INT32_MAX || spans > 65535) return GLU_ERR_SHAPE;
+        grid = dim3(unsigned(blocks), unsigned(spans));
+    }
+    const int threads = by_block ? 256 : 256 / p.tpr * p.tpr;
+    const QuantFn fn = dtype == GLU_F32   ? quant_kernel<float>(by_block, nv, vec)
+                       : dtype == GLU_F16 ? quant_kernel<__half>(by_block, nv, vec)
+                                          : quant_kernel<__nv_bfloat16>(by_block, nv, vec);
+    if (int st = launch(fn, grid, threads, p, stream)) return st;
+    glu_launch_info_t info{};
+    info.launched = 1;
+    info.vec_bytes = vec ? 16 : E;
+    info.unroll = by_block ? 64 : nv * (vec ? V : 4);
+    info.threads = threads;
+    info.grid = int32_t(grid.x * grid.y > INT32_MAX ? INT32_MAX : grid.x * grid.y);
+    info.path = 10;
+    info.vector_units = srows * groups;
+    glu::record_launch(info);
+    return GLU_OK;
+}

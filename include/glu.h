@@ -524,6 +524,135 @@ int glu_add_rmsnorm_bwd(const void *dy, int64_t dy_stride,
                         int64_t n_rows, int64_t n_cols,
                         glu_dtype_t dtype, glu_stream_t stream);
 
+/*
+ * ---- The gated MLP in 8-bit floating point (inference) ----
+ *
+ * A matrix V is held as e4m3 bytes q (1 sign, 4 exponent, 3 mantissa bits, no
+ * infinities, largest value 448) and float scales, V[r, c] ~ q[r, c] * scale of
+ * its block: activations share a scale by 1 x 128 blocks along a row (scale is
+ * n_rows x ceil(n_cols / 128)), weights by 128 x 128 blocks (scale is
+ * ceil(n_rows / 128) x ceil(n_cols / 128)); the last blocks of a row or column
+ * may be smaller.  Quantising a block:
+ *
+ *     scale = max(amax, 2^-100) / 448        amax = its largest magnitude
+ *     q     = e4m3(v / scale)                round to nearest, ties to even
+ *
+ * A NaN is held as NaN and takes no part in amax; a block with an infinity
+ * holds NaN.  Scales are float matrices with their own row stride, in floats,
+ * 4-byte aligned (GLU_ERR_STRIDE).  Strides of e4m3 matrices are in bytes.  In
+ * this section an output's footprint, from its first to its last element, must
+ * not overlap another operand's (GLU_ERR_ALIAS), except where a call says so.
+ */
+
+/*
+ * Quantises x: q and scale by rows (block_rows = 1) or by 128 x 128 blocks
+ * (block_rows = 128), else GLU_ERR_VALUE.
+ *   x, x_stride            n_rows x n_cols of `dtype` (any glu_dtype_t).
+ *   q, q_stride            n_rows x n_cols e4m3 bytes, q_stride >= n_cols.
+ *   scale, scale_stride    as above; scale_stride >= ceil(n_cols / 128).
+ * One kernel on `stream`; glu_last_launch reports path = 10.  n_rows == 0 or
+ * n_cols == 0: no work.
+ */
+int glu_quantize(const void *x, int64_t x_stride,
+                 void *q, int64_t q_stride, float *scale, int64_t scale_stride,
+                 int64_t n_rows, int64_t n_cols, int block_rows,
+                 glu_dtype_t dtype, glu_stream_t stream);
+
+/*
+ * glu_add_rmsnorm_fwd with its result quantised by rows, in one pass:
+ *
+ *     s = x + residual,  h = round(s),  rstd = 1 / sqrt(mean(s^2) + eps)
+ *     q, scale = quantised (s * rstd * gamma)      (from fp32, not rounded to dtype first)
+ *
+ * x, residual, gamma, h, rstd, eps, n_cols <= 32768 and dtype as there: h may
+ * be exactly x or exactly residual, rstd may be NULL.  q and scale as in
+ * glu_quantize; they overlap nothing.  glu_last_launch reports path = 9.
+ */
+int glu_add_rmsnorm_q(const void *x, int64_t x_stride,
+                      const void *residual, int64_t res_stride,
+                      const void *gamma,
+                      void *h, int64_t h_stride,
+                      void *q, int64_t q_stride, float *scale, int64_t scale_stride,
+                      float *rstd,
+                      int64_t n_rows, int64_t n_cols, float eps,
+                      glu_dtype_t dtype, glu_stream_t stream);
+
+/*
+ * The plain product of quantised matrices on the tensor cores:
+ *
+ *     d[m, n] = round(sum over K blocks b of
+ *                     a_scale[m, b] * b_scale[n / 128, b] * sum_{k in b} a[m, k] * b[n, k])
+ *
+ * the inner sums of 128 products in the tensor core's fp32, the outer ones in
+ * fp32 with one rounding per block, one rounding to `dtype` at the end.
+ *   a, a_stride              M x K e4m3, a_scale M x ceil(K / 128).
+ *   b, b_stride              N x K e4m3 (row n holds output feature n), b_scale
+ *                            ceil(N / 128) x ceil(K / 128).
+ *   d, d_stride              M x N of `dtype`, GLU_F16 or GLU_BF16.
+ * a and b: 16-byte aligned bases and row strides that are multiples of 16
+ * (GLU_ERR_STRIDE; K itself may be any size, the bytes past it are not read
+ * into the sums); a, b and d in device memory (GLU_ERR_VALUE).  M, K, N <
+ * 2^31 - 65536.  M == 0 or N == 0: no work; K == 0: d = 0.  The result does not
+ * depend on what else runs: sums are formed in a fixed order.
+ * glu_last_launch reports path = 12 and unroll = blocks that share a tile.
+ */
+int glu_gemm_q_nt(const void *a, int64_t a_stride, const float *a_scale, int64_t a_scale_stride,
+                  const void *b, int64_t b_stride, const float *b_scale, int64_t b_scale_stride,
+                  void *d, int64_t d_stride,
+                  int64_t M, int64_t K, int64_t N,
+                  glu_dtype_t dtype, glu_stream_t stream);
+
+/*
+ * glu_gemm_fwd on quantised matrices with its result quantised by rows:
+ *
+ *     y, y_scale = quantised (act(x . w_gate) * (x . w_up))
+ *
+ * with both products as in glu_gemm_q_nt, kept in fp32 through the activation
+ * and the quantisation.
+ *   x, x_stride, x_scale         M x K.
+ *   w_gate, w_up, w_stride       I x K each, one row stride; gate_scale and
+ *                                up_scale with one row stride.
+ *   y, y_stride                  M x I e4m3, y_scale M x ceil(I / 128).
+ * Other rules as glu_gemm_q_nt; K == 0 gives zeros.  path = 11.
+ */
+int glu_gemm_q_fwd(const void *x, int64_t x_stride, const float *x_scale, int64_t x_scale_stride,
+                   const void *w_gate, const void *w_up, int64_t w_stride,
+                   const float *gate_scale, const float *up_scale, int64_t w_scale_stride,
+                   void *y, int64_t y_stride, float *y_scale, int64_t y_scale_stride,
+                   int64_t M, int64_t K, int64_t I,
+                   glu_act_t act, glu_stream_t stream);
+
+/*
+ * The two products by expert.  The M rows are sorted by expert: expert e's are
+ * rows offsets[e] .. offsets[e + 1] - 1, multiplied by its own weights, at
+ * e * group elements from expert 0's (bytes for e4m3, a multiple of 16; floats
+ * for scales).
+ *   offsets      n_groups + 1 int32 in device memory, not decreasing, from
+ *                >= 0 to <= M; read by the kernel, never by the host.  An
+ *                expert may have no rows.  Rows before offsets[0] and from
+ *                offsets[n_groups] on are left as they were.  (Offsets out of
+ *                order give wrong results, but no access outside the operands.)
+ *   n_groups     0 .. 1024, else GLU_ERR_SHAPE; 0: no work.
+ * Rows of a that no expert has may hold anything.  M / n_groups, not the
+ * offsets, picks the kernel.
+ */
+int glu_gemm_q_grouped_nt(const void *a, int64_t a_stride, const float *a_scale, int64_t a_scale_stride,
+                          const void *b, int64_t b_stride, int64_t b_group,
+                          const float *b_scale, int64_t b_scale_stride, int64_t b_scale_group,
+                          void *d, int64_t d_stride,
+                          int64_t M, int64_t K, int64_t N,
+                          const int32_t *offsets, int64_t n_groups,
+                          glu_dtype_t dtype, glu_stream_t stream);
+
+int glu_gemm_q_grouped_fwd(const void *x, int64_t x_stride, const float *x_scale, int64_t x_scale_stride,
+                           const void *w_gate, const void *w_up, int64_t w_stride, int64_t w_group,
+                           const float *gate_scale, const float *up_scale, int64_t w_scale_stride,
+                           int64_t w_scale_group,
+                           void *y, int64_t y_stride, float *y_scale, int64_t y_scale_stride,
+                           int64_t M, int64_t K, int64_t I,
+                           const int32_t *offsets, int64_t n_groups,
+                           glu_act_t act, glu_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
