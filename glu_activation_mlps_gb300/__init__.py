@@ -74,6 +74,8 @@ def build(force: bool = False) -> str:
 def lib() -> ctypes.CDLL:
     """The loaded CUDA library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -568,63 +570,93 @@ def add_rmsnorm_bwd(dy, h, rstd, gamma, *, dh=None, dx=None, dres=None, dgamma=N
 
 # ---- 8-bit floating point ----------------------------------------------------------
 
-def _same_device(x, *others):
-    """Every tensor on x's device, which is the current one (the device the
-    library launches on)."""
+def _same_device(x, *others) -> int:
+    """The index of x's device, which holds every other tensor and is the
+    current one (the device the library launches on)."""
     import torch
-    dev = x.device
-    if not x.is_cuda or dev.index != torch.cuda.current_device():
+    dev = x.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError("the tensors must be on the current CUDA device")
     for t in others:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("all tensors must be on one device")
+    return dev
 
 
-def _groups(n: int) -> int:
-    return (n + 127) // 128
+def _raw_stream(stream, dev: int) -> int:
+    """The stream's handle; the device's current stream for None."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _empty_q(shape, device):
+def _mat(t, name):
+    """_rows of a CUDA tensor, quick for plain matrices."""
+    if t.dim() == 2:
+        stride, inner = t.stride()
+        if inner == 1 or t.shape[1] <= 1:
+            return t.shape[0], stride
+    return _rows(t, name)
+
+
+def _empty_q(shape, like):
     """An e4m3 tensor whose rows start on 16-byte boundaries (the products'
     rule): the last dimension of a wider tensor where it is no multiple of 16."""
     import torch
     n = shape[-1]
     if n % 16 == 0:
-        return torch.empty(shape, dtype=torch.float8_e4m3fn, device=device)
-    return torch.empty((*shape[:-1], n + -n % 16), dtype=torch.float8_e4m3fn, device=device)[..., :n]
+        return like.new_empty(shape, dtype=torch.float8_e4m3fn)
+    return like.new_empty((*shape[:-1], n + -n % 16), dtype=torch.float8_e4m3fn)[..., :n]
 
 
-def _check_q(q, scale, name):
+def _out_q(q, scale, shape, scale_shape, like, name):
+    """q and its scales, allocated where they are None, else checked."""
+    import torch
+    if q is None:
+        q = _empty_q(shape, like)
+    elif q.dtype != torch.float8_e4m3fn or q.shape != shape:
+        raise ValueError(f"{name} must be float8_e4m3fn of shape {tuple(shape)}")
+    if scale is None:
+        scale = like.new_empty(scale_shape, dtype=torch.float32)
+    elif scale.dtype != torch.float32 or scale.shape != scale_shape:
+        raise ValueError(f"{name}'s scales must be float32 of shape {tuple(scale_shape)}")
+    return q, scale
+
+
+def _in_q(q, scale, name):
+    """(n_rows, row stride, scale's row stride, K) of a matrix quantised by rows."""
     import torch
     if q.dtype != torch.float8_e4m3fn or scale.dtype != torch.float32:
         raise TypeError(f"{name} must be float8_e4m3fn with float32 scales")
+    shape = q.shape
+    K = shape[-1]
+    if scale.shape != (*shape[:-1], (K + 127) // 128):
+        raise ValueError(f"{name}'s scales must have shape {(*shape[:-1], (K + 127) // 128)}")
+    n_rows, stride = _mat(q, name)
+    return n_rows, stride, _mat(scale, name)[1], K
 
 
-def _scale_rows(scale, shape, name):
-    """Row stride of a scale matrix of the given shape."""
-    if tuple(scale.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(scale.shape)}")
-    return _rows(scale, name)[1]
-
-
-def _weight(w, s, K, name, grouped):
+def _weight_q(w, s, K, name, grouped):
     """(N, row stride, expert stride, scale's row stride, scale's expert stride) of (N, K) or (E, N, K) weights."""
-    _check_q(w, s, name)
-    if w.dim() != (3 if grouped else 2) or w.shape[-1] != K:
+    import torch
+    if w.dtype != torch.float8_e4m3fn or s.dtype != torch.float32:
+        raise TypeError(f"{name} must be float8_e4m3fn with float32 scales")
+    shape = w.shape
+    if len(shape) != (3 if grouped else 2) or shape[-1] != K:
         raise ValueError(f"{name} must be {'(E, N, K)' if grouped else '(N, K)'} with K = {K}")
-    N = w.shape[-2]
-    want = (*w.shape[:-2], _groups(N), _groups(K))
-    if tuple(s.shape) != want:
-        raise ValueError(f"{name}'s scales must have shape {want}, not {tuple(s.shape)}")
-    if (w.stride(-1) != 1 and K > 1) or (s.stride(-1) != 1 and s.shape[-1] > 1):
+    N = shape[-2]
+    if s.shape != (*shape[:-2], (N + 127) // 128, (K + 127) // 128):
+        raise ValueError(f"{name}'s scales must have shape {(*shape[:-2], (N + 127) // 128, (K + 127) // 128)}")
+    ws, ss = w.stride(), s.stride()
+    if (ws[-1] != 1 and K > 1) or (ss[-1] != 1 and K > 128):
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return (N, w.stride(-2), w.stride(0) if grouped else 0, s.stride(-2), s.stride(0) if grouped else 0)
+    return (N, ws[0], 0, ss[0], 0) if not grouped else (N, ws[1], ws[0], ss[1], ss[0])
 
 
 def _offsets(offsets, w):
     import torch
     if offsets.dtype != torch.int32 or not offsets.is_contiguous() or offsets.shape != (w.shape[0] + 1,):
         raise ValueError("offsets must be a contiguous int32 tensor of one entry more than there are experts")
+    return offsets.data_ptr()
 
 
 def quantize(x, *, block_rows: int = 1, q=None, scale=None, stream=None):
@@ -633,30 +665,26 @@ def quantize(x, *, block_rows: int = 1, q=None, scale=None, stream=None):
     scale (..., ceil(K / 128))), or of 128 rows (128, weights; x is (N, K), or
     (E, N, K) for the weights of E experts, and scale (.., ceil(N / 128),
     ceil(K / 128)))."""
-    import torch
-    if block_rows not in (1, 128):
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
     code = _dtype_code(x)
+    shape = x.shape
     if block_rows == 128:
-        if x.dim() not in (2, 3):
+        if len(shape) not in (2, 3):
             raise ValueError("x must be (N, K) or (E, N, K) for 128 x 128 blocks")
-        shape = (*x.shape[:-2], _groups(x.shape[-2]), _groups(x.shape[-1]))
+        blocks = (*shape[:-2], (shape[-2] + 127) // 128, (shape[-1] + 127) // 128)
     else:
-        shape = (*x.shape[:-1], _groups(x.shape[-1]))
-    _same_device(x, q, scale)
-    q = _empty_q(x.shape, x.device) if q is None else q
-    scale = torch.empty(shape, dtype=torch.float32, device=x.device) if scale is None else scale
-    _check_q(q, scale, "q")
-    if q.shape != x.shape or tuple(scale.shape) != tuple(shape):
-        raise ValueError("q and scale must have the shapes of x and of its blocks")
-    st = 0
-    parts = [(x, q, scale)] if x.dim() < 3 or block_rows == 1 else list(zip(x, q, scale))
+        blocks = (*shape[:-1], (shape[-1] + 127) // 128)
+    dev = _same_device(x, q, scale)
+    q, scale = _out_q(q, scale, shape, blocks, x, "q")
+    s = _raw_stream(stream, dev)
+    parts = ((x, q, scale),) if len(shape) < 3 or block_rows == 1 else zip(x, q, scale)
     for xe, qe, se in parts:
-        n_rows, x_stride = _rows(xe, "x")
-        st = st or glu_quantize(xe.data_ptr(), x_stride, qe.data_ptr(), _rows(qe, "q")[1], se.data_ptr(),
-                                _rows(se, "scale")[1], n_rows, xe.shape[-1], block_rows, code, _stream(stream))
-    if st:
-        raise GluError(st, "glu_quantize")
+        n_rows, x_stride = _mat(xe, "x")
+        st = glu_quantize(xe.data_ptr(), x_stride, qe.data_ptr(), _mat(qe, "q")[1], se.data_ptr(),
+                          _mat(se, "scale")[1], n_rows, shape[-1], block_rows, code, s)
+        if st:
+            raise GluError(st, "glu_quantize")
     return q, scale
 
 
@@ -666,34 +694,30 @@ def add_rmsnorm_q(x, residual, gamma, eps: float = 1e-5, *, h=None, q=None, scal
     pass.  ``h`` may be x or residual; ``rstd`` as in add_rmsnorm.  Returns
     (h, q, scale) or (h, q, scale, rstd)."""
     import torch
-    _same_device(x, residual, gamma, h, q, scale)
-    n_rows, x_stride = _rows(x, "x")
-    _, r_stride = _rows(residual, "residual")
-    if residual.shape != x.shape or residual.dtype != x.dtype:
+    dev = _same_device(x, residual, gamma, h, q, scale)
+    code = _dtype_code(x)
+    shape, dtype = x.shape, x.dtype
+    H = shape[-1]
+    if residual.shape != shape or residual.dtype != dtype:
         raise ValueError("residual must match x in shape and dtype")
-    H = x.shape[-1]
-    if gamma.shape != (H,) or gamma.dtype != x.dtype or not gamma.is_contiguous():
+    if gamma.shape != (H,) or gamma.dtype != dtype or not gamma.is_contiguous():
         raise ValueError("gamma must be a contiguous (H,) tensor of x's dtype")
-    h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if h is None else h
-    if h.shape != x.shape or h.dtype != x.dtype:
+    n_rows, x_stride = _mat(x, "x")
+    r_stride = _mat(residual, "residual")[1]
+    if h is None:
+        h = x.new_empty(shape)
+    elif h.shape != shape or h.dtype != dtype:
         raise ValueError("h must match x in shape and dtype")
-    shape = (*x.shape[:-1], _groups(H))
-    q = _empty_q(x.shape, x.device) if q is None else q
-    scale = torch.empty(shape, dtype=torch.float32, device=x.device) if scale is None else scale
-    _check_q(q, scale, "q")
-    if q.shape != x.shape:
-        raise ValueError("q must match x in shape")
-    s_stride = _scale_rows(scale, shape, "scale")
+    q, scale = _out_q(q, scale, shape, (*shape[:-1], (H + 127) // 128), x, "q")
     want_rstd = rstd is not None and rstd is not False
     if rstd is True:
-        rstd = torch.empty(n_rows, dtype=torch.float32, device=x.device)
+        rstd = x.new_empty(n_rows, dtype=torch.float32)
     if want_rstd and (rstd.dtype != torch.float32 or rstd.numel() != n_rows or not rstd.is_contiguous() or
-                      rstd.device != x.device):
+                      rstd.get_device() != dev):
         raise ValueError("rstd must be a contiguous float32 tensor with one entry per row")
     st = glu_add_rmsnorm_q(x.data_ptr(), x_stride, residual.data_ptr(), r_stride, gamma.data_ptr(), h.data_ptr(),
-                           _rows(h, "h")[1], q.data_ptr(), _rows(q, "q")[1], scale.data_ptr(), s_stride,
-                           rstd.data_ptr() if want_rstd else None, n_rows, H, float(eps), _dtype_code(x),
-                           _stream(stream))
+                           _mat(h, "h")[1], q.data_ptr(), _mat(q, "q")[1], scale.data_ptr(), _mat(scale, "scale")[1],
+                           rstd.data_ptr() if want_rstd else None, n_rows, H, eps, code, _raw_stream(stream, dev))
     if st:
         raise GluError(st, "glu_add_rmsnorm_q")
     return (h, q, scale, rstd) if want_rstd else (h, q, scale)
@@ -707,29 +731,26 @@ def gemm_q_nt(a, a_scale, b, b_scale, *, d=None, dtype=None, offsets=None, strea
     .. offsets[e + 1] are multiplied by b[e]; rows of d that no expert has are
     left as they were."""
     import torch
-    _same_device(a, a_scale, b, b_scale, d, offsets)
-    _check_q(a, a_scale, "a")
-    n_rows, a_stride = _rows(a, "a")
-    K = a.shape[-1]
-    as_stride = _scale_rows(a_scale, (*a.shape[:-1], _groups(K)), "a_scale")
-    grouped = offsets is not None
-    N, b_stride, b_group, bs_stride, bs_group = _weight(b, b_scale, K, "b", grouped)
+    dev = _same_device(a, a_scale, b, b_scale, d, offsets)
+    n_rows, a_stride, as_stride, K = _in_q(a, a_scale, "a")
+    N, b_stride, b_group, bs_stride, bs_group = _weight_q(b, b_scale, K, "b", offsets is not None)
+    shape = (*a.shape[:-1], N)
     if d is None:
-        d = torch.empty((*a.shape[:-1], N), dtype=dtype or torch.bfloat16, device=a.device)
-    if tuple(d.shape) != (*a.shape[:-1], N) or (dtype is not None and d.dtype != dtype):
+        d = a.new_empty(shape, dtype=dtype or torch.bfloat16)
+    elif d.shape != shape or (dtype is not None and d.dtype != dtype):
         raise ValueError("d has the wrong shape or dtype")
-    _, d_stride = _rows(d, "d")
+    d_stride = _mat(d, "d")[1]
     code = _dtype_code(d)
-    if grouped:
-        _offsets(offsets, b)
+    s = _raw_stream(stream, dev)
+    if offsets is None:
+        st = glu_gemm_q_nt(a.data_ptr(), a_stride, a_scale.data_ptr(), as_stride, b.data_ptr(), b_stride,
+                           b_scale.data_ptr(), bs_stride, d.data_ptr(), d_stride, n_rows, K, N, code, s)
+    else:
         st = glu_gemm_q_grouped_nt(a.data_ptr(), a_stride, a_scale.data_ptr(), as_stride, b.data_ptr(), b_stride,
                                    b_group, b_scale.data_ptr(), bs_stride, bs_group, d.data_ptr(), d_stride, n_rows,
-                                   K, N, offsets.data_ptr(), b.shape[0], code, _stream(stream))
-    else:
-        st = glu_gemm_q_nt(a.data_ptr(), a_stride, a_scale.data_ptr(), as_stride, b.data_ptr(), b_stride,
-                           b_scale.data_ptr(), bs_stride, d.data_ptr(), d_stride, n_rows, K, N, code, _stream(stream))
+                                   K, N, _offsets(offsets, b), b.shape[0], code, s)
     if st:
-        raise GluError(st, "glu_gemm_q_grouped_nt" if grouped else "glu_gemm_q_nt")
+        raise GluError(st, "glu_gemm_q_nt" if offsets is None else "glu_gemm_q_grouped_nt")
     return d
 
 
@@ -739,37 +760,27 @@ def gemm_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, y=None, y_scal
     the tensor cores, quantised by rows in the epilogue.  x is (..., K), the
     weights (I, K) with one row stride, or (E, I, K) with ``offsets`` (see
     gemm_q_nt)."""
-    import torch
-    _same_device(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, y_scale, offsets)
-    _check_q(x, x_scale, "x")
-    n_rows, x_stride = _rows(x, "x")
-    K = x.shape[-1]
-    xs_stride = _scale_rows(x_scale, (*x.shape[:-1], _groups(K)), "x_scale")
-    grouped = offsets is not None
-    N, *gate = _weight(w_gate, gate_scale, K, "w_gate", grouped)
-    if w_up.shape != w_gate.shape or _weight(w_up, up_scale, K, "w_up", grouped)[1:] != tuple(gate):
+    dev = _same_device(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, y_scale, offsets)
+    n_rows, x_stride, xs_stride, K = _in_q(x, x_scale, "x")
+    gate = _weight_q(w_gate, gate_scale, K, "w_gate", offsets is not None)
+    if w_up.shape != w_gate.shape or _weight_q(w_up, up_scale, K, "w_up", offsets is not None) != gate:
         raise ValueError("w_gate and w_up (and their scales) must have one shape and one stride")
-    w_stride, w_group, s_stride, s_group = gate
-    y = _empty_q((*x.shape[:-1], N), x.device) if y is None else y
-    shape = (*x.shape[:-1], _groups(N))
-    y_scale = torch.empty(shape, dtype=torch.float32, device=x.device) if y_scale is None else y_scale
-    _check_q(y, y_scale, "y")
-    if tuple(y.shape) != (*x.shape[:-1], N):
-        raise ValueError("y has the wrong shape")
-    ys_stride = _scale_rows(y_scale, shape, "y_scale")
-    _, y_stride = _rows(y, "y")
-    if grouped:
-        _offsets(offsets, w_gate)
+    N, w_stride, w_group, s_stride, s_group = gate
+    lead = x.shape[:-1]
+    y, y_scale = _out_q(y, y_scale, (*lead, N), (*lead, (N + 127) // 128), x, "y")
+    y_stride, ys_stride = _mat(y, "y")[1], _mat(y_scale, "y_scale")[1]
+    s = _raw_stream(stream, dev)
+    if offsets is None:
+        st = glu_gemm_q_fwd(x.data_ptr(), x_stride, x_scale.data_ptr(), xs_stride, w_gate.data_ptr(), w_up.data_ptr(),
+                            w_stride, gate_scale.data_ptr(), up_scale.data_ptr(), s_stride, y.data_ptr(), y_stride,
+                            y_scale.data_ptr(), ys_stride, n_rows, K, N, ACT[act], s)
+    else:
         st = glu_gemm_q_grouped_fwd(x.data_ptr(), x_stride, x_scale.data_ptr(), xs_stride, w_gate.data_ptr(),
                                     w_up.data_ptr(), w_stride, w_group, gate_scale.data_ptr(), up_scale.data_ptr(),
                                     s_stride, s_group, y.data_ptr(), y_stride, y_scale.data_ptr(), ys_stride, n_rows,
-                                    K, N, offsets.data_ptr(), w_gate.shape[0], ACT[act], _stream(stream))
-    else:
-        st = glu_gemm_q_fwd(x.data_ptr(), x_stride, x_scale.data_ptr(), xs_stride, w_gate.data_ptr(), w_up.data_ptr(),
-                            w_stride, gate_scale.data_ptr(), up_scale.data_ptr(), s_stride, y.data_ptr(), y_stride,
-                            y_scale.data_ptr(), ys_stride, n_rows, K, N, ACT[act], _stream(stream))
+                                    K, N, _offsets(offsets, w_gate), w_gate.shape[0], ACT[act], s)
     if st:
-        raise GluError(st, "glu_gemm_q_grouped_fwd" if grouped else "glu_gemm_q_fwd")
+        raise GluError(st, "glu_gemm_q_fwd" if offsets is None else "glu_gemm_q_grouped_fwd")
     return y, y_scale
 
 

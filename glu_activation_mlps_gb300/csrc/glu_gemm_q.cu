@@ -66,8 +66,7 @@ struct Params {
     int n_blocks;                   // column tiles
     int group_m;                    // wide: row tiles side by side in the tile order
     int m_tiles;                    // row tiles; with offsets the most there can be
-    int vec_store;                  // y's base and rows 16-byte aligned
-    int tma_store;                  // ... and its width too: y leaves through the copy engine
+    int tma_store;                  // wide: y's base, rows and width are 16-byte multiples: it leaves through the copy engine
 };
 
 static __device__ unsigned int g_q_timeouts;
@@ -127,6 +126,57 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
           "=r"(r[15])
         : "r"(taddr)
         : "memory");
+}
+
+// Arrives on a barrier of the pair after tensor-memory reads, which the
+// tcgen05 fence before it orders.  The barrier orders nothing else, so the
+// arrival is a release at block scope only: at cluster scope each one waited
+// for the warp's whole memory traffic (1262 us instead of 581 at 4096 x 4096 x
+// 2 x 14336).
+__device__ __forceinline__ void arrive_pair(uint32_t bar_cluster)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+// wait_parity that asks once before it reads the clock: the waits of the K loop
+// are handshakes of a few hundred cycles, one after the other.
+__device__ __forceinline__ bool wait_quick(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done || wait_parity(bar, parity);
+}
+
+// Waits for this thread's tensor-memory loads; the registers pass through, so
+// that no use of them can be moved before the wait.
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// One lane of a converged warp.  The MMA warp runs its loop as a whole and only
+// issues from one lane: the loop's values stay warp-uniform, which is how the
+// MMAs take them.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(yes));
+    return yes != 0;
 }
 
 __device__ __forceinline__ float ld_cluster(uint32_t addr)
@@ -236,52 +286,63 @@ struct Plain {};
 
 // ---------------------------------------------------------------- wide
 
-constexpr int kWideThreads = 320;   // warp 0 loads, warp 1 issues MMAs, warps 2-9 sum and store
+// Warp 0 loads, warp 1 issues MMAs, warps 2-3 prepare scales, warps 4-11 sum
+// and store.  Launched with 168 registers a thread (64512 a block); the first
+// four warps give theirs up to the summing ones: 128 * 88 + 256 * 208 = 64512.
+constexpr int kWideThreads = 384;
 constexpr int kWideEpi = 8;
+constexpr int kChunk = 8;           // K blocks whose scales are prepared at once (32 bytes of a row's)
+constexpr int kChunks = 3;
 
-template <int N>
 struct Wide {
+    static constexpr int N = 256;                           // columns of one tile's sums: two halves of 128
     static constexpr int kTileA = BM * BK;
     static constexpr int kTileB = N / 2 * BK;
     static constexpr int kStageBytes = kTileA + kTileB;
-    static constexpr int kStages = N == 256 ? 5 : 7;
-    static constexpr int kCols = N;                         // one buffer of tensor memory
-    static constexpr int kTmemCols = 2 * kCols;
+    static constexpr int kStages = 5;
+    static constexpr int kCols = N;                         // one of two buffers of tensor memory
     static constexpr int kStageY = kWideEpi * 2 * kBox * 64;
-    static constexpr int kBars = 2 * kStages + 4 + 1 + 4;   // full, empty, acc_full, acc_empty, done, row maxima
-    static constexpr int kMax = 2 * 2 * BM * 4;             // row maxima of two halves, two tiles
+    static constexpr int kBars = 2 * kStages + 2 + 2 * kChunks + 1 + 4;
+    static constexpr int kScales = kChunks * kChunk * 2 * BM * 4;   // [chunk][K block][half][row]
+    static constexpr int kMax = 2 * 2 * BM * 4;             // row maxima of two column halves, two tiles
     static constexpr int kPrefix = (kMaxGroups + 4) * 4;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStageY + kMax + kBars * 8 + 16 + kPrefix;
+    static constexpr int kSmemBytes =
+        1024 + kStages * kStageBytes + kStageY + kScales + kMax + kBars * 8 + 16 + kPrefix;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
 };
 
-// Act = Plain: T is y's 16-bit type, a tile is N columns.  Otherwise y is
-// quantised, N = 256 holds 128 gate and 128 up columns, and T is unused.
-template <class Act, class T, int N>
+// A tile is 256 rows (128 per block of the pair) and two halves of 128 columns:
+// two neighbouring blocks of b's columns (Act = Plain; T is y's 16-bit type), or
+// a gate and an up block (y is quantised, T is unused).
+// Warps 2-3 fetch the row scales eight K blocks at a time (32 bytes of a row),
+// multiply them by the two weight scales and leave the products in shared
+// memory, three chunks ahead: loaded by the summing threads one K block ahead,
+// their latency was the bound (0.70 PFLOP/s at 4096 x 4096 x 2 x 14336).
+template <class Act, class T>
 __global__ void __launch_bounds__(kWideThreads, 1)
     gemm_q_wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w0,
                        const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_y,
                        const Params p)
 {
-    using S = Wide<N>;
+    using S = Wide;
     constexpr int ST = S::kStages;
     constexpr bool kPlain = std::is_same<Act, Plain>::value;
-    static_assert(kPlain || N == 256, "a gated tile is one block of 128 columns");
-    constexpr int kOutCols = kPlain ? N : N / 2;    // output columns of a tile
-    constexpr int kMine = N / 2;                    // sums per thread
-    constexpr uint32_t kIdesc = idesc_e4m3(2 * BM, N);
+    constexpr int kOutCols = kPlain ? 256 : 128;    // output columns of a tile
+    constexpr uint32_t kIdesc = idesc_e4m3(2 * BM, S::kCols);
 
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = saddr(smem_raw);
     unsigned char *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     unsigned char *ystage = smem + ST * S::kStageBytes;
-    float *rowmax = reinterpret_cast<float *>(ystage + S::kStageY);     // [2 tiles][2 halves][BM]
-    uint64_t *full = reinterpret_cast<uint64_t *>(rowmax + 4 * BM);
-    uint64_t *empty = full + ST;
-    uint64_t *acc_full = empty + ST;        // [2]: the MMAs of one K block done
-    uint64_t *acc_empty = acc_full + 2;     // [2]: both blocks' epilogues have read it
-    uint64_t *done = acc_empty + 2;
-    uint64_t *maxbar = done + 1;            // [4]: both halves of 32 rows have their maxima
+    float *scales = reinterpret_cast<float *>(ystage + S::kStageY);
+    float *rowmax = scales + S::kScales / 4;
+    uint64_t *full = reinterpret_cast<uint64_t *>(rowmax + S::kMax / 4);
+    uint64_t *used = full + ST;             // [ST]: the MMAs of a stage done: it is free and its sums are there
+    uint64_t *acc_empty = used + ST;        // [2]: both blocks' epilogues have read a buffer of sums
+    uint64_t *sc_full = acc_empty + 2;      // [kChunks]: a chunk of scales is in shared memory
+    uint64_t *sc_empty = sc_full + kChunks;
+    uint64_t *done = sc_empty + kChunks;
+    uint64_t *maxbar = done + 1;            // [4]: both column halves of 32 rows have their maxima
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(maxbar + 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(maxbar + 4) + 1;
     int *prefix = reinterpret_cast<int *>(maxbar + 6);
@@ -305,19 +366,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         };
         for (int s = 0; s < ST; ++s) {
             init(&full[s], 1);
-            init(&empty[s], 1);
+            init(&used[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
-            init(&acc_full[b], 1);
-            init(&acc_empty[b], kWideEpi * 2);
+        for (int b = 0; b < 2; ++b) init(&acc_empty[b], kWideEpi * 2);
+        for (int b = 0; b < 4; ++b) init(&maxbar[b], 2);
+        for (int c = 0; c < kChunks; ++c) {
+            init(&sc_full[c], 2);
+            init(&sc_empty[c], kWideEpi);
         }
         init(done, 1);
-        for (int q = 0; q < 4; ++q) init(&maxbar[q], 2);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == 1) tmem_alloc<2>(saddr(const_cast<uint32_t *>(tmem_slot)), S::kTmemCols);
+    if (warp == 1) tmem_alloc<2>(saddr(const_cast<uint32_t *>(tmem_slot)), 2 * S::kCols);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     count_tiles(p, 2 * BM, prefix);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -327,18 +389,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const int n_tiles = prefix[p.n_groups] * p.n_blocks;
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 0 && lane == 0) {
             uint32_t it = 0;
             for (int t = cluster; t < n_tiles && !*abort_flag; t += n_clusters) {
                 const Tile tl = tile_at(p, prefix, t, 2 * BM);
                 const int m0 = tl.row + int(rank) * BM;
+                // this block's half of the weight rows: 128 columns of y, or gate or up
                 const CUtensorMap *tw = rank == 0 ? &tm_w0 : &tm_w1;
-                const int w0 = kPlain ? tl.nb * N + int(rank) * (N / 2) : tl.nb * kOutCols;
+                const int w0 = tl.nb * kOutCols + (kPlain ? int(rank) * 128 : 0);
                 for (int kt = 0; kt < p.k_tiles; ++kt, ++it) {
                     const uint32_t s = it % ST, use = it / ST;
                     if (*abort_flag) break;
-                    if (use > 0 && !wait_parity(saddr(&empty[s]), (use - 1) & 1)) {
+                    if (use > 0 && !wait_parity(saddr(&used[s]), (use - 1) & 1)) {
                         raise_abort();
                         break;
                     }
@@ -362,48 +426,100 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                         break;
                     }
             }
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
+        } else if (warp == 1) {
+            // The issuing loop is a bound of its own (it took 860 cycles a K
+            // block with one commit for the stage, another for the sums and the
+            // abort flag read every time): one barrier tells both the loader
+            // and the epilogues that the MMAs of a stage are done.
             if (rank == 0) {
-                uint32_t it = 0;
+                uint32_t st = 0, phase = 0, ab = 0, acc_phase = 1;     // the first waits on acc_empty pass
                 bool ok = true;
+                const uint32_t ring = saddr(smem);
                 for (int t = cluster; t < n_tiles && ok; t += n_clusters) {
-                    for (int kt = 0; kt < p.k_tiles; ++kt, ++it) {
-                        const uint32_t s = it % ST, use = it / ST;
-                        const uint32_t ab = it & 1, use_acc = it >> 1;
-                        if (*abort_flag ||
-                            (use_acc > 0 && !wait_parity(saddr(&acc_empty[ab]), (use_acc - 1) & 1)) ||
-                            !wait_parity(saddr(&full[s]), use & 1)) {
-                            raise_abort();
-                            ok = false;
+                    for (int kt = 0; kt < p.k_tiles; ++kt) {
+                        const uint32_t a0 = ring + st * S::kStageBytes;
+                        const uint64_t da = desc_sw128(a0), db = desc_sw128(a0 + S::kTileA);
+                        ok = wait_quick(saddr(&full[st]), phase) && wait_quick(saddr(&acc_empty[ab]), acc_phase);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) {
+                            if (lane == 0) raise_abort();
                             break;
                         }
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        const uint32_t a0 = saddr(smem + s * S::kStageBytes);
-                        const uint64_t da = desc_sw128(a0), db = desc_sw128(a0 + S::kTileA);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < BK / 32; ++kk) {
-                            const uint64_t step = uint64_t(kk * 32 >> 4);   // 32 bytes inside the swizzle row
-                            mma_f8<2>(tmem + ab * S::kCols, da + step, db + step, kIdesc, kk != 0);
+                            for (int kk = 0; kk < BK / 32; ++kk) {
+                                const uint64_t step = uint64_t(kk * 32 >> 4);   // 32 bytes inside the swizzle row
+                                mma_f8<2>(tmem + ab * S::kCols, da + step, db + step, kIdesc, kk != 0);
+                            }
+                            mma_commit<2>(saddr(&used[st]));
                         }
-                        mma_commit<2>(saddr(&empty[s]));
-                        mma_commit<2>(saddr(&acc_full[ab]));
+                        __syncwarp();
+                        if (++st == ST) {
+                            st = 0;
+                            phase ^= 1;
+                        }
+                        ab ^= 1;
+                        if (ab == 0) acc_phase ^= 1;
                     }
                 }
-                mma_commit<2>(saddr(done));
+                if (elect_one()) mma_commit<2>(saddr(done));
+                __syncwarp();
             }
-            if (!wait_parity(saddr(done), 0)) atomicAdd(&g_q_timeouts, 1u);
+            if (!wait_parity(saddr(done), 0) && lane == 0) atomicAdd(&g_q_timeouts, 1u);
+        } else if (warp >= 2) {
+            // scales: this thread prepares two of the block's 128 rows
+            const int id = (warp - 2) * 32 + lane;
+            uint32_t cc = 0;
+            bool ok = true;
+            const int wlast = (p.N - 1) / quant::kBlock;
+            for (int t = cluster; t < n_tiles && ok; t += n_clusters) {
+                const Tile tl = tile_at(p, prefix, t, 2 * BM);
+                const int m0 = tl.row + int(rank) * BM + id;
+                const float *sa0 = p.sa + int64_t(m0 < tl.end ? m0 : 0) * p.sa_stride;
+                const float *sa1 = p.sa + int64_t(m0 + 64 < tl.end ? m0 + 64 : 0) * p.sa_stride;
+                const int b0 = kPlain ? tl.nb * 2 : tl.nb, b1 = kPlain ? min(b0 + 1, wlast) : b0;
+                const float *sw0 = p.sw0 + int64_t(tl.e) * p.sw_group + int64_t(b0) * p.sw_stride;
+                const float *sw1 = p.sw1 + int64_t(tl.e) * p.sw_group + int64_t(b1) * p.sw_stride;
+                for (int kb = 0; kb < p.k_tiles; kb += kChunk, ++cc) {
+                    float r0[kChunk], r1[kChunk], v0[kChunk], v1[kChunk];
+#pragma unroll
+                    for (int k = 0; k < kChunk; ++k) {
+                        const bool in = kb + k < p.k_tiles;
+                        r0[k] = in && m0 < tl.end ? sa0[kb + k] : 0.0f;
+                        r1[k] = in && m0 + 64 < tl.end ? sa1[kb + k] : 0.0f;
+                        v0[k] = in ? sw0[kb + k] : 0.0f;
+                        v1[k] = in ? sw1[kb + k] : 0.0f;
+                    }
+                    const uint32_t slot = cc % kChunks, use = cc / kChunks;
+                    ok = __all_sync(0xFFFFFFFFu,
+                                    *abort_flag == 0 &&
+                                        (use == 0 || wait_parity(saddr(&sc_empty[slot]), (use - 1) & 1)));
+                    if (!ok) {
+                        if (lane == 0) raise_abort();
+                        break;
+                    }
+                    float *o = scales + slot * (kChunk * 2 * BM) + id;
+#pragma unroll
+                    for (int k = 0; k < kChunk; ++k) {
+                        o[(2 * k) * BM] = r0[k] * v0[k];
+                        o[(2 * k) * BM + 64] = r1[k] * v0[k];
+                        o[(2 * k + 1) * BM] = r0[k] * v1[k];
+                        o[(2 * k + 1) * BM + 64] = r1[k] * v1[k];
+                    }
+                    __syncwarp();
+                    if (lane == 0) arrive_local(saddr(&sc_full[slot]));
+                }
+            }
         }
     } else {
-        // warp w reads lanes 32 (w % 4) .. +31, one row per thread; the first
-        // four warps take one half of the columns, the others the other half
-        const int q = warp & 3, half = (warp - 2) >> 2;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // warp w reads lanes 32 (w % 4) .. +31, one row per thread; warps 4-7
+        // take the first 64 columns of either half, warps 8-11 the others
+        const int q = warp & 3, part = (warp - 4) >> 2;
         const uint32_t lane_base = uint32_t(q * 32) << 16;
-        // plain: columns half * N/2 ..; gated: 64 gate and 64 up columns
-        const uint32_t col0 = kPlain ? uint32_t(half * (N / 2)) : uint32_t(half * 64);
-        const uint32_t col1 = kPlain ? col0 + kMine / 2 : uint32_t(128 + half * 64);
-        uint32_t it = 0, n_boxes = 0;
+        const uint32_t empty0 = mapa(saddr(&acc_empty[0]), 0);
+        uint32_t it = 0, st = 0, phase = 0, cc = 0, n_boxes = 0;
         int lt = 0;
         bool ok = true;
         for (int t = cluster; t < n_tiles && ok; t += n_clusters, ++lt) {
@@ -411,105 +527,119 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const int base = tl.row + int(rank) * BM + q * 32;
             const int m = base + lane;
             const bool on = m < tl.end;
-            // this thread's row scales and its two column halves' weight scales
-            const float *sa = p.sa + int64_t(on ? m : 0) * p.sa_stride;
-            const int wlast = (p.N - 1) / quant::kBlock;
-            const int wb = kPlain ? min((tl.nb * N + half * (N / 2)) / quant::kBlock, wlast) : tl.nb;
-            const float *s0 = p.sw0 + int64_t(tl.e) * p.sw_group + int64_t(wb) * p.sw_stride;
-            const float *s1 = p.sw1 + int64_t(tl.e) * p.sw_group + int64_t(wb) * p.sw_stride;
-            f2 acc[kMine / 2];
+            f2 acc[2][32];
 #pragma unroll
-            for (int j = 0; j < kMine / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
-            float na = on ? sa[0] : 0.0f, n0 = s0[0], n1 = kPlain ? 0.0f : s1[0];
-            for (int kt = 0; kt < p.k_tiles; ++kt, ++it) {
-                const float f0 = na * n0, f1 = kPlain ? f0 : na * n1;
-                if (kt + 1 < p.k_tiles) {       // the next block's scales, loaded while this one is awaited
-                    na = on ? sa[kt + 1] : 0.0f;
-                    n0 = s0[kt + 1];
-                    if (!kPlain) n1 = s1[kt + 1];
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) acc[h][j] = make_float2(0.0f, 0.0f);
+            for (int kt = 0; kt < p.k_tiles && ok; ++kt, ++it) {
+                const uint32_t slot = cc % kChunks;
+                if (kt % kChunk == 0) ok = wait_parity(saddr(&sc_full[slot]), (cc / kChunks) & 1);
+                const float *sc = scales + (slot * kChunk + uint32_t(kt % kChunk)) * (2 * BM) + q * 32 + lane;
+                const float sc0 = sc[0], sc1 = sc[BM];
+                if (kt % kChunk == kChunk - 1 || kt + 1 == p.k_tiles) {     // this chunk read
+                    __syncwarp();
+                    if (lane == 0) arrive_local(saddr(&sc_empty[slot]));
+                    ++cc;
                 }
-                const uint32_t ab = it & 1, use_acc = it >> 1;
-                ok = __all_sync(0xFFFFFFFFu, wait_parity(saddr(&acc_full[ab]), use_acc & 1));
+                const uint32_t ab = it & 1;
+                ok = __all_sync(0xFFFFFFFFu, ok && wait_quick(saddr(&used[st]), phase));
+                if (++st == ST) {
+                    st = 0;
+                    phase ^= 1;
+                }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 if (!ok) {
                     if (lane == 0) raise_abort();
                     break;
                 }
-                const uint32_t a0 = tmem + lane_base + ab * S::kCols;
+                // 32 columns are multiplied while the next 32 are on their way
+                const uint32_t a0 = tmem + lane_base + ab * S::kCols + uint32_t(part * 64);
+                const f2 f0 = splat(sc0), f1 = splat(sc1);
+                uint32_t r0[32], r1[32];
+                const auto add = [](f2 (&a)[32], int at, const uint32_t (&r)[32], f2 f) {
 #pragma unroll
-                for (int c = 0; c < kMine; c += 32) {
-                    uint32_t r[32];
-                    const bool second = c >= kMine / 2;
-                    tmem_ld32(a0 + (second ? col1 + uint32_t(c - kMine / 2) : col0 + uint32_t(c)), r);
-                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                    if (c + 32 == kMine) {      // all of this block's sums read
-                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) arrive_cluster(mapa(saddr(&acc_empty[ab]), 0));
-                    }
-                    const f2 f = splat(second ? f1 : f0);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        acc[(c + j) / 2] = fma2(pair(r[j], r[j + 1]), f, acc[(c + j) / 2]);
-                }
+                    for (int j = 0; j < 16; ++j) a[at + j] = fma2(pair(r[2 * j], r[2 * j + 1]), f, a[at + j]);
+                };
+                tmem_ld32(a0, r0);
+                tmem_wait(r0);
+                tmem_ld32(a0 + 32, r1);
+                add(acc[0], 0, r0, f0);
+                tmem_wait(r1);
+                tmem_ld32(a0 + 128, r0);
+                add(acc[0], 16, r1, f0);
+                tmem_wait(r0);
+                tmem_ld32(a0 + 160, r1);
+                add(acc[1], 0, r0, f1);
+                tmem_wait(r1);
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                if (elect_one()) arrive_pair(empty0 + 8 * ab);
+                add(acc[1], 16, r1, f1);
             }
             if (!ok || __any_sync(0xFFFFFFFFu, *abort_flag != 0)) break;
 
-            // a box may leave through the copy engine if all its rows are this
-            // expert's, or the matrix ends where they end (the engine clips)
-            const bool box = p.tma_store && (base + kBox <= tl.end || tl.end == p.M) && base < tl.end;
-            const auto stage_box = [&](const uint32_t (&w)[16], int x) {
-                const uint32_t buf = saddr(ystage) + uint32_t((warp - 2) * 2 + (n_boxes & 1)) * (kBox * 64);
+            // Each warp's 32 rows of 64 bytes go through shared memory.  They may
+            // leave through the copy engine if all of them are this expert's,
+            // or the matrix ends where they end (the engine clips); else the
+            // warp writes them row by row, a row's elements side by side.
+            const bool box = p.tma_store && (base + kBox <= tl.end || tl.end == p.M);
+            const auto store_box = [&](const uint32_t (&w)[16], int n) {
+                if (n >= p.N || base >= tl.end) return;
+                unsigned char *buf = ystage + ((warp - 4) * 2 + (n_boxes & 1)) * (kBox * 64);
                 if (lane == 0 && n_boxes >= 2)      // the box stored from this buffer has been read
                     asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                 __syncwarp();
-                const uint32_t row = buf + uint32_t(lane) * 64u, sw = (uint32_t(lane) >> 1) & 3u;
+                const uint32_t row = saddr(buf) + uint32_t(lane) * 64u, sw = (uint32_t(lane) >> 1) & 3u;
 #pragma unroll
                 for (uint32_t c = 0; c < 4; ++c)
                     st_shared16(row + ((c ^ sw) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (box) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) tma_store(&tm_y, saddr(buf), n, base);
+                    ++n_boxes;
+                    return;
+                }
                 __syncwarp();
-                if (lane == 0) tma_store(&tm_y, buf, x, base);
-                ++n_boxes;
+                const int rows = min(kBox, tl.end - base);
+                const uint32_t at = uint32_t(lane) * 2, cols = uint32_t(p.N - n) * (kPlain ? 2 : 1);
+                for (int r = 0; r < rows; ++r) {
+                    const uint32_t chunk = (at >> 4) ^ ((uint32_t(r) >> 1) & 3u);
+                    const uint16_t v = *reinterpret_cast<const uint16_t *>(buf + r * 64 + chunk * 16 + (at & 15));
+                    char *dst = p.y + int64_t(base + r) * p.y_stride + int64_t(n) * (kPlain ? 2 : 1) + at;
+                    if constexpr (kPlain) {
+                        if (at < cols) *reinterpret_cast<uint16_t *>(dst) = v;
+                    } else {
+                        if (at < cols) dst[0] = char(v & 0xFFu);
+                        if (at + 1 < cols) dst[1] = char(v >> 8);
+                    }
+                }
+                __syncwarp();
             };
             if constexpr (kPlain) {
                 using Cd = Codec<T>;
 #pragma unroll
-                for (int c = 0; c < kMine; c += 32) {
-                    const int n = tl.nb * N + half * (N / 2) + c;
+                for (int c = 0; c < 4; ++c) {
+                    const int n = tl.nb * kOutCols + (c / 2) * 128 + part * 64 + (c % 2) * 32;
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float f[2] = {acc[c / 2 + j].x, acc[c / 2 + j].y};
+                        const f2 v = acc[c / 2][(c % 2) * 16 + j];
+                        const float f[2] = {v.x, v.y};
                         w[j] = Cd::put(f);
                     }
-                    if (box) {
-                        if (n < p.N) stage_box(w, n);
-                    } else if (on) {
-                        char *dst = p.y + int64_t(m) * p.y_stride + int64_t(n) * 2;
-                        if (p.vec_store && n + 32 <= p.N) {
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) {
-                                const uint32_t w4[4] = {w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]};
-                                Access<16>::store(dst + 16 * v, w4);
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (n + j < p.N) Cd::store1(dst + 2 * j, Cd::get(w[j / 2], j % 2));
-                        }
-                    }
+                    store_box(w, n);
                 }
             } else {
-                // y = act(gate) * up over this thread's 64 columns, and the row's maximum over both halves
+                // y = act(gate) * up over this thread's 64 columns, and the row's maximum over both parts
                 float top = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    acc[j] = gated<Act>(acc[j], acc[32 + j]);
-                    top = fmaxf(top, fmaxf(fabsf(acc[j].x), fabsf(acc[j].y)));
+                    acc[0][j] = gated<Act>(acc[0][j], acc[1][j]);
+                    top = fmaxf(top, fmaxf(fabsf(acc[0][j].x), fabsf(acc[0][j].y)));
                 }
                 float *mx = rowmax + (lt & 1) * 2 * BM + q * 32 + lane;
-                mx[half * BM] = top;
+                mx[part * BM] = top;
                 __syncwarp();
                 if (lane == 0) arrive_local(saddr(&maxbar[q]));
                 ok = __all_sync(0xFFFFFFFFu, wait_parity(saddr(&maxbar[q]), lt & 1));
@@ -517,30 +647,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     if (lane == 0) raise_abort();
                     break;
                 }
-                top = fmaxf(top, mx[(half ^ 1) * BM]);
+                top = fmaxf(top, mx[(part ^ 1) * BM]);
                 const quant::Divider d(top);
                 uint32_t w[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    w[j] = quant::pack4(d(acc[2 * j].x), d(acc[2 * j].y), d(acc[2 * j + 1].x), d(acc[2 * j + 1].y));
-                const int n = tl.nb * kOutCols + half * 64;
-                if (on && half == 0) p.ys[int64_t(m) * p.ys_stride + tl.nb] = d.scale();
-                if (box) {
-                    if (n < p.N) stage_box(w, n);
-                } else if (on) {
-                    char *dst = p.y + int64_t(m) * p.y_stride + n;
-                    if (p.vec_store && n + 64 <= p.N) {
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const uint32_t w4[4] = {w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]};
-                            Access<16>::store(dst + 16 * v, w4);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if (n + j < p.N) dst[j] = char((w[j / 4] >> (8 * (j % 4))) & 0xFFu);
-                    }
-                }
+                    w[j] = quant::pack4(d(acc[0][2 * j].x), d(acc[0][2 * j].y), d(acc[0][2 * j + 1].x),
+                                        d(acc[0][2 * j + 1].y));
+                if (on && part == 0) p.ys[int64_t(m) * p.ys_stride + tl.nb] = d.scale();
+                store_box(w, tl.nb * kOutCols + part * 64);
             }
         }
         if (lane == 0 && n_boxes > 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -552,7 +667,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (warp == 1) {
         __syncwarp();
-        tmem_dealloc<2>(tmem, S::kTmemCols);
+        tmem_dealloc<2>(tmem, 2 * S::kCols);
     }
 }
 
@@ -945,17 +1060,16 @@ constexpr int kOutF16 = 4, kOutBF16 = 5;
 using WideFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Params);
 using NarrowFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Params, int);
 
-WideFn wide_kernel(int out, int n)
+WideFn wide_kernel(int out)
 {
     using B = __nv_bfloat16;
-    using H = __half;
     switch (out) {
-    case 0: return gemm_q_wide_kernel<Silu, B, 256>;
-    case 1: return gemm_q_wide_kernel<GeluErf, B, 256>;
-    case 2: return gemm_q_wide_kernel<GeluTanh, B, 256>;
-    case 3: return gemm_q_wide_kernel<Relu, B, 256>;
-    case 4: return n == 256 ? gemm_q_wide_kernel<Plain, H, 256> : gemm_q_wide_kernel<Plain, H, 128>;
-    default: return n == 256 ? gemm_q_wide_kernel<Plain, B, 256> : gemm_q_wide_kernel<Plain, B, 128>;
+    case 0: return gemm_q_wide_kernel<Silu, B>;
+    case 1: return gemm_q_wide_kernel<GeluErf, B>;
+    case 2: return gemm_q_wide_kernel<GeluTanh, B>;
+    case 3: return gemm_q_wide_kernel<Relu, B>;
+    case 4: return gemm_q_wide_kernel<Plain, __half>;
+    default: return gemm_q_wide_kernel<Plain, B>;
     }
 }
 
@@ -981,7 +1095,7 @@ int narrow_smem(int out)
 
 // The shared-memory opt-in of each kernel, once per device.
 constexpr int kMaxDevices = 64;
-std::atomic<int> g_opted[kMaxDevices][6][5];    // [device][output][128- or 256-wide, 16, 32, 64]
+std::atomic<int> g_opted[kMaxDevices][6][4];    // [device][output][wide, 16, 32, 64]
 
 int opt_in(const void *fn, int smem, int dev, int out, int shape)
 {
@@ -1162,7 +1276,6 @@ int run(Args x, glu_stream_t stream)
     p.M = int(x.M);
     p.N = int(x.N);
     p.k_tiles = int((x.K + BK - 1) / BK);
-    p.vec_store = uintptr_t(x.y) % 16 == 0 && p.y_stride % 16 == 0;
     glu_launch_info_t info{};
     info.launched = 1;
     info.path = plain ? 12 : 11;
@@ -1192,14 +1305,14 @@ int run(Args x, glu_stream_t stream)
         p.m_tiles = p.group_m = int(m_tiles);
         const int64_t tiles = m_tiles * p.n_blocks;
         const int64_t slots = int64_t(sms) * (nt <= 32 ? 2 : 1);
-        // Blocks per tile: the split of K whose rounds of tiles take the fewest
-        // K blocks; one K block's time stands for each doubling of the parts
-        // that have to be added.
+        // Blocks per tile: the split of K whose rounds of tiles take the least
+        // time, in K blocks: a round costs about eight more for its start and
+        // its end, and adding the parts half a one each.
         int split = 1;
         if (!grouped) {
             int64_t best = -1;
             for (int sp = 1; sp <= 8 && sp * 2 <= p.k_tiles; sp *= 2) {
-                const int64_t cost = (tiles * sp + slots - 1) / slots * ((p.k_tiles + sp - 1) / sp) + sp / 2;
+                const int64_t cost = (tiles * sp + slots - 1) / slots * ((p.k_tiles + sp - 1) / sp + 8) + sp / 2;
                 if (best < 0 || cost < best) {
                     best = cost;
                     split = sp;
@@ -1213,7 +1326,7 @@ int run(Args x, glu_stream_t stream)
         const NarrowFn fn = nt == 16 ? narrow_kernel<16>(x.out) : nt == 32 ? narrow_kernel<32>(x.out) : narrow_kernel<64>(x.out);
         const int smem = nt == 16 ? narrow_smem<16>(x.out) : nt == 32 ? narrow_smem<32>(x.out) : narrow_smem<64>(x.out);
         const void *f = reinterpret_cast<const void *>(fn);
-        if (int st = opt_in(f, smem, dev, x.out, nt == 16 ? 2 : nt == 32 ? 3 : 4)) return st;
+        if (int st = opt_in(f, smem, dev, x.out, nt == 16 ? 1 : nt == 32 ? 2 : 3)) return st;
         const int64_t grid = split > 1 ? tiles * split : (tiles < slots ? tiles : slots);
         void *args[] = {&ta, &t0, &t1, &p, &split};
         if (int st = launch(f, unsigned(grid), kNarrowThreads, smem, unsigned(split), args, s)) return st;
@@ -1226,8 +1339,7 @@ int run(Args x, glu_stream_t stream)
         return GLU_OK;
     }
 
-    const int n = 256;
-    const int out_cols = plain ? n : n / 2;
+    const int out_cols = plain ? 256 : 128;
     p.n_blocks = int((x.N + out_cols - 1) / out_cols);
     const int64_t block_bytes = int64_t(2 * BM) * x.K;
     int64_t group = (int64_t(48) << 20) / block_bytes;
@@ -1240,20 +1352,19 @@ int run(Args x, glu_stream_t stream)
     p.m_tiles = int(m_tiles);
     p.group_m = int(group);
     if (!make_map(&ta, u8, x.a, x.K, x.M, x.a_stride, 0, 0, BK, BM, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map(&t0, u8, x.w0, x.K, x.N, x.w_stride, depth, w_group, BK, n / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map(&t1, u8, x.w1, x.K, x.N, x.w_stride, depth, w_group, BK, n / 2, CU_TENSOR_MAP_SWIZZLE_128B))
+        !make_map(&t0, u8, x.w0, x.K, x.N, x.w_stride, depth, w_group, BK, BM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&t1, u8, x.w1, x.K, x.N, x.w_stride, depth, w_group, BK, BM, CU_TENSOR_MAP_SWIZZLE_128B))
         return glu::cuda_fail(cudaErrorInvalidValue);
     const auto yt = x.out == kOutF16    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                     : x.out == kOutBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                         : u8;
     // the copy engine clips a box at y's last column in 16-byte units
-    p.tma_store = p.vec_store && (x.N * E) % 16 == 0 && p.y_stride < (int64_t(1) << 40) &&
+    p.tma_store = uintptr_t(x.y) % 16 == 0 && p.y_stride % 16 == 0 && (x.N * E) % 16 == 0 && p.y_stride < (int64_t(1) << 40) &&
                   make_map(&ty, yt, x.y, x.N, x.M, p.y_stride, 0, 0, 64 / E, kBox, CU_TENSOR_MAP_SWIZZLE_64B);
     if (!p.tma_store) ty = ta;
-    const WideFn fn = wide_kernel(x.out, n);
-    const int smem = n == 256 ? Wide<256>::kSmemBytes : Wide<128>::kSmemBytes;
-    const void *f = reinterpret_cast<const void *>(fn);
-    if (int st = opt_in(f, smem, dev, x.out, n == 256 ? 1 : 0)) return st;
+    const int smem = Wide::kSmemBytes;
+    const void *f = reinterpret_cast<const void *>(wide_kernel(x.out));
+    if (int st = opt_in(f, smem, dev, x.out, 0)) return st;
     const int64_t slots = sms / 2;
     const int64_t clusters = tiles < slots ? tiles : slots;
     void *args[] = {&ta, &t0, &t1, &ty, &p};
@@ -1261,7 +1372,7 @@ int run(Args x, glu_stream_t stream)
     info.threads = kWideThreads;
     info.grid = int32_t(2 * clusters);
     info.unroll = 2;
-    info.vec_bytes = p.tma_store ? 64 : (p.vec_store ? 16 : E);
+    info.vec_bytes = p.tma_store ? 64 : E;
     info.vector_units = grouped ? 0 : tiles;
     glu::record_launch(info);
     return GLU_OK;
