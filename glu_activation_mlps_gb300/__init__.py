@@ -604,8 +604,8 @@ def _empty_q(shape, like):
     import torch
     n = shape[-1]
     if n % 16 == 0:
-        return like.new_empty(shape, dtype=torch.float8_e4m3fn)
-    return like.new_empty((*shape[:-1], n + -n % 16), dtype=torch.float8_e4m3fn)[..., :n]
+        return torch.empty(shape, dtype=torch.float8_e4m3fn, device=like.device)
+    return torch.empty((*shape[:-1], n + -n % 16), dtype=torch.float8_e4m3fn, device=like.device)[..., :n]
 
 
 def _out_q(q, scale, shape, scale_shape, like, name):
@@ -616,7 +616,7 @@ def _out_q(q, scale, shape, scale_shape, like, name):
     elif q.dtype != torch.float8_e4m3fn or q.shape != shape:
         raise ValueError(f"{name} must be float8_e4m3fn of shape {tuple(shape)}")
     if scale is None:
-        scale = like.new_empty(scale_shape, dtype=torch.float32)
+        scale = torch.empty(scale_shape, dtype=torch.float32, device=like.device)
     elif scale.dtype != torch.float32 or scale.shape != scale_shape:
         raise ValueError(f"{name}'s scales must be float32 of shape {tuple(scale_shape)}")
     return q, scale
@@ -705,13 +705,13 @@ def add_rmsnorm_q(x, residual, gamma, eps: float = 1e-5, *, h=None, q=None, scal
     n_rows, x_stride = _mat(x, "x")
     r_stride = _mat(residual, "residual")[1]
     if h is None:
-        h = x.new_empty(shape)
+        h = torch.empty(shape, dtype=dtype, device=x.device)
     elif h.shape != shape or h.dtype != dtype:
         raise ValueError("h must match x in shape and dtype")
     q, scale = _out_q(q, scale, shape, (*shape[:-1], (H + 127) // 128), x, "q")
     want_rstd = rstd is not None and rstd is not False
     if rstd is True:
-        rstd = x.new_empty(n_rows, dtype=torch.float32)
+        rstd = torch.empty(n_rows, dtype=torch.float32, device=x.device)
     if want_rstd and (rstd.dtype != torch.float32 or rstd.numel() != n_rows or not rstd.is_contiguous() or
                       rstd.get_device() != dev):
         raise ValueError("rstd must be a contiguous float32 tensor with one entry per row")
@@ -736,7 +736,7 @@ def gemm_q_nt(a, a_scale, b, b_scale, *, d=None, dtype=None, offsets=None, strea
     N, b_stride, b_group, bs_stride, bs_group = _weight_q(b, b_scale, K, "b", offsets is not None)
     shape = (*a.shape[:-1], N)
     if d is None:
-        d = a.new_empty(shape, dtype=dtype or torch.bfloat16)
+        d = torch.empty(shape, dtype=dtype or torch.bfloat16, device=a.device)
     elif d.shape != shape or (dtype is not None and d.dtype != dtype):
         raise ValueError("d has the wrong shape or dtype")
     d_stride = _mat(d, "d")[1]

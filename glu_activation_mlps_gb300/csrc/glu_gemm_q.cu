@@ -115,6 +115,15 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, 
             : "memory");
 }
 
+// The same box of the first expert into L2 only.
+__device__ __forceinline__ void prefetch3(const CUtensorMap *map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(0)
+                 : "memory");
+}
+
 // 16 consecutive fp32 columns of this warp's 32 tensor-memory lanes.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
 {
@@ -675,6 +684,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
 constexpr int kNarrowThreads = 192;     // warp 0 loads, warp 1 issues MMAs, warps 2-5 sum and store
 constexpr int kAhead = 4;               // K blocks whose row scales are loaded ahead
+constexpr int kMaxSplit = 8;            // blocks of a cluster that share a tile's K blocks
 
 constexpr int pow2_at_least(int v) { return v <= 32 ? 32 : v <= 64 ? 64 : v <= 128 ? 128 : v <= 256 ? 256 : 512; }
 
@@ -683,8 +693,9 @@ struct Narrow {
     static constexpr int kTileW = BM * BK;
     static constexpr int kTileA = NT * BK;
     static constexpr int kStageBytes = MATS * kTileW + kTileA;
-    // two blocks per SM up to 32 rows, else one
-    static constexpr int kStages = (NT <= 32 ? 104 * 1024 : 200 * 1024) / kStageBytes;
+    // two blocks per SM, each with three stages or more, where that fits
+    static constexpr int kPerSm = 104 * 1024 / kStageBytes >= 3 ? 2 : 1;
+    static constexpr int kStages = (kPerSm == 2 ? 104 : 200) * 1024 / kStageBytes;
     static constexpr int kCols = MATS * NT;
     static constexpr int kTmemCols = pow2_at_least(2 * kCols);
     static constexpr int kRing = kStages * kStageBytes;
@@ -755,6 +766,16 @@ __global__ void __launch_bounds__(kNarrowThreads)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<1>(saddr(const_cast<uint32_t *>(tmem_slot)), S::kTmemCols);
+    // without experts the block's first weights are known: L2 is asked for a
+    // ring of them while the previous kernel ends (L2 is the point of
+    // coherence: what that kernel still writes there is read after the wait)
+    if (!p.offsets && warp == 2 && lane < ST) {
+        const int nb = cluster / p.m_tiles, kt = int(int64_t(p.k_tiles) * rank / split) + lane;
+        if (nb < p.n_blocks && kt < p.k_tiles) {
+            prefetch3(&tm_w0, kt * BK, nb * BM);
+            if constexpr (!kPlain) prefetch3(&tm_w1, kt * BK, nb * BM);
+        }
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     count_tiles(p, NT, prefix);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -983,10 +1004,14 @@ __global__ void __launch_bounds__(kNarrowThreads)
                 const Tile tl = tile_at(p, prefix, cluster, NT);
                 const int n = NT / split, j0 = int(rank) * n;
                 finish(tl, j0, n, 0, [&](int mat, int j) {
+                    // (all loads before the first sum: each is a trip to another SM)
                     const uint32_t at = saddr(parts + (mat * NT + j0 + j) * BM + q * 32 + lane);
-                    float v = 0.0f;
-                    for (int r = 0; r < split; ++r) v += ld_cluster(mapa(at, uint32_t(r)));
-                    return v;
+                    float v[kMaxSplit], sum = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < kMaxSplit; ++r) v[r] = r < split ? ld_cluster(mapa(at, uint32_t(r))) : 0.0f;
+#pragma unroll
+                    for (int r = 0; r < kMaxSplit; ++r) sum += v[r];
+                    return sum;
                 });
             }
         }
@@ -1077,20 +1102,23 @@ template <int NT>
 NarrowFn narrow_kernel(int out)
 {
     using B = __nv_bfloat16;
-    switch (out) {
-    case 0: return gemm_q_narrow_kernel<Silu, B, NT>;
-    case 1: return gemm_q_narrow_kernel<GeluErf, B, NT>;
-    case 2: return gemm_q_narrow_kernel<GeluTanh, B, NT>;
-    case 3: return gemm_q_narrow_kernel<Relu, B, NT>;
-    case 4: return gemm_q_narrow_kernel<Plain, __half, NT>;
-    default: return gemm_q_narrow_kernel<Plain, B, NT>;
+    if (out == kOutF16) return gemm_q_narrow_kernel<Plain, __half, NT>;
+    if (out == kOutBF16) return gemm_q_narrow_kernel<Plain, B, NT>;
+    if constexpr (NT <= 32) {
+        switch (out) {
+        case 0: return gemm_q_narrow_kernel<Silu, B, NT>;
+        case 1: return gemm_q_narrow_kernel<GeluErf, B, NT>;
+        case 2: return gemm_q_narrow_kernel<GeluTanh, B, NT>;
+        default: return gemm_q_narrow_kernel<Relu, B, NT>;
+        }
     }
+    return nullptr;
 }
 
 template <int NT>
 int narrow_smem(int out)
 {
-    return out < 4 ? Narrow<NT, 2>::kSmemBytes : Narrow<NT, 1>::kSmemBytes;
+    return out < kOutF16 ? Narrow<NT, NT <= 32 ? 2 : 1>::kSmemBytes : Narrow<NT, 1>::kSmemBytes;
 }
 
 // The shared-memory opt-in of each kernel, once per device.
@@ -1296,29 +1324,41 @@ int run(Args x, glu_stream_t stream)
     // rows per expert, as far as the host knows
     const int64_t rows = grouped ? (x.M + x.groups - 1) / x.groups : x.M;
     CUtensorMap ta, t0, t1, ty;
-    if (rows <= 64) {
-        const int nt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-        p.n_blocks = int((x.N + BM - 1) / BM);
-        // with experts at most: each may end in a part of a tile
-        const int64_t m_tiles = grouped ? x.M / nt + (x.groups < x.M ? x.groups : x.M) : (x.M + nt - 1) / nt;
-        if (m_tiles * p.n_blocks > INT32_MAX / 16) return GLU_ERR_SHAPE;
-        p.m_tiles = p.group_m = int(m_tiles);
-        const int64_t tiles = m_tiles * p.n_blocks;
-        const int64_t slots = int64_t(sms) * (nt <= 32 ? 2 : 1);
-        // Blocks per tile: the split of K whose rounds of tiles take the least
-        // time, in K blocks: a round costs about eight more for its start and
-        // its end, and adding the parts half a one each.
-        int split = 1;
-        if (!grouped) {
-            int64_t best = -1;
-            for (int sp = 1; sp <= 8 && sp * 2 <= p.k_tiles; sp *= 2) {
-                const int64_t cost = (tiles * sp + slots - 1) / slots * ((p.k_tiles + sp - 1) / sp + 8) + sp / 2;
-                if (best < 0 || cost < best) {
-                    best = cost;
-                    split = sp;
-                }
-            }
+    const int nt = rows <= 16 ? 16 : rows <= 32 || !plain ? 32 : 64;
+    const int64_t n_blocks = (x.N + BM - 1) / BM;
+    // row tiles; with experts at most: each may end in a part of a tile
+    const auto row_tiles = [&](int64_t r) {
+        return grouped ? x.M / r + (x.groups < x.M ? x.groups : x.M) : (x.M + r - 1) / r;
+    };
+    const int64_t tiles_n = row_tiles(nt) * n_blocks;
+    const int64_t slots_n = int64_t(sms) * (plain || nt == 16 ? 2 : Narrow<32, 2>::kPerSm);
+    // Narrow: blocks per tile, the split of K whose rounds of tiles take the
+    // least time: in K blocks, a round costs about ten more for its start and
+    // its end, and adding the parts half a one each.
+    int split = 1;
+    int64_t best = -1;
+    for (int sp = 1; sp <= (grouped ? 1 : kMaxSplit) && (sp == 1 || sp * 2 <= p.k_tiles); sp *= 2) {
+        const int64_t cost = (tiles_n * sp + slots_n - 1) / slots_n * ((p.k_tiles + sp - 1) / sp + 10) + sp / 2;
+        if (best < 0 || cost < best) {
+            best = cost;
+            split = sp;
         }
+    }
+    // Which kernel.  Up to 32 rows the narrow one wins throughout (16 rows at
+    // 4096 x 4096: 7.2 us against 19).  Beyond, only the plain product has a
+    // narrow form (64 rows a tile; a gated one would hold 128 sums a thread):
+    // by expert up to 96 rows each (64 experts of 2048 x 2048: 73 us against 87
+    // at 64 rows, 108 against 96 at 128); else where its rounds, of K blocks
+    // that take 4/3 the wide kernel's time, end sooner (14336 x 4096: 24 us
+    // against 56 at 128 rows, 41 against 57 at 256, 69 against 58 at 384).
+    const int64_t tiles_w = row_tiles(2 * BM) * ((x.N + (plain ? 255 : 127)) / (plain ? 256 : 128));
+    const int64_t cost_w = (tiles_w + sms / 2 - 1) / (sms / 2) * (p.k_tiles + 9);
+    const bool narrow = rows <= 32 || (plain && (grouped ? rows <= 96 : 4 * best / 3 < cost_w));
+    if (narrow) {
+        const int64_t m_tiles = row_tiles(nt);
+        if (tiles_n > INT32_MAX / 16) return GLU_ERR_SHAPE;
+        p.n_blocks = int(n_blocks);
+        p.m_tiles = p.group_m = int(m_tiles);
         if (!make_map(&ta, u8, x.a, x.K, x.M, x.a_stride, 0, 0, BK, nt, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !make_map(&t0, u8, x.w0, x.K, x.N, x.w_stride, depth, w_group, BK, BM, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !make_map(&t1, u8, x.w1, x.K, x.N, x.w_stride, depth, w_group, BK, BM, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -1327,14 +1367,14 @@ int run(Args x, glu_stream_t stream)
         const int smem = nt == 16 ? narrow_smem<16>(x.out) : nt == 32 ? narrow_smem<32>(x.out) : narrow_smem<64>(x.out);
         const void *f = reinterpret_cast<const void *>(fn);
         if (int st = opt_in(f, smem, dev, x.out, nt == 16 ? 1 : nt == 32 ? 2 : 3)) return st;
-        const int64_t grid = split > 1 ? tiles * split : (tiles < slots ? tiles : slots);
+        const int64_t grid = split > 1 ? tiles_n * split : (tiles_n < slots_n ? tiles_n : slots_n);
         void *args[] = {&ta, &t0, &t1, &p, &split};
         if (int st = launch(f, unsigned(grid), kNarrowThreads, smem, unsigned(split), args, s)) return st;
         info.threads = kNarrowThreads;
         info.grid = int32_t(grid);
         info.unroll = split;
         info.vec_bytes = E;
-        info.vector_units = grouped ? 0 : tiles;
+        info.vector_units = grouped ? 0 : tiles_n;
         glu::record_launch(info);
         return GLU_OK;
     }
@@ -1344,10 +1384,9 @@ int run(Args x, glu_stream_t stream)
     const int64_t block_bytes = int64_t(2 * BM) * x.K;
     int64_t group = (int64_t(48) << 20) / block_bytes;
     group = group < 1 ? 1 : group;
-    const int64_t m_tiles = grouped ? x.M / (2 * BM) + (x.groups < x.M ? x.groups : x.M)
-                                    : (x.M + 2 * BM - 1) / (2 * BM);
+    const int64_t m_tiles = row_tiles(2 * BM);
     if (group > m_tiles) group = m_tiles;
-    const int64_t tiles = m_tiles * p.n_blocks;
+    const int64_t tiles = tiles_w;
     if (tiles > INT32_MAX / 16) return GLU_ERR_SHAPE;
     p.m_tiles = int(m_tiles);
     p.group_m = int(group);
