@@ -6,11 +6,12 @@
 //                         y = s / sqrt(mean(s^2) + eps) * gamma,  q, scale of y by rows
 //
 // Both are bound by HBM: a value is read once and written once.  A thread owns
-// 16 bytes of a row (V = 8 values of a 16-bit type, 4 of f32), so a block of
-// 128 columns is 128 / V neighbouring lanes of one warp and its largest
-// magnitude a few shuffles; the values stay in registers between the load and
-// the store.  Rows that are not 16-byte multiples take the same code with V = 4
-// values at stride 32 (element accesses, coalesced), a block being one warp.
+// pieces of 32 bytes of a row (V = 16 values of a 16-bit type, 8 of f32; 16
+// bytes where the rows are only 16-byte multiples), so a block of 128 columns is
+// 128 / V neighbouring lanes of one warp and its largest magnitude a few
+// shuffles; the values stay in registers between the load and the store.  Other
+// rows take the same code with V = 4 values at stride 32 (element accesses,
+// coalesced), a block being one warp.
 // y is quantised from fp32: it is never rounded to the input's type.
 #include <cuda_runtime.h>
 
@@ -26,11 +27,13 @@
 namespace glu {
 namespace quant {
 
-// How a thread's V values of one 128-column block lie in a row: contiguous
-// with 16-byte accesses (VEC), or at stride 32 with element accesses.
-template <class T, bool VEC>
+// How a thread's V values of one 128-column block lie in a row: VB contiguous
+// bytes in one access (32 or 16), or (VB = 0) at stride 32 with element accesses.
+template <class T, int VB>
 struct Lanes {
-    static constexpr int V = VEC ? 16 / int(sizeof(T)) : 4;
+    static constexpr bool VEC = VB > 0;
+    static constexpr int V = VEC ? VB / int(sizeof(T)) : 4;
+    static constexpr int kWords = VEC ? VB / 4 : V;
     static constexpr int kPer = kBlock / V;         // lanes that share a block
     using C = Codec<T>;
     // first column of the piece number `piece` (counted over the row)
@@ -38,19 +41,19 @@ struct Lanes {
     {
         return VEC ? piece * V : (piece / 32) * kBlock + piece % 32;
     }
-    static constexpr int kStep = VEC ? 1 : 32;      // distance of a thread's columns
-
     struct Raw {
-        uint32_t w[VEC ? 4 : V];
+        uint32_t w[kWords];
     };
     __device__ __forceinline__ static Raw load(const char *row, int col, int H)
     {
         Raw r;
         if constexpr (VEC) {
-            if (col < H)
-                Access<16>::load(row + int64_t(col) * sizeof(T), r.w);
-            else
-                r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0;      // zeros in every type
+            if (col < H) {
+                Access<VB>::load(row + int64_t(col) * sizeof(T), r.w);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) r.w[j] = 0;    // zeros in every type
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -71,10 +74,10 @@ struct Lanes {
     {
         if constexpr (VEC) {
             if (col < H) {
-                uint32_t w[4];
+                uint32_t w[kWords];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = C::put(f + j * C::kPerWord);
-                Access<16>::store(row + int64_t(col) * sizeof(T), w);
+                for (int j = 0; j < kWords; ++j) w[j] = C::put(f + j * C::kPerWord);
+                Access<VB>::store(row + int64_t(col) * sizeof(T), w);
             }
         } else {
 #pragma unroll
@@ -87,7 +90,11 @@ struct Lanes {
     {
         if constexpr (VEC) {
             if (col < H) {
-                if constexpr (V == 8)
+                if constexpr (V == 16) {
+                    const uint32_t w[4] = {pack4(f[0], f[1], f[2], f[3]), pack4(f[4], f[5], f[6], f[7]),
+                                           pack4(f[8], f[9], f[10], f[11]), pack4(f[12], f[13], f[14], f[15])};
+                    Access<16>::store(row + col, w);
+                } else if constexpr (V == 8)
                     asm volatile("st.global.L1::no_allocate.v2.b32 [%0], {%1, %2};" ::"l"(row + col),
                                  "r"(pack4(f[0], f[1], f[2], f[3])), "r"(pack4(f[4], f[5], f[6], f[7]))
                                  : "memory");
@@ -137,12 +144,12 @@ struct NormParams {
 // residual are read once, h, q and the scales written once.  The sum of squares
 // is formed with fused multiply-adds in two chains per thread, then over the
 // warp by shuffles and over the row's warps through shared memory.
-template <class T, int NV, bool VEC>
-__global__ void __launch_bounds__(1024) add_rmsnorm_q_kernel(const NormParams p)
+template <class T, int NV, int VB>
+__global__ void __launch_bounds__(512) add_rmsnorm_q_kernel(const NormParams p)
 {
-    using L = Lanes<T, VEC>;
+    using L = Lanes<T, VB>;
     constexpr int V = L::V;
-    __shared__ float red[32];
+    __shared__ float red[16];
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -169,6 +176,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_q_kernel(const NormParams p)
         }
         L::store(p.h + row * p.sh, L::col(t + k * p.tpr), H, s[k]);
     }
+    typename L::Raw g[NV];          // on its way during the reduction
+#pragma unroll
+    for (int k = 0; k < NV; ++k) g[k] = L::load(p.gamma, L::col(t + k * p.tpr), H);
     float total = sum32(ss[0] + ss[1]);
     if (p.tpr > 32) {
         const int lane = threadIdx.x & 31, nw = p.tpr >> 5;
@@ -181,11 +191,10 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_q_kernel(const NormParams p)
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int piece = t + k * p.tpr, c = L::col(piece);
-        const typename L::Raw g = L::load(p.gamma, c, H);
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            s[k][i] = s[k][i] * rstd * L::get(g, i);
+            s[k][i] = s[k][i] * rstd * L::get(g[k], i);
             m = fmaxf(m, fabsf(s[k][i]));
         }
         const Divider d(L::block_max(m));
@@ -211,10 +220,10 @@ struct QuantParams {
 
 // By rows: a team of tpr threads (a multiple of 32) takes NV pieces each of one
 // row; blockIdx.y counts stretches of NV * tpr pieces along wide rows.
-template <class T, int NV, bool VEC>
+template <class T, int NV, int VB>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
 {
-    using L = Lanes<T, VEC>;
+    using L = Lanes<T, VB>;
     constexpr int V = L::V;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -244,10 +253,10 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
 }
 
 // By blocks: 256 threads hold one 128 x 128 block in registers.
-template <class T, bool VEC>
+template <class T, int VB>
 __global__ void __launch_bounds__(256) quantize_blocks_kernel(const QuantParams p)
 {
-    using L = Lanes<T, VEC>;
+    using L = Lanes<T, VB>;
     constexpr int V = L::V;
     constexpr int kRows = 256 / L::kPer;        // rows of the block loaded at once
     constexpr int NV = kBlock / kRows;
@@ -292,34 +301,41 @@ namespace {
 using NormFn = void (*)(NormParams);
 using QuantFn = void (*)(QuantParams);
 
-template <class T>
-NormFn norm_kernel(int nv, bool vec)
+// The kernel for nv pieces per thread (a power of two that leaves a row of up to
+// 32768 columns to 512 threads, so at most 64 values).
+template <class T, int VB, int NV = 1>
+NormFn norm_kernel(int nv)
 {
-    if (vec) {
-        switch (nv) {
-        case 1: return add_rmsnorm_q_kernel<T, 1, true>;
-        case 2: return add_rmsnorm_q_kernel<T, 2, true>;
-        case 4: return add_rmsnorm_q_kernel<T, 4, true>;
-        default: return sizeof(T) == 4 ? add_rmsnorm_q_kernel<T, sizeof(T) == 4 ? 8 : 4, true> : nullptr;
-        }
-    }
-    switch (nv) {
-    case 1: return add_rmsnorm_q_kernel<T, 1, false>;
-    case 2: return add_rmsnorm_q_kernel<T, 2, false>;
-    case 4: return add_rmsnorm_q_kernel<T, 4, false>;
-    default: return add_rmsnorm_q_kernel<T, 8, false>;
-    }
+    if (nv == NV) return add_rmsnorm_q_kernel<T, NV, VB>;
+    if constexpr (NV * Lanes<T, VB>::V < 64)
+        return norm_kernel<T, VB, 2 * NV>(nv);
+    else
+        return nullptr;
 }
 
 template <class T>
-QuantFn quant_kernel(bool blocks, int nv, bool vec)
+NormFn norm_kernel(int nv, int vb)
 {
-    if (blocks) return vec ? quantize_blocks_kernel<T, true> : quantize_blocks_kernel<T, false>;
-    if (nv == 1) return vec ? quantize_rows_kernel<T, 1, true> : quantize_rows_kernel<T, 1, false>;
-    return vec ? quantize_rows_kernel<T, 4, true> : quantize_rows_kernel<T, 4, false>;
+    return vb == 32 ? norm_kernel<T, 32>(nv) : vb == 16 ? norm_kernel<T, 16>(nv) : norm_kernel<T, 0>(nv);
 }
 
-bool a16(const void *p) { return uintptr_t(p) % 16 == 0; }
+template <class T, int VB>
+QuantFn quant_kernel(bool blocks, int nv)
+{
+    if (blocks) return quantize_blocks_kernel<T, VB>;
+    return nv == 1 ? quantize_rows_kernel<T, 1, VB> : quantize_rows_kernel<T, VB == 32 ? 2 : 4, VB>;
+}
+
+template <class T>
+QuantFn quant_kernel(bool blocks, int nv, int vb)
+{
+    return vb == 32 ? quant_kernel<T, 32>(blocks, nv) : vb == 16 ? quant_kernel<T, 16>(blocks, nv)
+                                                                  : quant_kernel<T, 0>(blocks, nv);
+}
+
+// The widest access (32, 16, or 0 for single elements) that every base and row
+// stride of `bits` (their bytes, or-ed) allows.
+int access_bytes(uint64_t bits) { return bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 0; }
 
 // Launches with the programmatic dependency of every kernel here (the kernel
 // waits for the previous grid itself), or without where that is refused.
@@ -393,15 +409,16 @@ extern "C" int glu_add_rmsnorm_q(const void *x, int64_t x_stride, const void *re
             if (glu::overlap(all[i], all[o])) return GLU_ERR_ALIAS;
     if (uintptr_t(scale) % 4 || (rstd && uintptr_t(rstd) % 4)) return GLU_ERR_STRIDE;
 
-    const int V = 16 / E;
-    const bool vec = a16(x) && a16(residual) && a16(gamma) && a16(h) && (n_cols * E) % 16 == 0 &&
-                     (x_stride * E) % 16 == 0 && (res_stride * E) % 16 == 0 && (h_stride * E) % 16 == 0 &&
-                     uintptr_t(q) % V == 0 && q_stride % V == 0;
-    // pieces (16 bytes, or 4 elements) a row has, and pieces per thread: two up
-    // to 1024 threads, more only beyond
-    const int64_t pieces = vec ? n_cols / V : groups * 32;
-    int nv = pieces <= 128 ? 1 : 2;
-    while (pieces > int64_t(1024) * nv) nv *= 2;
+    // q's accesses are V bytes wide: a quarter or half of the others'
+    int vb = access_bytes(uintptr_t(x) | uintptr_t(residual) | uintptr_t(gamma) | uintptr_t(h) |
+                          uint64_t(n_cols * E) | uint64_t(x_stride * E) | uint64_t(res_stride * E) |
+                          uint64_t(h_stride * E));
+    if (vb && (uintptr_t(q) | uint64_t(q_stride)) % uint64_t(vb / E)) vb = 0;
+    // pieces a row has (V values each), and pieces per thread
+    const int V = vb ? vb / E : 4;
+    const int64_t pieces = vb ? n_cols / V : groups * 32;
+    int nv = 1;
+    while (pieces > int64_t(512) * nv) nv *= 2;
     int tpr = int((pieces + nv - 1) / nv);
     tpr = (tpr + 31) / 32 * 32;
     const int teams = tpr >= 128 ? 1 : 128 / tpr;
@@ -424,14 +441,14 @@ extern "C" int glu_add_rmsnorm_q(const void *x, int64_t x_stride, const void *re
     p.eps = eps;
     const int64_t blocks = (n_rows + teams - 1) / teams;
     if (blocks > INT32_MAX) return GLU_ERR_SHAPE;
-    const NormFn fn = dtype == GLU_F32   ? norm_kernel<float>(nv, vec)
-                      : dtype == GLU_F16 ? norm_kernel<__half>(nv, vec)
-                                         : norm_kernel<__nv_bfloat16>(nv, vec);
+    const NormFn fn = dtype == GLU_F32   ? norm_kernel<float>(nv, vb)
+                      : dtype == GLU_F16 ? norm_kernel<__half>(nv, vb)
+                                         : norm_kernel<__nv_bfloat16>(nv, vb);
     if (int st = launch(fn, dim3(unsigned(blocks)), tpr * teams, p, stream)) return st;
     glu_launch_info_t info{};
     info.launched = 1;
-    info.vec_bytes = vec ? 16 : E;
-    info.unroll = nv * (vec ? V : 4);
+    info.vec_bytes = vb ? vb : E;
+    info.unroll = nv * V;
     info.threads = tpr * teams;
     info.grid = int32_t(blocks);
     info.path = 9;
@@ -453,7 +470,7 @@ extern "C" int glu_quantize(const void *x, int64_t x_stride, void *q, int64_t q_
         return GLU_OK;
     }
     if (!x || !q || !scale) return GLU_ERR_NULL;
-    const int E = dtype == GLU_F32 ? 4 : 2, V = 16 / E;
+    const int E = dtype == GLU_F32 ? 4 : 2;
     const bool by_block = block_rows == kBlock;
     const int64_t groups = (n_cols + kBlock - 1) / kBlock;
     const int64_t srows = by_block ? (n_rows - 1) / kBlock + 1 : n_rows;
@@ -466,8 +483,9 @@ extern "C" int glu_quantize(const void *x, int64_t x_stride, void *q, int64_t q_
         return GLU_ERR_SHAPE;
     if (glu::overlap(sx, sq) || glu::overlap(sx, ss) || glu::overlap(sq, ss)) return GLU_ERR_ALIAS;
     if (uintptr_t(scale) % 4) return GLU_ERR_STRIDE;
-    const bool vec = a16(x) && (n_cols * E) % 16 == 0 && (x_stride * E) % 16 == 0 && uintptr_t(q) % V == 0 &&
-                     q_stride % V == 0;
+    int vb = access_bytes(uintptr_t(x) | uint64_t(n_cols * E) | uint64_t(x_stride * E));
+    if (vb && (uintptr_t(q) | uint64_t(q_stride)) % uint64_t(vb / E)) vb = 0;
+    const int V = vb ? vb / E : 4;
     QuantParams p{};
     p.x = static_cast<const char *>(x);
     p.q = static_cast<char *>(q);
@@ -483,9 +501,11 @@ extern "C" int glu_quantize(const void *x, int64_t x_stride, void *q, int64_t q_
         if (srows > 65535 || groups > INT32_MAX) return GLU_ERR_SHAPE;
         grid = dim3(unsigned(groups), unsigned(srows));
     } else {
-        // four pieces per thread in rows that fill a block with them, else one
-        const int64_t pieces = vec ? n_cols / V : groups * 32;
-        nv = pieces >= 1024 ? 4 : 1;
+        // two 32-byte pieces per thread (four of the others) in rows that fill
+        // a block with them, else one
+        const int64_t pieces = vb ? n_cols / V : groups * 32;
+        const int wide = vb == 32 ? 2 : 4;
+        nv = pieces >= 256 * wide ? wide : 1;
         int64_t tpr = (pieces + nv - 1) / nv;
         tpr = tpr > 256 ? 256 : (tpr + 31) / 32 * 32;
         p.tpr = int(tpr);
@@ -496,14 +516,14 @@ extern "C" int glu_quantize(const void *x, int64_t x_stride, void *q, int64_t q_
         grid = dim3(unsigned(blocks), unsigned(spans));
     }
     const int threads = by_block ? 256 : 256 / p.tpr * p.tpr;
-    const QuantFn fn = dtype == GLU_F32   ? quant_kernel<float>(by_block, nv, vec)
-                       : dtype == GLU_F16 ? quant_kernel<__half>(by_block, nv, vec)
-                                          : quant_kernel<__nv_bfloat16>(by_block, nv, vec);
+    const QuantFn fn = dtype == GLU_F32   ? quant_kernel<float>(by_block, nv, vb)
+                       : dtype == GLU_F16 ? quant_kernel<__half>(by_block, nv, vb)
+                                          : quant_kernel<__nv_bfloat16>(by_block, nv, vb);
     if (int st = launch(fn, grid, threads, p, stream)) return st;
     glu_launch_info_t info{};
     info.launched = 1;
-    info.vec_bytes = vec ? 16 : E;
-    info.unroll = by_block ? 64 : nv * (vec ? V : 4);
+    info.vec_bytes = vb ? vb : E;
+    info.unroll = by_block ? 64 : nv * V;
     info.threads = threads;
     info.grid = int32_t(grid.x * grid.y > INT32_MAX ? INT32_MAX : grid.x * grid.y);
     info.path = 10;
