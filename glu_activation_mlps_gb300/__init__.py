@@ -9,8 +9,10 @@ Two levels:
   * ``glu_fwd`` / ``glu_bwd`` / ``glu_status_string`` / ... : the C entry points
     with the same names and arguments (raw device addresses as ints, strides
     in elements, enum codes, the stream handle as an int);
-  * ``fwd`` / ``bwd``: the same calls taking torch CUDA tensors, reading
-    pointers and strides from the tensors' metadata.
+  * ``fwd`` / ``bwd`` / ...: the same calls taking torch CUDA tensors, reading
+    pointers and strides from the tensors' metadata.  The 8-bit calls
+    (``quantize``, ``add_rmsnorm_q``, ``gemm_q_nt``, ``gemm_q_fwd``,
+    ``mlp_q_fwd``) take float8_e4m3fn tensors with float32 scales.
 """
 from __future__ import annotations
 
@@ -36,7 +38,7 @@ EXPORTS = ("glu_fwd", "glu_bwd", "glu_fwd_host", "glu_bwd_host", "glu_fwd_host_n
            "glu_gemm_nt", "glu_mlp_fwd", "glu_mlp_workspace_bytes",
            "glu_add_rmsnorm_fwd", "glu_add_rmsnorm_bwd",
            "glu_quantize", "glu_add_rmsnorm_q", "glu_gemm_q_nt", "glu_gemm_q_fwd", "glu_gemm_q_grouped_nt",
-           "glu_gemm_q_grouped_fwd")
+           "glu_gemm_q_grouped_fwd", "glu_mlp_q_fwd", "glu_mlp_q_workspace_bytes")
 
 
 class GluError(RuntimeError):
@@ -144,6 +146,11 @@ def lib() -> ctypes.CDLL:
             L.glu_gemm_q_grouped_fwd.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, vp, vp, i64, i64, vp, i64, vp,
                                                  i64, i64, i64, i64, vp, i64, ci, vp]
             L.glu_gemm_q_grouped_fwd.restype = ci
+            L.glu_mlp_q_fwd.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, vp, vp, i64, i64, vp, i64, i64, vp, i64,
+                                        i64, vp, i64, i64, i64, i64, vp, i64, ci, ci, vp, sz, vp]
+            L.glu_mlp_q_fwd.restype = ci
+            L.glu_mlp_q_workspace_bytes.argtypes = [i64, i64]
+            L.glu_mlp_q_workspace_bytes.restype = sz
             _lib = L
     return _lib
 
@@ -295,6 +302,20 @@ def glu_gemm_q_grouped_fwd(x, x_stride, x_scale, x_scale_stride, w_gate, w_up, w
     return lib().glu_gemm_q_grouped_fwd(x, x_stride, x_scale, x_scale_stride, w_gate, w_up, w_stride, w_group,
                                         gate_scale, up_scale, w_scale_stride, w_scale_group, y, y_stride, y_scale,
                                         y_scale_stride, M, K, I, offsets, n_groups, act, stream)
+
+
+def glu_mlp_q_fwd(x, x_stride, x_scale, x_scale_stride, w_gate, w_up, w_stride, w_group, gate_scale, up_scale,
+                  w_scale_stride, w_scale_group, w_down, w_down_stride, w_down_group, down_scale, down_scale_stride,
+                  down_scale_group, out, out_stride, M, H, I, offsets, n_groups, act, dtype, workspace,
+                  workspace_bytes, stream) -> int:
+    return lib().glu_mlp_q_fwd(x, x_stride, x_scale, x_scale_stride, w_gate, w_up, w_stride, w_group, gate_scale,
+                               up_scale, w_scale_stride, w_scale_group, w_down, w_down_stride, w_down_group,
+                               down_scale, down_scale_stride, down_scale_group, out, out_stride, M, H, I, offsets,
+                               n_groups, act, dtype, workspace, workspace_bytes, stream)
+
+
+def glu_mlp_q_workspace_bytes(M, I) -> int:
+    return lib().glu_mlp_q_workspace_bytes(M, I)
 
 
 def glu_get_tuning() -> dict:
@@ -782,6 +803,44 @@ def gemm_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, y=None, y_scal
     if st:
         raise GluError(st, "glu_gemm_q_fwd" if offsets is None else "glu_gemm_q_grouped_fwd")
     return y, y_scale
+
+
+def mlp_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, *, out=None, dtype=None,
+              act: str = "silu", offsets=None, workspace=None, stream=None):
+    """out = y @ w_down^T with y = act(x @ w_gate^T) * (x @ w_up^T) quantised by
+    rows: gemm_q_fwd and gemm_q_nt through a workspace (a uint8 device tensor of
+    glu_mlp_q_workspace_bytes(rows, I) bytes, allocated here when not given).
+    x is (..., H), the gate and up weights (I, H), the down weights (H, I); with
+    ``offsets`` (E, I, H) and (E, H, I) (see gemm_q_nt)."""
+    import torch
+    grouped = offsets is not None
+    dev = _same_device(x, x_scale, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, out, offsets, workspace)
+    n_rows, x_stride, xs_stride, H = _in_q(x, x_scale, "x")
+    gate = _weight_q(w_gate, gate_scale, H, "w_gate", grouped)
+    if w_up.shape != w_gate.shape or _weight_q(w_up, up_scale, H, "w_up", grouped) != gate:
+        raise ValueError("w_gate and w_up (and their scales) must have one shape and one stride")
+    I, w_stride, w_group, s_stride, s_group = gate
+    N, d_stride, d_group, ds_stride, ds_group = _weight_q(w_down, down_scale, I, "w_down", grouped)
+    if N != H or (grouped and w_down.shape[0] != w_gate.shape[0]):
+        raise ValueError("w_down must be (H, I), for as many experts as w_gate")
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype or torch.bfloat16, device=x.device)
+    elif out.shape != x.shape or (dtype is not None and out.dtype != dtype):
+        raise ValueError("out has the wrong shape or dtype")
+    if workspace is None:
+        workspace = torch.empty(max(16, glu_mlp_q_workspace_bytes(max(n_rows, 1), max(I, 1))), dtype=torch.uint8,
+                                device=x.device)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    st = glu_mlp_q_fwd(x.data_ptr(), x_stride, x_scale.data_ptr(), xs_stride, w_gate.data_ptr(), w_up.data_ptr(),
+                       w_stride, w_group, gate_scale.data_ptr(), up_scale.data_ptr(), s_stride, s_group,
+                       w_down.data_ptr(), d_stride, d_group, down_scale.data_ptr(), ds_stride, ds_group,
+                       out.data_ptr(), _mat(out, "out")[1], n_rows, H, I,
+                       _offsets(offsets, w_gate) if grouped else None, w_gate.shape[0] if grouped else 0, ACT[act],
+                       _dtype_code(out), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    if st:
+        raise GluError(st, "glu_mlp_q_fwd")
+    return out
 
 
 # ---- host tensors ---------------------------------------------------------------

@@ -15,9 +15,12 @@ from torch import nn
 
 from . import add_rmsnorm as _add_rmsnorm
 from . import add_rmsnorm_bwd as _add_rmsnorm_bwd
+from . import add_rmsnorm_q as _add_rmsnorm_q
 from . import bwd as _bwd
 from . import fwd as _fwd
 from . import gemm_fwd as _gemm_fwd
+from . import mlp_q_fwd as _mlp_q_fwd
+from . import quantize as _quantize
 
 ACTS = ("silu", "gelu_erf", "gelu_tanh", "relu")
 
@@ -158,6 +161,43 @@ class GatedMLP(nn.Module):
         return self.down_proj(h)
 
 
+class QuantGatedMLP(nn.Module):
+    """A gated MLP in 8-bit floating point for inference: e4m3 weights with a
+    scale for each 128 x 128 block, held as buffers, and activations quantised by
+    rows.  ``from_mlp`` quantises a GatedMLP; ``from_mlps`` several into the
+    experts of one module, whose forward takes the rows sorted by expert and
+    their offsets."""
+
+    def __init__(self, gate, up, down, act: str = "silu", dtype=torch.bfloat16):
+        super().__init__()
+        self.act, self.dtype = _check_act(act), dtype
+        for name, w in (("gate", gate), ("up", up), ("down", down)):
+            # rows on 16-byte boundaries, the products' rule: quantize lays them out so
+            q, s = _quantize(w.detach(), block_rows=128)
+            self.register_buffer(f"{name}_weight", q)
+            self.register_buffer(f"{name}_scale", s)
+
+    @classmethod
+    def from_mlp(cls, mlp: GatedMLP):
+        gate, up = mlp._gate_up_weights()
+        return cls(gate, up, mlp.down_proj.weight, mlp.act, mlp.down_proj.weight.dtype)
+
+    @classmethod
+    def from_mlps(cls, mlps):
+        gates, ups = zip(*(m._gate_up_weights() for m in mlps))
+        down = [m.down_proj.weight for m in mlps]
+        return cls(torch.stack(gates), torch.stack(ups), torch.stack(down), mlps[0].act, down[0].dtype)
+
+    @torch.no_grad()
+    def forward(self, x, scale=None, offsets=None):
+        """x in any float type, or already quantised by rows with its scales (as
+        FusedAddRMSNorm.quantized returns it)."""
+        if scale is None:
+            x, scale = _quantize(x)
+        return _mlp_q_fwd(x, scale, self.gate_weight, self.gate_scale, self.up_weight, self.up_scale,
+                          self.down_weight, self.down_scale, dtype=self.dtype, act=self.act, offsets=offsets)
+
+
 class AddRMSNormFunction(torch.autograd.Function):
     """(h, y) = (x + residual, rmsnorm(x + residual) * gamma) in one pass
     ("Skill: Write a Triton Fused Add+RMSNorm Kernel", Purpose; steps 9-10 for
@@ -196,6 +236,12 @@ class FusedAddRMSNorm(nn.Module):
 
     def forward(self, x, residual):
         return AddRMSNormFunction.apply(x, residual, self.weight, self.eps)
+
+    @torch.no_grad()
+    def quantized(self, x, residual):
+        """(h, q, scale): forward with its result quantised by rows, for an
+        8-bit MLP behind it.  Inference only."""
+        return _add_rmsnorm_q(x, residual, self.weight, self.eps)
 
     def extra_repr(self):
         return f"{self.weight.shape[0]}, eps={self.eps}"

@@ -1262,6 +1262,19 @@ int validate(Args &x, bool *empty)
     return GLU_OK;
 }
 
+// The operands of the tensor-memory accelerator are in device memory.
+int check_device(const Args &x)
+{
+    for (const void *q : {x.a, x.w0, x.w1 == x.w0 ? nullptr : x.w1, static_cast<const void *>(x.y)}) {
+        bool dev_mem = false;
+        if (!q || (x.K == 0 && q != x.y)) continue;
+        const cudaError_t pe = glu::on_device(q, &dev_mem);
+        if (pe != cudaSuccess) return glu::cuda_fail(pe);
+        if (!dev_mem) return GLU_ERR_VALUE;
+    }
+    return GLU_OK;
+}
+
 int run(Args x, glu_stream_t stream)
 {
     bool empty = false;
@@ -1273,14 +1286,7 @@ int run(Args x, glu_stream_t stream)
     const bool plain = x.out >= kOutF16, grouped = x.groups > 0;
     const int E = plain ? 2 : 1;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    for (const void *q : {x.a, x.w0, x.w1, static_cast<const void *>(x.y)}) {
-        bool dev_mem = false;
-        if (x.K == 0 && q != x.y) continue;
-        if (q == x.w1 && x.w1 == x.w0) continue;
-        const cudaError_t pe = glu::on_device(q, &dev_mem);
-        if (pe != cudaSuccess) return glu::cuda_fail(pe);
-        if (!dev_mem) return GLU_ERR_VALUE;
-    }
+    if (int st = check_device(x)) return st;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -1474,4 +1480,70 @@ extern "C" int glu_gemm_q_grouped_fwd(const void *x, int64_t x_stride, const flo
                 w_scale_stride, w_scale_group, y, y_stride, y_scale, y_scale_stride, M, K, I, offsets, n_groups,
                 int(act)},
                stream);
+}
+
+// ---------------------------------------------------------------- the gated MLP
+
+namespace glu {
+namespace gemmq {
+namespace {
+
+int64_t round_up16(int64_t v) { return (v + 15) / 16 * 16; }
+
+}  // namespace
+}  // namespace gemmq
+}  // namespace glu
+
+extern "C" size_t glu_mlp_q_workspace_bytes(int64_t M, int64_t I)
+{
+    using namespace glu::gemmq;
+    if (M <= 0 || I <= 0 || M > INT32_MAX || I > INT32_MAX) return 0;
+    return size_t(M) * size_t(round_up16(I) + (I + glu::quant::kBlock - 1) / glu::quant::kBlock * 4);
+}
+
+extern "C" int glu_mlp_q_fwd(const void *x, int64_t x_stride, const float *x_scale, int64_t x_scale_stride,
+                             const void *w_gate, const void *w_up, int64_t w_stride, int64_t w_group,
+                             const float *gate_scale, const float *up_scale, int64_t w_scale_stride,
+                             int64_t w_scale_group, const void *w_down, int64_t w_down_stride, int64_t w_down_group,
+                             const float *down_scale, int64_t down_scale_stride, int64_t down_scale_group, void *out,
+                             int64_t out_stride, int64_t M, int64_t H, int64_t I, const int32_t *offsets,
+                             int64_t n_groups, glu_act_t act, glu_dtype_t dtype, void *workspace,
+                             size_t workspace_bytes, glu_stream_t stream)
+{
+    using namespace glu::gemmq;
+    if (act < GLU_ACT_SILU || act > GLU_ACT_RELU || (dtype != GLU_F16 && dtype != GLU_BF16)) return GLU_ERR_ENUM;
+    if (!offsets) n_groups = 0;
+    if (M < 0 || H < 0 || I < 0 || M > INT32_MAX || I > INT32_MAX) return GLU_ERR_SHAPE;
+    if (M > 0 && H > 0 && I > 0) {
+        if (!workspace || workspace_bytes < glu_mlp_q_workspace_bytes(M, I)) return GLU_ERR_WORKSPACE;
+        if (uintptr_t(workspace) % 16) return GLU_ERR_STRIDE;
+    }
+    // the workspace: y's rows of round_up(I, 16) bytes, then its scales
+    const int64_t ys = round_up16(I), groups = (I + glu::quant::kBlock - 1) / glu::quant::kBlock;
+    float *y_scale = I > 0 && workspace ? reinterpret_cast<float *>(static_cast<char *>(workspace) + M * ys) : nullptr;
+    Args up{x, x_stride, x_scale, x_scale_stride, w_gate, w_up, w_stride, w_group, gate_scale, up_scale,
+            w_scale_stride, w_scale_group, workspace, ys, y_scale, groups, M, H, I, offsets, n_groups, int(act)};
+    Args down{workspace, ys, y_scale, groups, w_down, w_down, w_down_stride, w_down_group, down_scale, down_scale,
+              down_scale_stride, down_scale_group, out, out_stride, nullptr, 0, M, I, H, offsets, n_groups,
+              dtype == GLU_F16 ? kOutF16 : kOutBF16};
+    if (H == 0) up.M = down.M = 0;
+    // both calls are checked before the first launch
+    Args cu = up, cd = down;
+    bool empty = false;
+    if (I > 0)
+        if (int st = validate(cu, &empty)) return st;
+    if (int st = validate(cd, &empty)) return st;
+    if (!empty) {
+        glu::Span so{}, sx{}, ss{};
+        if (!glu::span(out, M, cd.y_stride, H, 2, &so) || !glu::span(x, I > 0 ? M : 0, cu.a_stride, H, 1, &sx) ||
+            !glu::span(x_scale, I > 0 ? M : 0, cu.sa_stride, (H + 127) / 128, 4, &ss))
+            return GLU_ERR_SHAPE;
+        if (glu::overlap(so, sx) || glu::overlap(so, ss)) return GLU_ERR_ALIAS;
+        if (I > 0)
+            if (int st = check_device(cu)) return st;
+        if (int st = check_device(cd)) return st;
+        if (I > 0)
+            if (int st = run(up, stream)) return st;
+    }
+    return run(down, stream);
 }

@@ -26,7 +26,7 @@
  *     (cudaHostAlloc, cudaHostRegister) is device memory in this sense: the
  *     kernels then read and write it in place over the host link (zero-copy),
  *     except the operands of the tensor-core entry points (glu_gemm_fwd,
- *     glu_gemm_nt, glu_mlp_fwd) and glu_add_rmsnorm_bwd's dgamma, which must
+ *     glu_gemm_nt, glu_mlp_fwd, glu_gemm_q_*, glu_mlp_q_fwd) and glu_add_rmsnorm_bwd's dgamma, which must
  *     be in device memory.
  *   - Matrices are row-major with a contiguous last dimension: element (r, c)
  *     of operand X is at X + r * X_stride + c.  Strides are in ELEMENTS of
@@ -652,6 +652,37 @@ int glu_gemm_q_grouped_fwd(const void *x, int64_t x_stride, const float *x_scale
                            int64_t M, int64_t K, int64_t I,
                            const int32_t *offsets, int64_t n_groups,
                            glu_act_t act, glu_stream_t stream);
+
+/*
+ * The gated MLP on quantised matrices: glu_gemm_q_fwd into the workspace, then
+ * glu_gemm_q_nt from it (two launches on `stream`),
+ *
+ *     y, y_scale = quantised (act(x . w_gate) * (x . w_up)),   out = round(y . w_down)
+ *
+ *   x, x_scale             M x H; w_gate, w_up I x H; w_down H x I; out M x H
+ *                          of `dtype` (GLU_F16 or GLU_BF16).
+ *   offsets, n_groups      NULL and anything: one MLP (the *_group strides are
+ *                          then ignored).  Else by expert, as in
+ *                          glu_gemm_q_grouped_nt.
+ *   workspace              device memory for y and its scales, 16-byte aligned,
+ *                          at least glu_mlp_q_workspace_bytes(M, I) bytes, else
+ *                          GLU_ERR_WORKSPACE.
+ * Every argument is checked before the first launch; out overlaps nothing.
+ * M == 0 or H == 0: no work; I == 0: out = 0.
+ */
+int glu_mlp_q_fwd(const void *x, int64_t x_stride, const float *x_scale, int64_t x_scale_stride,
+                  const void *w_gate, const void *w_up, int64_t w_stride, int64_t w_group,
+                  const float *gate_scale, const float *up_scale, int64_t w_scale_stride, int64_t w_scale_group,
+                  const void *w_down, int64_t w_down_stride, int64_t w_down_group,
+                  const float *down_scale, int64_t down_scale_stride, int64_t down_scale_group,
+                  void *out, int64_t out_stride,
+                  int64_t M, int64_t H, int64_t I,
+                  const int32_t *offsets, int64_t n_groups,
+                  glu_act_t act, glu_dtype_t dtype,
+                  void *workspace, size_t workspace_bytes, glu_stream_t stream);
+
+/* M * (round_up(I, 16) + 4 * ceil(I / 128)); 0 for invalid arguments. */
+size_t glu_mlp_q_workspace_bytes(int64_t M, int64_t I);
 
 #ifdef __cplusplus
 }
