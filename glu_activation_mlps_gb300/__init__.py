@@ -619,28 +619,31 @@ def _mat(t, name):
     return _rows(t, name)
 
 
-def _empty_q(shape, like):
-    """An e4m3 tensor whose rows start on 16-byte boundaries (the products'
-    rule): the last dimension of a wider tensor where it is no multiple of 16."""
+def _out_q(q, scale, shape, lead, like, name):
+    """(q, scale, row stride of q, row stride of scale) of a result of the given
+    shape (``lead``: its leading dimensions) quantised by rows.  What is None is
+    allocated, q with rows on 16-byte boundaries (the products' rule)."""
     import torch
     n = shape[-1]
-    if n % 16 == 0:
-        return torch.empty(shape, dtype=torch.float8_e4m3fn, device=like.device)
-    return torch.empty((*shape[:-1], n + -n % 16), dtype=torch.float8_e4m3fn, device=like.device)[..., :n]
-
-
-def _out_q(q, scale, shape, scale_shape, like, name):
-    """q and its scales, allocated where they are None, else checked."""
-    import torch
+    groups = (n + 127) // 128
     if q is None:
-        q = _empty_q(shape, like)
+        q_stride = n + -n % 16
+        if q_stride == n:
+            q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=like.device)
+        elif len(shape) == 2:
+            q = torch.empty_strided(shape, (q_stride, 1), dtype=torch.float8_e4m3fn, device=like.device)
+        else:
+            q = torch.empty((*lead, q_stride), dtype=torch.float8_e4m3fn, device=like.device)[..., :n]
     elif q.dtype != torch.float8_e4m3fn or q.shape != shape:
         raise ValueError(f"{name} must be float8_e4m3fn of shape {tuple(shape)}")
+    else:
+        q_stride = _mat(q, name)[1]
     if scale is None:
-        scale = torch.empty(scale_shape, dtype=torch.float32, device=like.device)
-    elif scale.dtype != torch.float32 or scale.shape != scale_shape:
-        raise ValueError(f"{name}'s scales must be float32 of shape {tuple(scale_shape)}")
-    return q, scale
+        scale = torch.empty((*lead, groups), dtype=torch.float32, device=like.device)
+        return q, scale, q_stride, groups
+    if scale.dtype != torch.float32 or scale.shape != (*lead, groups):
+        raise ValueError(f"{name}'s scales must be float32 of shape {(*lead, groups)}")
+    return q, scale, q_stride, _mat(scale, name)[1]
 
 
 def _in_q(q, scale, name):
@@ -686,24 +689,39 @@ def quantize(x, *, block_rows: int = 1, q=None, scale=None, stream=None):
     scale (..., ceil(K / 128))), or of 128 rows (128, weights; x is (N, K), or
     (E, N, K) for the weights of E experts, and scale (.., ceil(N / 128),
     ceil(K / 128)))."""
-    if block_rows != 1 and block_rows != 128:
-        raise ValueError("block_rows must be 1 or 128")
+    import torch
     code = _dtype_code(x)
     shape = x.shape
-    if block_rows == 128:
-        if len(shape) not in (2, 3):
-            raise ValueError("x must be (N, K) or (E, N, K) for 128 x 128 blocks")
-        blocks = (*shape[:-2], (shape[-2] + 127) // 128, (shape[-1] + 127) // 128)
-    else:
-        blocks = (*shape[:-1], (shape[-1] + 127) // 128)
     dev = _same_device(x, q, scale)
-    q, scale = _out_q(q, scale, shape, blocks, x, "q")
     s = _raw_stream(stream, dev)
-    parts = ((x, q, scale),) if len(shape) < 3 or block_rows == 1 else zip(x, q, scale)
-    for xe, qe, se in parts:
+    if block_rows == 1:
+        n_rows, x_stride = _mat(x, "x")
+        q, scale, q_stride, s_stride = _out_q(q, scale, shape, shape[:-1], x, "q")
+        st = glu_quantize(x.data_ptr(), x_stride, q.data_ptr(), q_stride, scale.data_ptr(), s_stride, n_rows,
+                          shape[-1], 1, code, s)
+        if st:
+            raise GluError(st, "glu_quantize")
+        return q, scale
+    if block_rows != 128:
+        raise ValueError("block_rows must be 1 or 128")
+    if len(shape) not in (2, 3):
+        raise ValueError("x must be (N, K) or (E, N, K) for 128 x 128 blocks")
+    K = shape[-1]
+    blocks = (*shape[:-2], (shape[-2] + 127) // 128, (K + 127) // 128)
+    if scale is None:
+        scale = torch.empty(blocks, dtype=torch.float32, device=x.device)
+    elif scale.dtype != torch.float32 or scale.shape != blocks:
+        raise ValueError(f"q's scales must be float32 of shape {blocks}")
+    if q is None:
+        wide = K + -K % 16              # rows on 16-byte boundaries, the products' rule
+        strides = (wide, 1) if len(shape) == 2 else (shape[1] * wide, wide, 1)
+        q = torch.empty_strided(shape, strides, dtype=torch.float8_e4m3fn, device=x.device)
+    elif q.dtype != torch.float8_e4m3fn or q.shape != shape:
+        raise ValueError(f"q must be float8_e4m3fn of shape {tuple(shape)}")
+    for xe, qe, se in (((x, q, scale),) if len(shape) == 2 else zip(x, q, scale)):
         n_rows, x_stride = _mat(xe, "x")
         st = glu_quantize(xe.data_ptr(), x_stride, qe.data_ptr(), _mat(qe, "q")[1], se.data_ptr(),
-                          _mat(se, "scale")[1], n_rows, shape[-1], block_rows, code, s)
+                          _mat(se, "scale")[1], n_rows, K, 128, code, s)
         if st:
             raise GluError(st, "glu_quantize")
     return q, scale
@@ -726,22 +744,25 @@ def add_rmsnorm_q(x, residual, gamma, eps: float = 1e-5, *, h=None, q=None, scal
     n_rows, x_stride = _mat(x, "x")
     r_stride = _mat(residual, "residual")[1]
     if h is None:
-        h = torch.empty(shape, dtype=dtype, device=x.device)
+        h, h_stride = torch.empty(shape, dtype=dtype, device=x.device), H
     elif h.shape != shape or h.dtype != dtype:
         raise ValueError("h must match x in shape and dtype")
-    q, scale = _out_q(q, scale, shape, (*shape[:-1], (H + 127) // 128), x, "q")
-    want_rstd = rstd is not None and rstd is not False
-    if rstd is True:
+    else:
+        h_stride = _mat(h, "h")[1]
+    q, scale, q_stride, s_stride = _out_q(q, scale, shape, shape[:-1], x, "q")
+    if rstd is None or rstd is False:
+        rstd = None
+    elif rstd is True:
         rstd = torch.empty(n_rows, dtype=torch.float32, device=x.device)
-    if want_rstd and (rstd.dtype != torch.float32 or rstd.numel() != n_rows or not rstd.is_contiguous() or
-                      rstd.get_device() != dev):
+    elif (rstd.dtype != torch.float32 or rstd.numel() != n_rows or not rstd.is_contiguous() or
+          rstd.get_device() != dev):
         raise ValueError("rstd must be a contiguous float32 tensor with one entry per row")
     st = glu_add_rmsnorm_q(x.data_ptr(), x_stride, residual.data_ptr(), r_stride, gamma.data_ptr(), h.data_ptr(),
-                           _mat(h, "h")[1], q.data_ptr(), _mat(q, "q")[1], scale.data_ptr(), _mat(scale, "scale")[1],
-                           rstd.data_ptr() if want_rstd else None, n_rows, H, eps, code, _raw_stream(stream, dev))
+                           h_stride, q.data_ptr(), q_stride, scale.data_ptr(), s_stride,
+                           None if rstd is None else rstd.data_ptr(), n_rows, H, eps, code, _raw_stream(stream, dev))
     if st:
         raise GluError(st, "glu_add_rmsnorm_q")
-    return (h, q, scale, rstd) if want_rstd else (h, q, scale)
+    return (h, q, scale) if rstd is None else (h, q, scale, rstd)
 
 
 def gemm_q_nt(a, a_scale, b, b_scale, *, d=None, dtype=None, offsets=None, stream=None):
@@ -757,10 +778,11 @@ def gemm_q_nt(a, a_scale, b, b_scale, *, d=None, dtype=None, offsets=None, strea
     N, b_stride, b_group, bs_stride, bs_group = _weight_q(b, b_scale, K, "b", offsets is not None)
     shape = (*a.shape[:-1], N)
     if d is None:
-        d = torch.empty(shape, dtype=dtype or torch.bfloat16, device=a.device)
+        d, d_stride = torch.empty(shape, dtype=dtype or torch.bfloat16, device=a.device), N
     elif d.shape != shape or (dtype is not None and d.dtype != dtype):
         raise ValueError("d has the wrong shape or dtype")
-    d_stride = _mat(d, "d")[1]
+    else:
+        d_stride = _mat(d, "d")[1]
     code = _dtype_code(d)
     s = _raw_stream(stream, dev)
     if offsets is None:
@@ -788,8 +810,7 @@ def gemm_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, y=None, y_scal
         raise ValueError("w_gate and w_up (and their scales) must have one shape and one stride")
     N, w_stride, w_group, s_stride, s_group = gate
     lead = x.shape[:-1]
-    y, y_scale = _out_q(y, y_scale, (*lead, N), (*lead, (N + 127) // 128), x, "y")
-    y_stride, ys_stride = _mat(y, "y")[1], _mat(y_scale, "y_scale")[1]
+    y, y_scale, y_stride, ys_stride = _out_q(y, y_scale, (*lead, N), lead, x, "y")
     s = _raw_stream(stream, dev)
     if offsets is None:
         st = glu_gemm_q_fwd(x.data_ptr(), x_stride, x_scale.data_ptr(), xs_stride, w_gate.data_ptr(), w_up.data_ptr(),
