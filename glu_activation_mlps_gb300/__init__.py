@@ -610,6 +610,16 @@ def _raw_stream(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
+def _used_on(stream, *tensors):
+    """Tells the allocator that tensors it gave to the current stream are used
+    on another one, so that their memory is not given out again too early."""
+    import torch
+    if not isinstance(stream, torch.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream))
+    for t in tensors:
+        t.record_stream(stream)
+
+
 def _mat(t, name):
     """_rows of a CUDA tensor, quick for plain matrices."""
     if t.dim() == 2:
@@ -701,6 +711,8 @@ def quantize(x, *, block_rows: int = 1, q=None, scale=None, stream=None):
                           shape[-1], 1, code, s)
         if st:
             raise GluError(st, "glu_quantize")
+        if stream is not None:
+            _used_on(stream, q, scale)
         return q, scale
     if block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
@@ -724,6 +736,8 @@ def quantize(x, *, block_rows: int = 1, q=None, scale=None, stream=None):
                           _mat(se, "scale")[1], n_rows, K, 128, code, s)
         if st:
             raise GluError(st, "glu_quantize")
+    if stream is not None:
+        _used_on(stream, q, scale)
     return q, scale
 
 
@@ -762,6 +776,10 @@ def add_rmsnorm_q(x, residual, gamma, eps: float = 1e-5, *, h=None, q=None, scal
                            None if rstd is None else rstd.data_ptr(), n_rows, H, eps, code, _raw_stream(stream, dev))
     if st:
         raise GluError(st, "glu_add_rmsnorm_q")
+    if stream is not None:
+        _used_on(stream, h, q, scale)
+        if rstd is not None:
+            _used_on(stream, rstd)
     return (h, q, scale) if rstd is None else (h, q, scale, rstd)
 
 
@@ -794,6 +812,8 @@ def gemm_q_nt(a, a_scale, b, b_scale, *, d=None, dtype=None, offsets=None, strea
                                    K, N, _offsets(offsets, b), b.shape[0], code, s)
     if st:
         raise GluError(st, "glu_gemm_q_nt" if offsets is None else "glu_gemm_q_grouped_nt")
+    if stream is not None:
+        _used_on(stream, d)
     return d
 
 
@@ -823,6 +843,8 @@ def gemm_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, y=None, y_scal
                                     K, N, _offsets(offsets, w_gate), w_gate.shape[0], ACT[act], s)
     if st:
         raise GluError(st, "glu_gemm_q_fwd" if offsets is None else "glu_gemm_q_grouped_fwd")
+    if stream is not None:
+        _used_on(stream, y, y_scale)
     return y, y_scale
 
 
@@ -861,6 +883,8 @@ def mlp_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, w_down, down_scale
                        _dtype_code(out), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if st:
         raise GluError(st, "glu_mlp_q_fwd")
+    if stream is not None:
+        _used_on(stream, out, workspace)
     return out
 
 

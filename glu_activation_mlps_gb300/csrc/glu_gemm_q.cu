@@ -164,14 +164,12 @@ __device__ __forceinline__ bool wait_quick(uint32_t bar, uint32_t parity)
 
 // Waits for this thread's tensor-memory loads; the registers pass through, so
 // that no use of them can be moved before the wait.
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+                   "+r"(r[15])::"memory");
 }
 
 // One lane of a converged warp.  The MMA warp runs its loop as a whole and only
@@ -186,6 +184,13 @@ __device__ __forceinline__ bool elect_one()
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(yes));
     return yes != 0;
+}
+
+__device__ __forceinline__ float ld_shared(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ float ld_cluster(uint32_t addr)
@@ -297,18 +302,20 @@ struct Plain {};
 
 // Warp 0 loads, warp 1 issues MMAs, warps 2-3 prepare scales, warps 4-11 sum
 // and store.  Launched with 168 registers a thread (64512 a block); the first
-// four warps give theirs up to the summing ones: 128 * 88 + 256 * 208 = 64512.
+// four warps give some up to the summing ones, which then spill nothing: 128 *
+// 152 + 256 * 176 = 64512.
 constexpr int kWideThreads = 384;
 constexpr int kWideEpi = 8;
 constexpr int kChunk = 8;           // K blocks whose scales are prepared at once (32 bytes of a row's)
-constexpr int kChunks = 3;
+constexpr int kChunks = 2;
 
 struct Wide {
     static constexpr int N = 256;                           // columns of one tile's sums: two halves of 128
     static constexpr int kTileA = BM * BK;
     static constexpr int kTileB = N / 2 * BK;
     static constexpr int kStageBytes = kTileA + kTileB;
-    static constexpr int kStages = 5;
+    // (a fifth stage measured level)
+    static constexpr int kStages = 4;
     static constexpr int kCols = N;                         // one of two buffers of tensor memory
     static constexpr int kStageY = kWideEpi * 2 * kBox * 64;
     static constexpr int kBars = 2 * kStages + 2 + 2 * kChunks + 1 + 4;
@@ -325,7 +332,7 @@ struct Wide {
 // a gate and an up block (y is quantised, T is unused).
 // Warps 2-3 fetch the row scales eight K blocks at a time (32 bytes of a row),
 // multiply them by the two weight scales and leave the products in shared
-// memory, three chunks ahead: loaded by the summing threads one K block ahead,
+// memory, two chunks ahead: loaded by the summing threads one K block ahead,
 // their latency was the bound (0.70 PFLOP/s at 4096 x 4096 x 2 x 14336).
 template <class Act, class T>
 __global__ void __launch_bounds__(kWideThreads, 1)
@@ -399,7 +406,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int n_tiles = prefix[p.n_groups] * p.n_blocks;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
         if (warp == 0 && lane == 0) {
             uint32_t it = 0;
             for (int t = cluster; t < n_tiles && !*abort_flag; t += n_clusters) {
@@ -522,70 +529,66 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         // warp w reads lanes 32 (w % 4) .. +31, one row per thread; warps 4-7
         // take the first 64 columns of either half, warps 8-11 the others
         const int q = warp & 3, part = (warp - 4) >> 2;
         const uint32_t lane_base = uint32_t(q * 32) << 16;
         const uint32_t empty0 = mapa(saddr(&acc_empty[0]), 0);
-        uint32_t it = 0, st = 0, phase = 0, cc = 0, n_boxes = 0;
+        const uint32_t sc0 = saddr(scales) + uint32_t(q * 32 + lane) * 4;
+        uint32_t it = 0, cc = 0, n_boxes = 0;
         int lt = 0;
         bool ok = true;
         for (int t = cluster; t < n_tiles && ok; t += n_clusters, ++lt) {
-            const Tile tl = tile_at(p, prefix, t, 2 * BM);
-            const int base = tl.row + int(rank) * BM + q * 32;
-            const int m = base + lane;
-            const bool on = m < tl.end;
+            // The K loop needs no more than the sums, two times 16 columns on
+            // their way and a few counters (with 32 at a time registers were
+            // spilled, whose loads were a third of the stalls: 213 us instead of
+            // 192 at 4096 x 14336 x 4096); which rows and columns these are is
+            // asked behind it.
             f2 acc[2][32];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) acc[h][j] = make_float2(0.0f, 0.0f);
-            for (int kt = 0; kt < p.k_tiles && ok; ++kt, ++it) {
-                const uint32_t slot = cc % kChunks;
-                if (kt % kChunk == 0) ok = wait_parity(saddr(&sc_full[slot]), (cc / kChunks) & 1);
-                const float *sc = scales + (slot * kChunk + uint32_t(kt % kChunk)) * (2 * BM) + q * 32 + lane;
-                const float sc0 = sc[0], sc1 = sc[BM];
+            for (int kt = 0; kt < p.k_tiles; ++kt, ++it) {
+                if (kt % kChunk == 0) ok = wait_quick(saddr(&sc_full[cc % kChunks]), (cc / kChunks) & 1);
+                const uint32_t sc = sc0 + ((cc % kChunks) * kChunk + uint32_t(kt % kChunk)) * (2 * BM * 4);
+                const float f0 = ld_shared(sc), f1 = ld_shared(sc + BM * 4);
                 if (kt % kChunk == kChunk - 1 || kt + 1 == p.k_tiles) {     // this chunk read
                     __syncwarp();
-                    if (lane == 0) arrive_local(saddr(&sc_empty[slot]));
+                    if (lane == 0) arrive_local(saddr(&sc_empty[cc % kChunks]));
                     ++cc;
                 }
-                const uint32_t ab = it & 1;
-                ok = __all_sync(0xFFFFFFFFu, ok && wait_quick(saddr(&used[st]), phase));
-                if (++st == ST) {
-                    st = 0;
-                    phase ^= 1;
-                }
+                ok = __all_sync(0xFFFFFFFFu, ok && wait_quick(saddr(&used[it % ST]), (it / ST) & 1));
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 if (!ok) {
                     if (lane == 0) raise_abort();
                     break;
                 }
-                // 32 columns are multiplied while the next 32 are on their way
-                const uint32_t a0 = tmem + lane_base + ab * S::kCols + uint32_t(part * 64);
-                const f2 f0 = splat(sc0), f1 = splat(sc1);
-                uint32_t r0[32], r1[32];
-                const auto add = [](f2 (&a)[32], int at, const uint32_t (&r)[32], f2 f) {
+                // 16 columns are multiplied while the next 16 are on their way
+                const uint32_t a0 = tmem + lane_base + (it & 1) * S::kCols + uint32_t(part * 64);
+                uint32_t r[2][16];
+                const auto add = [](f2 (&a)[32], int at, const uint32_t (&r)[16], float f) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) a[at + j] = fma2(pair(r[2 * j], r[2 * j + 1]), f, a[at + j]);
+                    for (int j = 0; j < 8; ++j) a[at + j] = fma2(pair(r[2 * j], r[2 * j + 1]), splat(f), a[at + j]);
                 };
-                tmem_ld32(a0, r0);
-                tmem_wait(r0);
-                tmem_ld32(a0 + 32, r1);
-                add(acc[0], 0, r0, f0);
-                tmem_wait(r1);
-                tmem_ld32(a0 + 128, r0);
-                add(acc[0], 16, r1, f0);
-                tmem_wait(r0);
-                tmem_ld32(a0 + 160, r1);
-                add(acc[1], 0, r0, f1);
-                tmem_wait(r1);
+                tmem_ld16(a0, r[0]);
+#pragma unroll
+                for (int c = 0; c < 7; ++c) {
+                    tmem_wait(r[c & 1]);
+                    tmem_ld16(a0 + uint32_t((c + 1) / 4 * 128 + (c + 1) % 4 * 16), r[(c + 1) & 1]);
+                    add(acc[c / 4], c % 4 * 8, r[c & 1], c < 4 ? f0 : f1);
+                }
+                tmem_wait(r[1]);
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                if (elect_one()) arrive_pair(empty0 + 8 * ab);
-                add(acc[1], 16, r1, f1);
+                if (elect_one()) arrive_pair(empty0 + 8 * (it & 1));
+                add(acc[1], 24, r[1], f1);
             }
             if (!ok || __any_sync(0xFFFFFFFFu, *abort_flag != 0)) break;
+            const Tile tl = tile_at(p, prefix, t, 2 * BM);
+            const int base = tl.row + int(rank) * BM + q * 32;
+            const int m = base + lane;
+            const bool on = m < tl.end;
 
             // Each warp's 32 rows of 64 bytes go through shared memory.  They may
             // leave through the copy engine if all of them are this expert's,
@@ -953,8 +956,11 @@ __global__ void __launch_bounds__(kNarrowThreads)
                     for (int c = 0; c < NT; c += 16) {
                         uint32_t r0[16], r1[16];
                         tmem_ld16(a0 + uint32_t(c), r0);
-                        if constexpr (!kPlain) tmem_ld16(a0 + uint32_t(NT + c), r1);
-                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                        if constexpr (!kPlain) {
+                            tmem_ld16(a0 + uint32_t(NT + c), r1);
+                            tmem_wait(r1);
+                        }
+                        tmem_wait(r0);
                         if (c + 16 == NT) {
                             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                             __syncwarp();
@@ -1262,15 +1268,21 @@ int validate(Args &x, bool *empty)
     return GLU_OK;
 }
 
-// The operands of the tensor-memory accelerator are in device memory.
+// The operands of the tensor-memory accelerator are in the current device's
+// memory.
 int check_device(const Args &x)
 {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     for (const void *q : {x.a, x.w0, x.w1 == x.w0 ? nullptr : x.w1, static_cast<const void *>(x.y)}) {
-        bool dev_mem = false;
         if (!q || (x.K == 0 && q != x.y)) continue;
-        const cudaError_t pe = glu::on_device(q, &dev_mem);
-        if (pe != cudaSuccess) return glu::cuda_fail(pe);
-        if (!dev_mem) return GLU_ERR_VALUE;
+        cudaPointerAttributes at{};
+        if (e == cudaSuccess) e = cudaPointerGetAttributes(&at, q);
+        if (e != cudaSuccess) {
+            (void)cudaGetLastError();
+            return glu::cuda_fail(e);
+        }
+        if (at.type != cudaMemoryTypeDevice || at.device != dev) return GLU_ERR_VALUE;
     }
     return GLU_OK;
 }

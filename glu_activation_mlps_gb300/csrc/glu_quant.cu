@@ -471,7 +471,7 @@ extern "C" int glu_quantize(const void *x, int64_t x_stride, void *q, int64_t q_
     using namespace glu::quant;
     if (!(dtype == GLU_F32 || dtype == GLU_F16 || dtype == GLU_BF16)) return GLU_ERR_ENUM;
     if (block_rows != 1 && block_rows != kBlock) return GLU_ERR_VALUE;
-    if (n_rows < 0 || n_cols < 0 || n_cols > INT32_MAX - 4096) return GLU_ERR_SHAPE;
+    if (n_rows < 0 || n_cols < 0 || n_cols > (int64_t(1) << 28)) return GLU_ERR_SHAPE;
     if (n_rows == 0 || n_cols == 0) {
         glu::record_launch(glu_launch_info_t{});
         return GLU_OK;

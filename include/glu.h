@@ -550,6 +550,8 @@ int glu_add_rmsnorm_bwd(const void *dy, int64_t dy_stride,
  *   x, x_stride            n_rows x n_cols of `dtype` (any glu_dtype_t).
  *   q, q_stride            n_rows x n_cols e4m3 bytes, q_stride >= n_cols.
  *   scale, scale_stride    as above; scale_stride >= ceil(n_cols / 128).
+ *   n_rows, n_cols         n_cols <= 2^28; with block_rows = 128 at most 65535
+ *                          blocks of rows; else GLU_ERR_SHAPE.
  * One kernel on `stream`; glu_last_launch reports path = 10.  n_rows == 0 or
  * n_cols == 0: no work.
  */
@@ -591,7 +593,7 @@ int glu_add_rmsnorm_q(const void *x, int64_t x_stride,
  *   d, d_stride              M x N of `dtype`, GLU_F16 or GLU_BF16.
  * a and b: 16-byte aligned bases and row strides that are multiples of 16
  * (GLU_ERR_STRIDE; K itself may be any size, the bytes past it are not read
- * into the sums); a, b and d in device memory (GLU_ERR_VALUE).  M, K, N <
+ * into the sums); a, b and d in the current device's memory (GLU_ERR_VALUE).  M, K, N <
  * 2^31 - 65536.  M == 0 or N == 0: no work; K == 0: d = 0.  The result does not
  * depend on what else runs: sums are formed in a fixed order.
  * glu_last_launch reports path = 12 and unroll = blocks that share a tile.

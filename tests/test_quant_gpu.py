@@ -562,6 +562,33 @@ def test_a_block_on_a_side_stream_and_in_graphs(M):
     assert all(same(out) for _, out in graphs)
 
 
+def test_stream_argument():
+    """Calls given another stream: their results, and the workspace of the MLP,
+    are not handed out again while that stream still works."""
+    g = gen(17)
+    M, H, I = 64, 512, 700
+    x, sx = random_q(g, M, H, 1, 0.5)
+    wg, wu = (glu.quantize(randn(g, I, H) / H ** 0.5, block_rows=128) for _ in range(2))
+    wd = glu.quantize(randn(g, H, I) / I ** 0.5, block_rows=128)
+    want = glu.mlp_q_fwd(x, sx, *wg, *wu, *wd)
+    xb = randn(g, M, H).to(torch.bfloat16)
+    gamma = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    norm = glu.add_rmsnorm_q(xb, xb, gamma, rstd=True)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        outs = []
+        for _ in range(20):
+            outs.append(glu.mlp_q_fwd(x, sx, *wg, *wu, *wd, stream=stream))
+            torch.full((M * 1024,), 0x7F, dtype=torch.uint8, device="cuda")     # would land in a freed workspace
+        got = glu.add_rmsnorm_q(xb, xb, gamma, rstd=True, stream=stream)
+        q, s = glu.quantize(xb, stream=stream)
+        side.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, norm))
+        check_quantised(q, s, xb.double(), 1, 4 * U)
+
+
 def test_two_calls_at_once():
     """Products on two streams at the same time do not disturb each other."""
     g = gen(31)
