@@ -212,6 +212,33 @@ __device__ __forceinline__ f2 gated(f2 g, f2 u)
     return mul2(a, u);
 }
 
+// gated() of two pairs.  The sigmoid forms take one reciprocal for all four,
+// 1 / (1 + e) of each from that of their product (in [1, 16]): the special
+// functions, eight cycles a warp each, are what a gated tile's end waits for.
+template <class Act>
+__device__ __forceinline__ void gated4(f2 &g0, f2 u0, f2 &g1, f2 u1)
+{
+    if constexpr (std::is_same<Act, Silu>::value || std::is_same<Act, GeluTanh>::value) {
+        f2 w0 = g0, w1 = g1;
+        if constexpr (std::is_same<Act, GeluTanh>::value) {
+            w0 = GeluTanh::arg2(g0);
+            w1 = GeluTanh::arg2(g1);
+        }
+        const f2 e0 = exp2_twice(mul2(abs2(w0), splat(kNegHalfLog2e)));
+        const f2 e1 = exp2_twice(mul2(abs2(w1), splat(kNegHalfLog2e)));
+        const f2 d0 = add2(e0, splat(1.0f)), d1 = add2(e1, splat(1.0f));
+        const float p0 = d0.x * d0.y, p1 = d1.x * d1.y;
+        const float r = rcp_ftz(p0 * p1), r0 = r * p1, r1 = r * p0;
+        const f2 m0 = make_float2(w0.x >= 0.0f ? 1.0f : e0.x, w0.y >= 0.0f ? 1.0f : e0.y);
+        const f2 m1 = make_float2(w1.x >= 0.0f ? 1.0f : e1.x, w1.y >= 0.0f ? 1.0f : e1.y);
+        g0 = mul2(mul2(g0, mul2(m0, mul2(splat(r0), make_float2(d0.y, d0.x)))), u0);
+        g1 = mul2(mul2(g1, mul2(m1, mul2(splat(r1), make_float2(d1.y, d1.x)))), u1);
+    } else {
+        g0 = gated<Act>(g0, u0);
+        g1 = gated<Act>(g1, u1);
+    }
+}
+
 // ---------------------------------------------------------------- tiles
 
 // First and last row of group e, clamped to the matrix and to each other, so
@@ -646,9 +673,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 // y = act(gate) * up over this thread's 64 columns, and the row's maximum over both parts
                 float top = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    acc[0][j] = gated<Act>(acc[0][j], acc[1][j]);
-                    top = fmaxf(top, fmaxf(fabsf(acc[0][j].x), fabsf(acc[0][j].y)));
+                for (int j = 0; j < 32; j += 2) {
+                    gated4<Act>(acc[0][j], acc[1][j], acc[0][j + 1], acc[1][j + 1]);
+                    top = fmaxf(fmaxf(top, fmaxf(fabsf(acc[0][j].x), fabsf(acc[0][j].y))),
+                                fmaxf(fabsf(acc[0][j + 1].x), fabsf(acc[0][j + 1].y)));
                 }
                 float *mx = rowmax + (lt & 1) * 2 * BM + q * 32 + lane;
                 mx[part * BM] = top;
@@ -661,11 +689,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 }
                 top = fmaxf(top, mx[(part ^ 1) * BM]);
                 const quant::Divider d(top);
+                const f2 inv = splat(d.factor());
                 uint32_t w[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    w[j] = quant::pack4(d(acc[0][2 * j].x), d(acc[0][2 * j].y), d(acc[0][2 * j + 1].x),
-                                        d(acc[0][2 * j + 1].y));
+                for (int j = 0; j < 16; ++j) {
+                    const f2 a = mul2(acc[0][2 * j], inv), b = mul2(acc[0][2 * j + 1], inv);
+                    w[j] = quant::pack4(a.x, a.y, b.x, b.y);
+                }
                 if (on && part == 0) p.ys[int64_t(m) * p.ys_stride + tl.nb] = d.scale();
                 store_box(w, tl.nb * kOutCols + part * 64);
             }
@@ -893,7 +923,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
                 const int m = tl.row + j0 + j;
                 if (m >= tl.end) break;
                 const quant::Divider d(fmaxf(fmaxf(mx[j], mx[NT + j]), fmaxf(mx[2 * NT + j], mx[3 * NT + j])));
-                const float v = d(y[j]);
+                const float v = y[j] * d.factor();
                 if (c < p.N) p.y[int64_t(m) * p.y_stride + c] = char(quant::pack4(v, 0.0f, 0.0f, 0.0f) & 0xFFu);
                 if (q == 0 && lane == 0) p.ys[int64_t(m) * p.ys_stride + tl.nb] = d.scale();
             }
