@@ -202,8 +202,9 @@ __global__ void __launch_bounds__(512) add_rmsnorm_q_kernel(const NormParams p)
             m = fmaxf(m, fabsf(s[k][i]));
         }
         const Divider d(L::block_max(m));
+        const float f = d.factor();
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[k][i] = d(s[k][i]);
+        for (int i = 0; i < V; ++i) s[k][i] *= f;
         L::store_q(p.q + row * p.sq, c, H, s[k]);
         if (piece % L::kPer == 0 && c < H) p.scale[row * p.ss + piece / L::kPer] = d.scale();
     }
