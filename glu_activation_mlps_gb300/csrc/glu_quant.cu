@@ -44,9 +44,7 @@ struct Lanes {
     struct Raw {
         uint32_t w[kWords];
     };
-    // Values past the row are zeros.  Single elements past it read column 0
-    // instead (a load behind a branch is waited for before the next is issued);
-    // for whole pieces the branch measured faster.
+    // Values past the row are zeros (single elements past it read column 0).
     __device__ __forceinline__ static Raw load(const char *row, int col, int H)
     {
         Raw r;
@@ -58,21 +56,41 @@ struct Lanes {
                 for (int j = 0; j < kWords; ++j) r.w[j] = 0;    // zeros in every type
             }
         } else {
+            if (whole(col, H)) {
+                const char *p = row + int64_t(col) * sizeof(T);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const bool in = col + 32 * i < H;
-                const float f = C::load1(row + int64_t(in ? col + 32 * i : 0) * sizeof(T));
-                r.w[i] = in ? __float_as_uint(f) : 0u;
+                for (int i = 0; i < V; ++i) r.w[i] = bits(p + 32 * i * sizeof(T));
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const bool in = col + 32 * i < H;
+                    const uint32_t w = bits(row + int64_t(in ? col + 32 * i : 0) * sizeof(T));
+                    r.w[i] = in ? w : 0u;
+                }
             }
         }
         return r;
+    }
+    // Single elements: whether this warp's block of 128 columns lies inside the
+    // row (the usual case needs no test and one address for each piece) ...
+    __device__ __forceinline__ static bool whole(int col, int H) { return (col | (kBlock - 1)) < H; }
+    // ... and an element's bits, left to be converted where they are used (a
+    // conversion here would wait for the load).
+    __device__ __forceinline__ static uint32_t bits(const char *p)
+    {
+        uint32_t v;
+        if constexpr (sizeof(T) == 2)
+            asm volatile("ld.global.u16 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+        else
+            asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+        return v;
     }
     __device__ __forceinline__ static float get(const Raw &r, int i)
     {
         if constexpr (VEC)
             return C::get(r.w[i / C::kPerWord], i % C::kPerWord);
         else
-            return __uint_as_float(r.w[i]);
+            return C::get(r.w[i], 0);
     }
     __device__ __forceinline__ static void store(char *row, int col, int H, const float (&f)[V])
     {
@@ -84,9 +102,11 @@ struct Lanes {
                 Access<VB>::store(row + int64_t(col) * sizeof(T), w);
             }
         } else {
+            char *p = row + int64_t(col) * sizeof(T);
+            const bool all = whole(col, H);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (col + 32 * i < H) C::store1(row + int64_t(col + 32 * i) * sizeof(T), f[i]);
+                if (all || col + 32 * i < H) C::store1(p + 32 * i * sizeof(T), f[i]);
         }
     }
     // V e4m3 values of one row
@@ -109,9 +129,11 @@ struct Lanes {
             }
         } else {
             const uint32_t w = pack4(f[0], f[1], f[2], f[3]);
+            char *p = row + col;
+            const bool all = whole(col, H);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (col + 32 * i < H) row[col + 32 * i] = char((w >> (8 * i)) & 0xFFu);
+                if (all || col + 32 * i < H) p[32 * i] = char((w >> (8 * i)) & 0xFFu);
         }
     }
     __device__ __forceinline__ static float block_max(float v)
@@ -163,26 +185,36 @@ __global__ void __launch_bounds__(512) add_rmsnorm_q_kernel(const NormParams p)
     const bool on = row < p.rows;               // whole teams, so whole warps
     const int H = on ? p.H : 0;                 // a team without a row stores nothing (and loads row 0's first column)
     const char *xr = p.x + (on ? row : 0) * p.sx, *rr = p.res + (on ? row : 0) * p.sr;
-    typename L::Raw a[NV], b[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = L::col(t + k * p.tpr);
-        a[k] = L::load(xr, c, H);
-        b[k] = L::load(rr, c, H);
-    }
+    // four pieces' loads at once; gamma is on its way during the reduction where
+    // registers allow
+    constexpr int CK = NV < 4 ? NV : 4;
+    constexpr bool kEarlyGamma = NV <= 4;
     float s[NV][V], ss[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
+    for (int k0 = 0; k0 < NV; k0 += CK) {
+        typename L::Raw a[CK], b[CK];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            s[k][i] = L::get(a[k], i) + L::get(b[k], i);
-            ss[i & 1] = fmaf(s[k][i], s[k][i], ss[i & 1]);
+        for (int k = 0; k < CK; ++k) {
+            const int c = L::col(t + (k0 + k) * p.tpr);
+            a[k] = L::load(xr, c, H);
+            b[k] = L::load(rr, c, H);
         }
-        L::store(p.h + row * p.sh, L::col(t + k * p.tpr), H, s[k]);
-    }
-    typename L::Raw g[NV];          // on its way during the reduction
 #pragma unroll
-    for (int k = 0; k < NV; ++k) g[k] = L::load(p.gamma, L::col(t + k * p.tpr), H);
+        for (int k = 0; k < CK; ++k) {
+            float(&v)[V] = s[k0 + k];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[i] = L::get(a[k], i) + L::get(b[k], i);
+                ss[i & 1] = fmaf(v[i], v[i], ss[i & 1]);
+            }
+            L::store(p.h + row * p.sh, L::col(t + (k0 + k) * p.tpr), H, v);
+        }
+    }
+    typename L::Raw g[kEarlyGamma ? NV : 1];
+    if constexpr (kEarlyGamma) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) g[k] = L::load(p.gamma, L::col(t + k * p.tpr), H);
+    }
     float total = sum32(ss[0] + ss[1]);
     if (p.tpr > 32) {
         const int lane = threadIdx.x & 31, nw = p.tpr >> 5;
@@ -196,9 +228,10 @@ __global__ void __launch_bounds__(512) add_rmsnorm_q_kernel(const NormParams p)
     for (int k = 0; k < NV; ++k) {
         const int piece = t + k * p.tpr, c = L::col(piece);
         float m = 0.0f;
+        if constexpr (!kEarlyGamma) g[0] = L::load(p.gamma, c, H);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            s[k][i] = s[k][i] * rstd * L::get(g[k], i);
+            s[k][i] = s[k][i] * rstd * L::get(g[kEarlyGamma ? k : 0], i);
             m = fmaxf(m, fabsf(s[k][i]));
         }
         const Divider d(L::block_max(m));
@@ -328,7 +361,7 @@ template <class T, int VB>
 QuantFn quant_kernel(bool blocks, int nv)
 {
     if (blocks) return quantize_blocks_kernel<T, VB>;
-    return nv == 1 ? quantize_rows_kernel<T, 1, VB> : quantize_rows_kernel<T, VB == 32 ? 2 : 4, VB>;
+    return nv == 1 ? quantize_rows_kernel<T, 1, VB> : quantize_rows_kernel<T, VB == 16 ? 4 : 2, VB>;
 }
 
 template <class T>
@@ -422,11 +455,11 @@ extern "C" int glu_add_rmsnorm_q(const void *x, int64_t x_stride, const void *re
     // Pieces a row has (V values each), and pieces per thread: for 16-bit types
     // and single elements as many as leave 128 threads to a row (bf16 4096 x
     // 4096: 20.6 us against 22.6 with 256 threads, 2048 x 16384: 43.7 against
-    // 50.6, 4096 x 4101: 62 against 96), for f32 pieces 512.
+    // 50.6), but no more than 16 single elements; for f32 pieces 512.
     const int V = vb ? vb / E : 4;
     const int64_t pieces = vb ? n_cols / V : groups * 32;
     int nv = 1;
-    while (pieces > int64_t(512) * nv || ((!vb || E == 2) && pieces > int64_t(128) * nv && nv * V < (vb ? 64 : 32))) nv *= 2;
+    while (pieces > int64_t(512) * nv || ((!vb || E == 2) && pieces > int64_t(128) * nv && nv * V < (vb ? 64 : 16))) nv *= 2;
     int tpr = int((pieces + nv - 1) / nv);
     tpr = (tpr + 31) / 32 * 32;
     const int teams = tpr >= 128 ? 1 : 128 / tpr;
@@ -509,10 +542,10 @@ extern "C" int glu_quantize(const void *x, int64_t x_stride, void *q, int64_t q_
         if (srows > 65535 || groups > INT32_MAX) return GLU_ERR_SHAPE;
         grid = dim3(unsigned(groups), unsigned(srows));
     } else {
-        // two 32-byte pieces per thread (four of the others) in rows that fill
+        // four 16-byte pieces per thread (two of the others) in rows that fill
         // a block with them, else one
         const int64_t pieces = vb ? n_cols / V : groups * 32;
-        const int wide = vb == 32 ? 2 : 4;
+        const int wide = vb == 16 ? 4 : 2;
         nv = pieces >= 256 * wide ? wide : 1;
         int64_t tpr = (pieces + nv - 1) / nv;
         tpr = tpr > 256 ? 256 : (tpr + 31) / 32 * 32;
