@@ -16,10 +16,10 @@
 //
 // Two kernels:
 //   * wide: a pair of blocks (cta_group::2) per tile of 256 rows of a; one
-//     thread holds half of one row's columns (64 or 128 sums), so the row scale
-//     is one float per thread and a row's largest magnitude needs two threads;
+//     thread holds half of one row's columns (128 sums), so the row scale is one
+//     float per thread and a row's largest magnitude needs two threads;
 //   * narrow, for few rows: the weights take the 128 lanes of the MMA and the
-//     rows of a its N (16 to 128), so no tensor-core row is wasted on absent
+//     rows of a its N (16 to 64), so no tensor-core row is wasted on absent
 //     rows and the time is the weights' trip from HBM; long sums over few tiles
 //     are split over the blocks of a cluster, which add their parts in a fixed
 //     order through distributed shared memory.

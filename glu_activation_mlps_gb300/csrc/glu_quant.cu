@@ -224,6 +224,12 @@ __global__ void __launch_bounds__(512) add_rmsnorm_q_kernel(const NormParams p)
     }
     const float rstd = 1.0f / sqrtf(total / float(p.H) + p.eps);
     if (on && t == 0 && p.rstd) p.rstd[row] = rstd;
+    // y / scale = s gamma 448 / max |s gamma|: rstd cancels, and with it a
+    // rounding of every value, and goes into the scale alone; where it is far
+    // from 1 it stays with the values, whose products with gamma might leave the
+    // range of floats without it.
+    const bool near1 = rstd > 0.0009765625f && rstd < 1024.0f;
+    const float pre = near1 ? 1.0f : rstd, post = near1 ? rstd : 1.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int piece = t + k * p.tpr, c = L::col(piece);
@@ -231,15 +237,18 @@ __global__ void __launch_bounds__(512) add_rmsnorm_q_kernel(const NormParams p)
         if constexpr (!kEarlyGamma) g[0] = L::load(p.gamma, c, H);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            s[k][i] = s[k][i] * rstd * L::get(g[kEarlyGamma ? k : 0], i);
+            s[k][i] = s[k][i] * pre * L::get(g[kEarlyGamma ? k : 0], i);
             m = fmaxf(m, fabsf(s[k][i]));
         }
-        const Divider d(L::block_max(m));
-        const float f = d.factor();
+        // (next to nothing, the scale's floor needs the largest y itself)
+        m = L::block_max(m);
+        const bool tiny = m < kAmaxFloor || m * post < kAmaxFloor;
+        const Divider d(tiny ? m * post : m);
+        const float f = tiny ? d.factor() * post : d.factor();
 #pragma unroll
         for (int i = 0; i < V; ++i) s[k][i] *= f;
         L::store_q(p.q + row * p.sq, c, H, s[k]);
-        if (piece % L::kPer == 0 && c < H) p.scale[row * p.ss + piece / L::kPer] = d.scale();
+        if (piece % L::kPer == 0 && c < H) p.scale[row * p.ss + piece / L::kPer] = tiny ? d.scale() : d.scale() * post;
     }
 }
 

@@ -50,9 +50,9 @@ struct Divider {
         return 512.0f * fmaf(fmaf(-q, top, n), inv, q);
     }
     // 1 / scale, for values that carry roundings of their own: v * factor() is
-    // off by two roundings more, which no longer moves exact ties.  NaN for a
-    // block with an infinity, as the corrected quotient is.
-    __device__ __forceinline__ float factor() const { return inv > 0.0f ? kFp8Max * inv : top - top; }
+    // off by two roundings, which no longer moves exact ties.  NaN for a block
+    // with an infinity, as the corrected quotient is.
+    __device__ __forceinline__ float factor() const { return inv > 0.0f ? kFp8Max / top : top - top; }
     __device__ __forceinline__ float scale() const { return top / kFp8Max; }
 };
 

@@ -225,6 +225,27 @@ def test_add_rmsnorm_q_strided_and_guarded(dt, cols):
         assert torch.all(buf[mask] == fill)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_add_rmsnorm_q_tiny_values(dt):
+    """Rows, and blocks of gamma, next to nothing: the scale's floor holds y."""
+    g = gen(77)
+    x = randn(g, 6, 512) * torch.tensor([1.0, 1e-15, 1e-25, 1e-31, 1e-36, 0.0], device="cuda")[:, None]
+    x = x.to(DT[dt])
+    gamma = torch.ones(512, device="cuda")
+    gamma[128:256], gamma[256:384] = 1e-20, 1e-33
+    gamma = (gamma * (1 + 0.1 * randn(g, 512))).to(DT[dt])
+    for eps in (1e-5, 1e-30):
+        h, q, s = glu.add_rmsnorm_q(x, torch.zeros_like(x), gamma, eps)
+        r = 1 / torch.sqrt((x.double() ** 2).mean(-1, keepdim=True) + float(np.float32(eps)))
+        # squares below 2^-149 vanish in the sum: where the mean square is not far
+        # above that, rstd is eps's
+        y = x.double() * r * gamma.double()
+        keep = (x.double() ** 2).mean(-1) > 2.0 ** -110
+        keep |= (x.double() ** 2).mean(-1) < 2.0 ** -30 * eps
+        # values of 2^-149 quanta, and a product of that size: an absolute slack
+        check_quantised(q[keep], s[keep], y[keep], 1, NORM_REL, 2.0 ** -120)
+
+
 def test_add_rmsnorm_q_zero_rows_and_nan():
     x = torch.zeros(3, 256, dtype=torch.bfloat16, device="cuda")
     x[1, 3] = float("nan")
