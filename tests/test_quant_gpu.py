@@ -465,6 +465,37 @@ def test_grouped_fwd(loads, act):
     assert torch.all(y.view(torch.uint8)[lo:] == 0x11) and torch.all(ys[lo:] == 7.0)
 
 
+def test_many_experts_many_rows_long_sums():
+    """The most experts (and one more is refused), a hundred thousand rows, a
+    sum of 70000 terms: exact grids, both kernels."""
+    g = gen(41)
+    E, N, K = 1024, 130, 128
+    w = torch.randint(-4, 5, (E, N, K), generator=g, device="cuda").float().to(FP8)
+    sw = torch.exp2(torch.randint(-1, 2, (E, 2, 1), generator=g, device="cuda").float())
+    for per in (1, 40, 100):
+        loads = torch.randint(0, 2 * per + 1, (E,), generator=g, device="cuda")
+        off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        off[1:] = loads.cumsum(0)
+        M = int(off[-1])
+        a, sa = grid(g, M, K, 1)
+        d = glu.gemm_q_nt(a, sa, w, sw, offsets=off)
+        e = torch.repeat_interleave(torch.arange(E, device="cuda"), loads)
+        for lo in range(0, M, 20000):       # each row with its own expert's weights
+            sl = slice(lo, min(M, lo + 20000))
+            scale = sw[e[sl]].repeat_interleave(128, 1)[:, :N, 0].double()
+            want = torch.einsum("mk,mnk->mn", a[sl].float(), w.float()[e[sl]]).double() * sa[sl].double() * scale
+            assert torch.equal(d[sl], want.float().to(torch.bfloat16))
+    with pytest.raises(glu.GluError) as err:
+        glu.gemm_q_nt(a, sa, torch.empty(1025, N, K, dtype=FP8, device="cuda"), torch.empty(1025, 2, 1, device="cuda"),
+                      offsets=torch.zeros(1026, dtype=torch.int32, device="cuda"))
+    assert err.value.status == -2
+    for M, K, N in ((100003, 200, 72), (5, 70000, 200), (300, 70000, 264)):
+        a, sa = grid(g, M, K, 1)
+        b, sb = grid(g, N, K, 128)
+        assert torch.equal(glu.gemm_q_nt(a, sa, b, sb, dtype=torch.float16),
+                           (value(a, sa, 1) @ value(b, sb, 128).T).float().half())
+
+
 def test_grouped_agrees_with_dense():
     """One expert with every row is the dense product bit for bit where both
     take the same kernel (sums do not depend on the tile order)."""
