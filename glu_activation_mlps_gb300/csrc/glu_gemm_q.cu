@@ -726,9 +726,8 @@ struct Narrow {
     static constexpr int kTileW = BM * BK;
     static constexpr int kTileA = NT * BK;
     static constexpr int kStageBytes = MATS * kTileW + kTileA;
-    // two blocks per SM, each with three stages or more, where that fits
-    static constexpr int kPerSm = 104 * 1024 / kStageBytes >= 3 ? 2 : 1;
-    static constexpr int kStages = (kPerSm == 2 ? 104 : 200) * 1024 / kStageBytes;
+    static constexpr int kStages = 104 * 1024 / kStageBytes;        // two blocks per SM
+    static_assert(kStages >= 3, "stages in flight");
     static constexpr int kCols = MATS * NT;
     static constexpr int kTmemCols = pow2_at_least(2 * kCols);
     static constexpr int kRing = kStages * kStageBytes;
@@ -1134,27 +1133,28 @@ WideFn wide_kernel(int out)
     }
 }
 
-template <int NT>
-NarrowFn narrow_kernel(int out)
+NarrowFn narrow_kernel(int out, int nt, int *smem)
 {
     using B = __nv_bfloat16;
-    if (out == kOutF16) return gemm_q_narrow_kernel<Plain, __half, NT>;
-    if (out == kOutBF16) return gemm_q_narrow_kernel<Plain, B, NT>;
-    if constexpr (NT <= 32) {
-        switch (out) {
-        case 0: return gemm_q_narrow_kernel<Silu, B, NT>;
-        case 1: return gemm_q_narrow_kernel<GeluErf, B, NT>;
-        case 2: return gemm_q_narrow_kernel<GeluTanh, B, NT>;
-        default: return gemm_q_narrow_kernel<Relu, B, NT>;
-        }
+    using H = __half;
+    *smem = out < kOutF16 ? Narrow<16, 2>::kSmemBytes
+            : nt == 16    ? Narrow<16, 1>::kSmemBytes
+            : nt == 32    ? Narrow<32, 1>::kSmemBytes
+                          : Narrow<64, 1>::kSmemBytes;
+    switch (out) {
+    case 0: return gemm_q_narrow_kernel<Silu, B, 16>;
+    case 1: return gemm_q_narrow_kernel<GeluErf, B, 16>;
+    case 2: return gemm_q_narrow_kernel<GeluTanh, B, 16>;
+    case 3: return gemm_q_narrow_kernel<Relu, B, 16>;
+    case kOutF16:
+        return nt == 16   ? gemm_q_narrow_kernel<Plain, H, 16>
+               : nt == 32 ? gemm_q_narrow_kernel<Plain, H, 32>
+                          : gemm_q_narrow_kernel<Plain, H, 64>;
+    default:
+        return nt == 16   ? gemm_q_narrow_kernel<Plain, B, 16>
+               : nt == 32 ? gemm_q_narrow_kernel<Plain, B, 32>
+                          : gemm_q_narrow_kernel<Plain, B, 64>;
     }
-    return nullptr;
-}
-
-template <int NT>
-int narrow_smem(int out)
-{
-    return out < kOutF16 ? Narrow<NT, NT <= 32 ? 2 : 1>::kSmemBytes : Narrow<NT, 1>::kSmemBytes;
 }
 
 // The shared-memory opt-in of each kernel, once per device.
@@ -1372,20 +1372,27 @@ int run(Args x, glu_stream_t stream)
     // rows per expert, as far as the host knows
     const int64_t rows = grouped ? (x.M + x.groups - 1) / x.groups : x.M;
     CUtensorMap ta, t0, t1, ty;
-    const int nt = rows <= 16 ? 16 : rows <= 32 || !plain ? 32 : 64;
+    // rows a narrow tile takes: 16, 32 or 64 for the plain product; always 16 for
+    // the gated one, whose tiles of 32 leave room for one block per SM only (200
+    // rows, 8 experts of 4096 x 14336: 186 us with tiles of 16, 226 with 32; one
+    // MLP and 32 rows: 28.4, 30.5)
+    const int nt = rows <= 16 || !plain ? 16 : rows <= 32 ? 32 : 64;
     const int64_t n_blocks = (x.N + BM - 1) / BM;
     // row tiles; with experts at most: each may end in a part of a tile
     const auto row_tiles = [&](int64_t r) {
         return grouped ? x.M / r + (x.groups < x.M ? x.groups : x.M) : (x.M + r - 1) / r;
     };
     const int64_t tiles_n = row_tiles(nt) * n_blocks;
-    const int64_t slots_n = int64_t(sms) * (plain || nt == 16 ? 2 : Narrow<32, 2>::kPerSm);
+    const int64_t slots_n = int64_t(sms) * 2;
     // Narrow: blocks per tile, the split of K whose rounds of tiles take the
     // least time: in K blocks, a round costs about ten more for its start and
-    // its end, and adding the parts half a one each.
+    // its end, and adding the parts half a one each.  (By expert only where the
+    // most tiles there can be have their parts on the GPU at once: a split grid
+    // holds a cluster for each of them, with a tile or not.)
     int split = 1;
     int64_t best = -1;
-    for (int sp = 1; sp <= (grouped ? 1 : kMaxSplit) && (sp == 1 || sp * 2 <= p.k_tiles); sp *= 2) {
+    for (int sp = 1; sp <= kMaxSplit && (sp == 1 || sp * 2 <= p.k_tiles); sp *= 2) {
+        if (sp > 1 && grouped && tiles_n * sp > slots_n) break;
         const int64_t cost = (tiles_n * sp + slots_n - 1) / slots_n * ((p.k_tiles + sp - 1) / sp + 10) + sp / 2;
         if (best < 0 || cost < best) {
             best = cost;
@@ -1393,12 +1400,12 @@ int run(Args x, glu_stream_t stream)
         }
     }
     // Which kernel.  Up to 32 rows the narrow one wins throughout (16 rows at
-    // 4096 x 4096: 7.2 us against 19).  Beyond, only the plain product has a
-    // narrow form (64 rows a tile; a gated one would hold 128 sums a thread):
-    // by expert up to 96 rows each (64 experts of 2048 x 2048: 73 us against 87
-    // at 64 rows, 108 against 96 at 128); else where its rounds, of K blocks
-    // that take 4/3 the wide kernel's time, end sooner (14336 x 4096: 24 us
-    // against 56 at 128 rows, 41 against 57 at 256, 69 against 58 at 384).
+    // 4096 x 4096: 7.2 us against 19).  Beyond, the gated product is wide (64
+    // rows at 4096 x 14336: 36 us against 54 in narrow tiles of 16); the plain
+    // one is narrow by expert up to 96 rows each (64 experts of 2048 x 2048: 73
+    // us against 87 at 64 rows, 108 against 96 at 128), else where its rounds, of
+    // K blocks that take 4/3 the wide kernel's time, end sooner (14336 x 4096:
+    // 24 us against 56 at 128 rows, 41 against 57 at 256, 69 against 58 at 384).
     const int64_t tiles_w = row_tiles(2 * BM) * ((x.N + (plain ? 255 : 127)) / (plain ? 256 : 128));
     const int64_t cost_w = (tiles_w + sms / 2 - 1) / (sms / 2) * (p.k_tiles + 9);
     const bool narrow = rows <= 32 || (plain && (grouped ? rows <= 96 : 4 * best / 3 < cost_w));
@@ -1411,9 +1418,8 @@ int run(Args x, glu_stream_t stream)
             !make_map(&t0, u8, x.w0, x.K, x.N, x.w_stride, depth, w_group, BK, BM, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !make_map(&t1, u8, x.w1, x.K, x.N, x.w_stride, depth, w_group, BK, BM, CU_TENSOR_MAP_SWIZZLE_128B))
             return glu::cuda_fail(cudaErrorInvalidValue);
-        const NarrowFn fn = nt == 16 ? narrow_kernel<16>(x.out) : nt == 32 ? narrow_kernel<32>(x.out) : narrow_kernel<64>(x.out);
-        const int smem = nt == 16 ? narrow_smem<16>(x.out) : nt == 32 ? narrow_smem<32>(x.out) : narrow_smem<64>(x.out);
-        const void *f = reinterpret_cast<const void *>(fn);
+        int smem = 0;
+        const void *f = reinterpret_cast<const void *>(narrow_kernel(x.out, nt, &smem));
         if (int st = opt_in(f, smem, dev, x.out, nt == 16 ? 1 : nt == 32 ? 2 : 3)) return st;
         const int64_t grid = split > 1 ? tiles_n * split : (tiles_n < slots_n ? tiles_n : slots_n);
         void *args[] = {&ta, &t0, &t1, &p, &split};
