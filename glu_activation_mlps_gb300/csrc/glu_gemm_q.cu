@@ -267,26 +267,29 @@ __device__ __forceinline__ void count_tiles(const Params &p, int rows_per_tile, 
         return;
     }
     if (threadIdx.x >= 32) return;
-    const int lane = threadIdx.x;
-    int base = 0;
-    for (int e0 = 0; e0 < p.n_groups; e0 += 32) {
-        const int e = e0 + lane;
-        int n = 0;
+    // each lane counts a run of neighbouring groups (their offsets come in one
+    // trip to memory), then the lanes' sums are scanned
+    const int lane = threadIdx.x, per = (p.n_groups + 31) / 32, first = lane * per;
+    int sum = 0;
+#pragma unroll 8
+    for (int i = 0; i < per; ++i) {
+        const int e = first + i;
         if (e < p.n_groups) {
             int lo, hi;
             group_rows(p, e, lo, hi);
-            n = min((hi - lo + rows_per_tile - 1) / rows_per_tile, p.m_tiles);
+            sum = min(sum + min((hi - lo + rows_per_tile - 1) / rows_per_tile, p.m_tiles), p.m_tiles);
+            prefix[e + 1] = sum;
         }
-        int v = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int w = __shfl_up_sync(0xFFFFFFFFu, v, o);
-            if (lane >= o) v = min(v + w, p.m_tiles);
-        }
-        if (e < p.n_groups) prefix[e + 1] = min(base + v, p.m_tiles);
-        base = min(base + __shfl_sync(0xFFFFFFFFu, v, 31), p.m_tiles);
     }
-    if (lane == 0) prefix[0] = 0;
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int w = __shfl_up_sync(0xFFFFFFFFu, before, o);
+        if (lane >= o) before = min(before + w, p.m_tiles);
+    }
+    before = __shfl_up_sync(0xFFFFFFFFu, before, 1);
+    if (lane == 0) before = prefix[0] = 0;
+    for (int e = first; e < min(first + per, p.n_groups); ++e) prefix[e + 1] = min(prefix[e + 1] + before, p.m_tiles);
 }
 
 struct Tile {
