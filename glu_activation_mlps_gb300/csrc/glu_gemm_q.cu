@@ -1563,7 +1563,10 @@ extern "C" int glu_mlp_q_fwd(const void *x, int64_t x_stride, const float *x_sca
 {
     using namespace glu::gemmq;
     if (act < GLU_ACT_SILU || act > GLU_ACT_RELU || (dtype != GLU_F16 && dtype != GLU_BF16)) return GLU_ERR_ENUM;
-    if (!offsets) n_groups = 0;
+    if (!offsets)
+        n_groups = 0;
+    else if (n_groups == 0 && M > 0)    // no expert, so no row
+        M = 0;
     if (M < 0 || H < 0 || I < 0 || M > INT32_MAX || I > INT32_MAX) return GLU_ERR_SHAPE;
     if (M > 0 && H > 0 && I > 0) {
         if (!workspace || workspace_bytes < glu_mlp_q_workspace_bytes(M, I)) return GLU_ERR_WORKSPACE;

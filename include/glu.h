@@ -665,7 +665,7 @@ int glu_gemm_q_grouped_fwd(const void *x, int64_t x_stride, const float *x_scale
  *                          of `dtype` (GLU_F16 or GLU_BF16).
  *   offsets, n_groups      NULL and anything: one MLP (the *_group strides are
  *                          then ignored).  Else by expert, as in
- *                          glu_gemm_q_grouped_nt.
+ *                          glu_gemm_q_grouped_nt (n_groups == 0: no work).
  *   workspace              device memory for y and its scales, 16-byte aligned,
  *                          at least glu_mlp_q_workspace_bytes(M, I) bytes, else
  *                          GLU_ERR_WORKSPACE.

@@ -146,6 +146,18 @@ def test_mlp():
     assert mlp(I=0) == CUDA and mlp() == CUDA and mlp(offsets=BASE + 63 * MB, n=2) == CUDA
 
 
+def test_mlp_without_experts():
+    """Offsets and no expert: no work, as in the grouped products, not the dense MLP."""
+    off = BASE + 63 * MB
+    assert mlp(offsets=off, n=0) == OK and glu.glu_last_launch()["launched"] == 0
+    assert mlp(offsets=off, n=0, I=0) == OK
+    # there are no weights to point to, nor rows for a workspace to hold
+    assert mlp(offsets=off, n=0, wd=None, ws=None, out=None, x=None) == OK
+    assert mlp(offsets=off, n=-1) == SHAPE and mlp(offsets=off, n=0, act=9) == ENUM
+    assert mlp(offsets=off, n=0, M=-1) == SHAPE
+    assert mlp(n=0) == CUDA             # without offsets it is the dense one
+
+
 def test_python_layer_refuses():
     x = torch.zeros(4, 256)
     q, s = torch.zeros(4, 256, dtype=torch.float8_e4m3fn), torch.zeros(4, 2)

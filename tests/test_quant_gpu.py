@@ -568,6 +568,22 @@ def test_mlp_by_expert():
     assert torch.equal(out, want) and torch.all(out[sum(loads):] == 7.0)
 
 
+def test_without_experts():
+    """A part of a model that holds no expert: every row of the outputs is left as it was."""
+    M, H, I = 5, 256, 384
+    x, sx = random_q(gen(2), M, H, 1)
+
+    def none(n, k):
+        return torch.empty(0, n, k, dtype=FP8, device="cuda"), torch.empty(0, -(-n // 128), -(-k // 128), device="cuda")
+
+    off = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((M, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    y, ys = torch.full((M, I), 0x11, dtype=torch.uint8, device="cuda").view(FP8), torch.full((M, 3), 7.0, device="cuda")
+    glu.mlp_q_fwd(x, sx, *none(I, H), *none(I, H), *none(H, I), out=out, offsets=off)
+    glu.gemm_q_fwd(x, sx, *none(I, H), *none(I, H), y=y, y_scale=ys, offsets=off)
+    assert torch.all(out == 7.0) and torch.all(y.view(torch.uint8) == 0x11) and torch.all(ys == 7.0)
+
+
 def block(x, res, gamma, wg, wu, wd):
     """One decoder sub-block: norm, MLP, and the next norm over its result."""
     h, q, s = glu.add_rmsnorm_q(x, res, gamma)
