@@ -1227,6 +1227,16 @@ struct Args {
     int out;
 };
 
+// The bytes of a stack of `depth` matrices, `group` elements apart; none for empty matrices.
+bool stack_span(const void *q, int64_t rows, int64_t stride, int64_t cols, int64_t group, int64_t depth, int e, Span *o)
+{
+    if (!span(q, rows, stride, cols, e, o)) return false;
+    int64_t more = 0;
+    return depth <= 1 || o->lo == o->hi ||
+           (!__builtin_mul_overflow(depth - 1, group * e, &more) &&
+            !__builtin_add_overflow(o->hi, uint64_t(more), &o->hi));
+}
+
 // Argument rules shared by the four entry points; no CUDA call.
 int validate(Args &x, bool *empty)
 {
@@ -1277,12 +1287,7 @@ int validate(Args &x, bool *empty)
         if (depth > 1 && (x.w_group < wspan || x.sw_group < swspan)) return GLU_ERR_STRIDE;
     }
     const auto stack = [&](const void *q, int64_t rows, int64_t stride, int64_t cols, int64_t group, int e, Span *o) {
-        if (!span(q, rows, stride, cols, e, o)) return false;
-        int64_t more = 0;
-        if (depth > 1 && (__builtin_mul_overflow(depth - 1, group * e, &more) ||
-                          __builtin_add_overflow(o->hi, uint64_t(more), &o->hi)))
-            return false;
-        return true;
+        return stack_span(q, rows, stride, cols, group, depth, e, o);
     };
     bool fits = span(x.y, x.M, x.y_stride, x.N, E, &s[0]) &&
                 span(x.ys, plain ? 0 : x.M, x.ys_stride, nb, 4, &s[1]) &&
@@ -1588,11 +1593,27 @@ extern "C" int glu_mlp_q_fwd(const void *x, int64_t x_stride, const float *x_sca
         if (int st = validate(cu, &empty)) return st;
     if (int st = validate(cd, &empty)) return st;
     if (!empty) {
-        glu::Span so{}, sx{}, ss{};
-        if (!glu::span(out, M, cd.y_stride, H, 2, &so) || !glu::span(x, I > 0 ? M : 0, cu.a_stride, H, 1, &sx) ||
-            !glu::span(x_scale, I > 0 ? M : 0, cu.sa_stride, (H + 127) / 128, 4, &ss))
-            return GLU_ERR_SHAPE;
-        if (glu::overlap(so, sx) || glu::overlap(so, ss)) return GLU_ERR_ALIAS;
+        // out and the whole workspace against every operand of either product
+        const int64_t hb = (H + glu::quant::kBlock - 1) / glu::quant::kBlock, depth = n_groups > 1 ? n_groups : 1;
+        const int64_t used = I > 0 ? 1 : 0;         // I == 0 reads and writes none of them
+        glu::Span outs[2] = {}, in[9] = {};
+        const bool fits =
+            glu::span(out, M, cd.y_stride, H, 2, &outs[0]) &&
+            glu::span(workspace, used, 1, M * (ys + 4 * groups), 1, &outs[1]) &&
+            glu::span(x, used * M, cu.a_stride, H, 1, &in[0]) &&
+            glu::span(x_scale, used * M, cu.sa_stride, hb, 4, &in[1]) &&
+            stack_span(w_gate, used * I, cu.w_stride, H, cu.w_group, depth, 1, &in[2]) &&
+            stack_span(w_up, used * I, cu.w_stride, H, cu.w_group, depth, 1, &in[3]) &&
+            stack_span(gate_scale, used * groups, cu.sw_stride, hb, cu.sw_group, depth, 4, &in[4]) &&
+            stack_span(up_scale, used * groups, cu.sw_stride, hb, cu.sw_group, depth, 4, &in[5]) &&
+            stack_span(w_down, used * H, cd.w_stride, I, cd.w_group, depth, 1, &in[6]) &&
+            stack_span(down_scale, used * hb, cd.sw_stride, groups, cd.sw_group, depth, 4, &in[7]) &&
+            glu::span(offsets, n_groups > 0 ? 1 : 0, 1, n_groups + 1, 4, &in[8]);
+        if (!fits) return GLU_ERR_SHAPE;
+        if (glu::overlap(outs[0], outs[1])) return GLU_ERR_ALIAS;
+        for (const glu::Span &o : outs)
+            for (const glu::Span &i : in)
+                if (glu::overlap(o, i)) return GLU_ERR_ALIAS;
         if (I > 0)
             if (int st = check_device(cu)) return st;
         if (int st = check_device(cd)) return st;

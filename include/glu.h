@@ -669,7 +669,8 @@ int glu_gemm_q_grouped_fwd(const void *x, int64_t x_stride, const float *x_scale
  *   workspace              device memory for y and its scales, 16-byte aligned,
  *                          at least glu_mlp_q_workspace_bytes(M, I) bytes, else
  *                          GLU_ERR_WORKSPACE.
- * Every argument is checked before the first launch; out overlaps nothing.
+ * Every argument is checked before the first launch; out and the workspace
+ * overlap nothing.
  * M == 0 or H == 0: no work; I == 0: out = 0.
  */
 int glu_mlp_q_fwd(const void *x, int64_t x_stride, const float *x_scale, int64_t x_scale_stride,

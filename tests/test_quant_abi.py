@@ -158,6 +158,32 @@ def test_mlp_without_experts():
     assert mlp(n=0) == CUDA             # without offsets it is the dense one
 
 
+def test_mlp_overlaps():
+    """out and the workspace (the gaps between its rows too) overlap no operand of
+    either product, dense or in any expert's part."""
+    off = BASE + 63 * MB
+    # x, its scales, gate and up weights and scales, down weights and scales: first and last bytes
+    ends = {BASE: 8 * 256, BASE + MB: 8 * 8, BASE + 2 * MB: 384 * 256, BASE + 4 * MB: 384 * 256, BASE + 6 * MB: 24,
+            BASE + 7 * MB: 24, BASE + 8 * MB: 256 * 384, BASE + 12 * MB: 24}
+    for at, size in ends.items():
+        for last in (0, size - 16 & ~15):
+            assert mlp(out=at + last) == ALIAS, (at - BASE, last)
+            assert mlp(ws=at + last) == ALIAS, (at - BASE, last)
+            assert mlp(out=at + last, offsets=off, n=1) == ALIAS and mlp(ws=at + last, offsets=off, n=1) == ALIAS
+        # just behind it
+        assert mlp(out=at + (size + 15 & ~15)) == CUDA and mlp(ws=at + (size + 15 & ~15)) == CUDA
+    for at, group in ((2 * MB, 384 * 256), (4 * MB, 384 * 256), (6 * MB, 24), (7 * MB, 24), (8 * MB, 256 * 384),
+                      (12 * MB, 24)):
+        third = BASE + at + 2 * group
+        assert mlp(out=third, offsets=off, n=3) == ALIAS and mlp(ws=third, offsets=off, n=3) == ALIAS
+        assert mlp(out=BASE + at + (3 * group + 15 & ~15), offsets=off, n=3) == CUDA
+    assert mlp(out=off, offsets=off, n=3) == ALIAS and mlp(ws=off, offsets=off, n=3) == ALIAS
+    # the workspace: 8 rows of 384 + 12 bytes
+    assert mlp(out=BASE + 64 * MB + 8 * 396 - 2) == ALIAS and mlp(out=BASE + 64 * MB + 8 * 396) == CUDA
+    # no columns between the products: the weights are not read
+    assert mlp(I=0, out=BASE + 8 * MB) == CUDA and mlp(I=0, out=BASE + 2 * MB, offsets=off, n=3) == CUDA
+
+
 def test_python_layer_refuses():
     x = torch.zeros(4, 256)
     q, s = torch.zeros(4, 256, dtype=torch.float8_e4m3fn), torch.zeros(4, 2)
