@@ -1233,7 +1233,7 @@ bool stack_span(const void *q, int64_t rows, int64_t stride, int64_t cols, int64
     if (!span(q, rows, stride, cols, e, o)) return false;
     int64_t more = 0;
     return depth <= 1 || o->lo == o->hi ||
-           (!__builtin_mul_overflow(depth - 1, group * e, &more) &&
+           (!__builtin_mul_overflow(group, int64_t(e), &more) && !__builtin_mul_overflow(more, depth - 1, &more) &&
             !__builtin_add_overflow(o->hi, uint64_t(more), &o->hi));
 }
 

@@ -124,6 +124,13 @@ def test_grouped():
     assert grouped(n=1, wg=0, wsg=0) == CUDA and grouped() == CUDA
 
 
+def test_grouped_extents_overflow():
+    """Experts so far apart that their bytes wrap around 64 bits."""
+    for wsg in (1 << 62, (1 << 62) + 6, 1 << 61, (1 << 63) - 1):
+        assert grouped(wsg=wsg) == SHAPE, wsg
+    assert grouped(wg=(1 << 63) - 16) == STRIDE and grouped(wg=1 << 40) == STRIDE
+
+
 def mlp(x=BASE, out=BASE + 32 * MB, so=256, M=8, H=256, I=384, ws=BASE + 64 * MB, wb=None, offsets=None, n=0, act=0,
         dtype=BF16, wd=BASE + 8 * MB):
     wb = glu.glu_mlp_q_workspace_bytes(M, I) if wb is None else wb
