@@ -401,6 +401,32 @@ def test_gemm_q_fwd(M, K, I, act):
     assert torch.all(buf[outside(buf, M, I)] == 0x44) and torch.all(sbuf[outside(sbuf, M, ys.shape[1])] == 7.0)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu_erf", "gelu_tanh", "relu"])
+@pytest.mark.parametrize("M", [8, 300])
+def test_gated_nan_stays_alone(M, act):
+    """A NaN in some rows of the gate and up weights is a NaN in those columns of
+    y and takes no part in the scales: everything else has the bits of weights
+    whose rows are zeros there, in the narrow kernel (8 rows) and the wide one."""
+    g = gen(M)
+    K, I = 384, 300
+    x, sx = random_q(g, M, K, 1, 0.5)
+    nans, zeros = [], []
+    cols = [5, 130, 299], [66, 131, 257]        # of the gate, of up
+    for at in cols:
+        w, s = glu.quantize(randn(g, I, K) / K ** 0.5, block_rows=128)
+        for out, byte in ((nans, 0x7F), (zeros, 0)):
+            v = w.clone()
+            v.view(torch.uint8)[at] = byte
+            out += [v, s]
+    y, ys = glu.gemm_q_fwd(x, sx, *nans, act=act)
+    y0, ys0 = glu.gemm_q_fwd(x, sx, *zeros, act=act)
+    hit = torch.zeros(I, dtype=torch.bool, device="cuda")
+    hit[cols[0] + cols[1]] = True
+    assert torch.all(torch.isnan(y.float()[:, hit]))
+    assert torch.equal(y.view(torch.uint8)[:, ~hit], y0.view(torch.uint8)[:, ~hit])
+    assert torch.equal(ys, ys0)
+
+
 # ---------------------------------------------------------------- by expert
 
 LOADS = [[5], [0, 3, 0, 1], [16, 16], [17, 0, 40, 1, 0], [200, 0, 3], [256, 256], [1, 700, 90, 0, 255, 257],
