@@ -12,7 +12,8 @@ Two levels:
   * ``fwd`` / ``bwd`` / ...: the same calls taking torch CUDA tensors, reading
     pointers and strides from the tensors' metadata.  The 8-bit calls
     (``quantize``, ``add_rmsnorm_q``, ``gemm_q_nt``, ``gemm_q_fwd``,
-    ``mlp_q_fwd``) take float8_e4m3fn tensors with float32 scales.
+    ``mlp_q_fwd``) take float8_e4m3fn tensors with float32 scales; given a
+    ``stream`` they allocate what they return from that stream's memory.
 """
 from __future__ import annotations
 
@@ -604,20 +605,30 @@ def _same_device(x, *others) -> int:
     return dev
 
 
-def _raw_stream(stream, dev: int) -> int:
-    """The stream's handle; the device's current stream for None."""
+def _raw_stream(dev: int) -> int:
+    """The handle of the device's current stream."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _used_on(stream, *tensors):
-    """Tells the allocator that tensors it gave to the current stream are used
-    on another one, so that their memory is not given out again too early."""
+def _on_stream(stream, call, *args, **kw):
+    """call(*args, **kw) with ``stream`` (a torch stream or a handle) current, so
+    that what it allocates is that stream's memory: memory of the current stream
+    may still be written by work queued there.  The allocator is told who uses
+    what on a stream not its own, so that nothing is given out again too early.
+    The caller orders the two streams' work on the operands and the results."""
     import torch
     if not isinstance(stream, torch.Stream):
         stream = torch.cuda.ExternalStream(_stream(stream))
-    for t in tensors:
-        t.record_stream(stream)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    for t in (*args, *kw.values()):
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+    for t in (out,) if isinstance(out, torch.Tensor) else out:
+        t.record_stream(here)
+    return out
 
 
 def _mat(t, name):
@@ -700,10 +711,12 @@ def quantize(x, *, block_rows: int = 1, q=None, scale=None, stream=None):
     (E, N, K) for the weights of E experts, and scale (.., ceil(N / 128),
     ceil(K / 128)))."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, quantize, x, block_rows=block_rows, q=q, scale=scale)
     code = _dtype_code(x)
     shape = x.shape
     dev = _same_device(x, q, scale)
-    s = _raw_stream(stream, dev)
+    s = _raw_stream(dev)
     if block_rows == 1:
         n_rows, x_stride = _mat(x, "x")
         q, scale, q_stride, s_stride = _out_q(q, scale, shape, shape[:-1], x, "q")
@@ -711,8 +724,6 @@ def quantize(x, *, block_rows: int = 1, q=None, scale=None, stream=None):
                           shape[-1], 1, code, s)
         if st:
             raise GluError(st, "glu_quantize")
-        if stream is not None:
-            _used_on(stream, q, scale)
         return q, scale
     if block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
@@ -736,8 +747,6 @@ def quantize(x, *, block_rows: int = 1, q=None, scale=None, stream=None):
                           _mat(se, "scale")[1], n_rows, K, 128, code, s)
         if st:
             raise GluError(st, "glu_quantize")
-    if stream is not None:
-        _used_on(stream, q, scale)
     return q, scale
 
 
@@ -747,6 +756,8 @@ def add_rmsnorm_q(x, residual, gamma, eps: float = 1e-5, *, h=None, q=None, scal
     pass.  ``h`` may be x or residual; ``rstd`` as in add_rmsnorm.  Returns
     (h, q, scale) or (h, q, scale, rstd)."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, add_rmsnorm_q, x, residual, gamma, eps, h=h, q=q, scale=scale, rstd=rstd)
     dev = _same_device(x, residual, gamma, h, q, scale)
     code = _dtype_code(x)
     shape, dtype = x.shape, x.dtype
@@ -773,13 +784,9 @@ def add_rmsnorm_q(x, residual, gamma, eps: float = 1e-5, *, h=None, q=None, scal
         raise ValueError("rstd must be a contiguous float32 tensor with one entry per row")
     st = glu_add_rmsnorm_q(x.data_ptr(), x_stride, residual.data_ptr(), r_stride, gamma.data_ptr(), h.data_ptr(),
                            h_stride, q.data_ptr(), q_stride, scale.data_ptr(), s_stride,
-                           None if rstd is None else rstd.data_ptr(), n_rows, H, eps, code, _raw_stream(stream, dev))
+                           None if rstd is None else rstd.data_ptr(), n_rows, H, eps, code, _raw_stream(dev))
     if st:
         raise GluError(st, "glu_add_rmsnorm_q")
-    if stream is not None:
-        _used_on(stream, h, q, scale)
-        if rstd is not None:
-            _used_on(stream, rstd)
     return (h, q, scale) if rstd is None else (h, q, scale, rstd)
 
 
@@ -791,6 +798,8 @@ def gemm_q_nt(a, a_scale, b, b_scale, *, d=None, dtype=None, offsets=None, strea
     .. offsets[e + 1] are multiplied by b[e]; rows of d that no expert has are
     left as they were."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, gemm_q_nt, a, a_scale, b, b_scale, d=d, dtype=dtype, offsets=offsets)
     dev = _same_device(a, a_scale, b, b_scale, d, offsets)
     n_rows, a_stride, as_stride, K = _in_q(a, a_scale, "a")
     N, b_stride, b_group, bs_stride, bs_group = _weight_q(b, b_scale, K, "b", offsets is not None)
@@ -802,7 +811,7 @@ def gemm_q_nt(a, a_scale, b, b_scale, *, d=None, dtype=None, offsets=None, strea
     else:
         d_stride = _mat(d, "d")[1]
     code = _dtype_code(d)
-    s = _raw_stream(stream, dev)
+    s = _raw_stream(dev)
     if offsets is None:
         st = glu_gemm_q_nt(a.data_ptr(), a_stride, a_scale.data_ptr(), as_stride, b.data_ptr(), b_stride,
                            b_scale.data_ptr(), bs_stride, d.data_ptr(), d_stride, n_rows, K, N, code, s)
@@ -812,8 +821,6 @@ def gemm_q_nt(a, a_scale, b, b_scale, *, d=None, dtype=None, offsets=None, strea
                                    K, N, _offsets(offsets, b), b.shape[0], code, s)
     if st:
         raise GluError(st, "glu_gemm_q_nt" if offsets is None else "glu_gemm_q_grouped_nt")
-    if stream is not None:
-        _used_on(stream, d)
     return d
 
 
@@ -823,6 +830,9 @@ def gemm_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, y=None, y_scal
     the tensor cores, quantised by rows in the epilogue.  x is (..., K), the
     weights (I, K) with one row stride, or (E, I, K) with ``offsets`` (see
     gemm_q_nt)."""
+    if stream is not None:
+        return _on_stream(stream, gemm_q_fwd, x, x_scale, w_gate, gate_scale, w_up, up_scale, y=y, y_scale=y_scale,
+                          act=act, offsets=offsets)
     dev = _same_device(x, x_scale, w_gate, gate_scale, w_up, up_scale, y, y_scale, offsets)
     n_rows, x_stride, xs_stride, K = _in_q(x, x_scale, "x")
     gate = _weight_q(w_gate, gate_scale, K, "w_gate", offsets is not None)
@@ -831,7 +841,7 @@ def gemm_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, y=None, y_scal
     N, w_stride, w_group, s_stride, s_group = gate
     lead = x.shape[:-1]
     y, y_scale, y_stride, ys_stride = _out_q(y, y_scale, (*lead, N), lead, x, "y")
-    s = _raw_stream(stream, dev)
+    s = _raw_stream(dev)
     if offsets is None:
         st = glu_gemm_q_fwd(x.data_ptr(), x_stride, x_scale.data_ptr(), xs_stride, w_gate.data_ptr(), w_up.data_ptr(),
                             w_stride, gate_scale.data_ptr(), up_scale.data_ptr(), s_stride, y.data_ptr(), y_stride,
@@ -843,8 +853,6 @@ def gemm_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, y=None, y_scal
                                     K, N, _offsets(offsets, w_gate), w_gate.shape[0], ACT[act], s)
     if st:
         raise GluError(st, "glu_gemm_q_fwd" if offsets is None else "glu_gemm_q_grouped_fwd")
-    if stream is not None:
-        _used_on(stream, y, y_scale)
     return y, y_scale
 
 
@@ -856,6 +864,9 @@ def mlp_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, w_down, down_scale
     x is (..., H), the gate and up weights (I, H), the down weights (H, I); with
     ``offsets`` (E, I, H) and (E, H, I) (see gemm_q_nt)."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, mlp_q_fwd, x, x_scale, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, out=out,
+                          dtype=dtype, act=act, offsets=offsets, workspace=workspace)
     grouped = offsets is not None
     dev = _same_device(x, x_scale, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, out, offsets, workspace)
     n_rows, x_stride, xs_stride, H = _in_q(x, x_scale, "x")
@@ -880,11 +891,9 @@ def mlp_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, w_down, down_scale
                        w_down.data_ptr(), d_stride, d_group, down_scale.data_ptr(), ds_stride, ds_group,
                        out.data_ptr(), _mat(out, "out")[1], n_rows, H, I,
                        _offsets(offsets, w_gate) if grouped else None, w_gate.shape[0] if grouped else 0, ACT[act],
-                       _dtype_code(out), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+                       _dtype_code(out), workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
     if st:
         raise GluError(st, "glu_mlp_q_fwd")
-    if stream is not None:
-        _used_on(stream, out, workspace)
     return out
 
 

@@ -683,6 +683,113 @@ def test_stream_argument():
         check_quantised(q, s, xb.double(), 1, 4 * U)
 
 
+def test_results_wait_for_the_memory_they_take():
+    """Given another stream, a call's results and workspace may come from memory
+    that work still queued on the current stream uses: a late fill of a freed
+    tensor of the same size must not land in them."""
+    g = gen(19)
+    M, H, I = 2048, 1024, 1024          # every result of 2 MB or more, so that a freed block is taken whole
+    xb = randn(g, M, H).to(torch.bfloat16)
+    gamma = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    x, sx = glu.quantize(xb)
+    wg, wu = (glu.quantize(randn(g, I, H) / H ** 0.5, block_rows=128) for _ in range(2))
+    wd = glu.quantize(randn(g, H, I) / I ** 0.5, block_rows=128)
+    experts = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    stacked = [t[None] for w in (wg, wu, wd) for t in w]
+    calls = {
+        "quantize rows": lambda **k: glu.quantize(xb, **k),
+        "quantize blocks": lambda **k: glu.quantize(xb, block_rows=128, **k),
+        "add_rmsnorm_q": lambda **k: glu.add_rmsnorm_q(xb, xb, gamma, rstd=True, **k),
+        "gemm_q_nt": lambda **k: (glu.gemm_q_nt(x, sx, *wg, **k),),
+        "gemm_q_fwd": lambda **k: glu.gemm_q_fwd(x, sx, *wg, *wu, **k),
+        "mlp_q_fwd": lambda **k: (glu.mlp_q_fwd(x, sx, *wg, *wu, *wd, **k),),
+        "mlp_q_fwd by expert": lambda **k: (glu.mlp_q_fwd(x, sx, *stacked, offsets=experts, **k),),
+    }
+    side = torch.cuda.Stream()
+    for name, call in calls.items():
+        want = [t.clone() for t in call()]
+        sizes = [t.untyped_storage().nbytes() for t in want]
+        sizes.append(glu.glu_mlp_q_workspace_bytes(M, I))
+        for stream in (side, side.cuda_stream):
+            torch.cuda.synchronize()
+            torch.cuda.empty_cache()
+            held = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+            torch.cuda._sleep(100_000_000)          # some 50 ms
+            for t in held:
+                t.fill_(0x55)
+            del held, t
+            got = call(stream=stream)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want)), name
+            del got
+
+
+def test_results_of_another_stream_are_kept_for_this_one():
+    """A result made on another stream and read on the current one: once freed,
+    its memory goes to no later call on that stream before the reading is done."""
+    g = gen(23)
+    xb = randn(g, 2048, 1024).to(torch.bfloat16)
+    want, scale = glu.quantize(xb)
+    zeros = torch.zeros_like(xb)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    for stream in (side, side.cuda_stream):
+        q, s = glu.quantize(xb, stream=stream)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(100_000_000)
+        got, got_scale = q.view(torch.uint8).clone(), s.clone()
+        del q, s
+        for _ in range(3):
+            glu.quantize(zeros, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want.view(torch.uint8)) and torch.equal(got_scale, scale)
+
+
+def test_stream_argument_is_the_default_stream():
+    """Handle 0, the default stream, from inside another one."""
+    g = gen(29)
+    xb = randn(g, 64, 512).to(torch.bfloat16)
+    want = glu.quantize(xb)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for stream in (0, torch.cuda.default_stream()):
+            q, s = glu.quantize(xb, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(q.view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(s, want[1])
+    # and errors leave the current stream as it was
+    here = torch.cuda.current_stream()
+    with pytest.raises(ValueError):
+        glu.quantize(xb, block_rows=3, stream=torch.cuda.Stream())
+    assert torch.cuda.current_stream() == here
+
+
+def test_stream_argument_in_a_graph():
+    """Two calls on a stream that joins a capture, replayed on other inputs."""
+    g = gen(37)
+    M, H, I = 300, 512, 700
+    wg, wu = (glu.quantize(randn(g, I, H) / H ** 0.5, block_rows=128) for _ in range(2))
+    wd = glu.quantize(randn(g, H, I) / I ** 0.5, block_rows=128)
+    xb = randn(g, M, H).to(torch.bfloat16)
+
+    def run(stream=None):
+        q, s = glu.quantize(xb, stream=stream)
+        return [glu.mlp_q_fwd(q, s, *wg, *wu, *wd, stream=stream) for _ in range(2)]
+
+    run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        side.wait_stream(torch.cuda.current_stream())
+        outs = run(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        xb.copy_(randn(g, M, H))
+        gr.replay()
+        assert all(torch.equal(o, w) for o, w in zip(outs, run()))
+
+
 def test_two_calls_at_once():
     """Products on two streams at the same time do not disturb each other."""
     g = gen(31)
