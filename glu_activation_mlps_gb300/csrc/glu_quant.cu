@@ -266,7 +266,7 @@ struct QuantParams {
 };
 
 // By rows: a team of tpr threads (a multiple of 32) takes NV pieces each of one
-// row; blockIdx.y counts stretches of NV * tpr pieces along wide rows.
+// row; blockIdx.y and .z count stretches of NV * tpr pieces along wide rows.
 template <class T, int NV, int VB>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
 {
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
     const int team = threadIdx.x / p.tpr, t = threadIdx.x - team * p.tpr;
     const int64_t row = int64_t(blockIdx.x) * (blockDim.x / p.tpr) + team;
     if (row >= p.rows) return;                  // whole teams, so whole warps
-    const int first = blockIdx.y * p.tpr * NV + t;
+    const int first = int(blockIdx.z * gridDim.y + blockIdx.y) * p.tpr * NV + t;
     const char *xr = p.x + row * p.sx;
     typename L::Raw a[NV];
 #pragma unroll
@@ -562,8 +562,10 @@ extern "C" int glu_quantize(const void *x, int64_t x_stride, void *q, int64_t q_
         const int64_t teams = 256 / tpr;
         const int64_t blocks = (n_rows + teams - 1) / teams;
         const int64_t spans = (pieces + tpr * nv - 1) / (tpr * nv);
-        if (blocks > INT32_MAX || spans > 65535) return GLU_ERR_SHAPE;
-        grid = dim3(unsigned(blocks), unsigned(spans));
+        if (blocks > INT32_MAX) return GLU_ERR_SHAPE;
+        // stretches in y and, above its limit of 65535, in z (the last ones may lie past the row and do nothing)
+        const int64_t layers = (spans + 65534) / 65535;
+        grid = dim3(unsigned(blocks), unsigned((spans + layers - 1) / layers), unsigned(layers));
     }
     const int threads = by_block ? 256 : 256 / p.tpr * p.tpr;
     const QuantFn fn = dtype == GLU_F32   ? quant_kernel<float>(by_block, nv, vb)
@@ -575,7 +577,8 @@ extern "C" int glu_quantize(const void *x, int64_t x_stride, void *q, int64_t q_
     info.vec_bytes = vb ? vb : E;
     info.unroll = by_block ? 64 : nv * V;
     info.threads = threads;
-    info.grid = int32_t(grid.x * grid.y > INT32_MAX ? INT32_MAX : grid.x * grid.y);
+    const uint64_t all = uint64_t(grid.x) * grid.y * grid.z;
+    info.grid = int32_t(all > INT32_MAX ? INT32_MAX : all);
     info.path = 10;
     info.vector_units = srows * groups;
     glu::record_launch(info);

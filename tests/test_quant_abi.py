@@ -41,6 +41,18 @@ def test_quantize():
     assert quantize() == CUDA and quantize(block=128, dtype=F32, sx=300) == CUDA
 
 
+def test_quantize_the_widest_rows():
+    """Up to 2^28 columns, whatever the accesses: whole pieces of 32 and 16
+    bytes, single elements for odd widths and bases."""
+    far = {"q": BASE + (1 << 31), "s": BASE + (1 << 32)}
+    for cols in ((1 << 28) - 1, 1 << 28, (1 << 27) - 1, (1 << 27) + 8, 134215681):
+        for dtype in (F32, F16, BF16):
+            for block in (1, 128):
+                assert quantize(rows=1, cols=cols, dtype=dtype, block=block, **far) == CUDA, (cols, dtype, block)
+                assert quantize(x=BASE + 4, rows=1, cols=cols, dtype=dtype, block=block, **far) == CUDA
+    assert quantize(rows=1, cols=(1 << 28) + 1, **far) == SHAPE
+
+
 def norm(x=BASE, sx=256, r=BASE + MB, sr=256, g=BASE + 2 * MB, h=BASE + 3 * MB, sh=256, q=BASE + 4 * MB, sq=256,
          s=BASE + 5 * MB, ss=2, rstd=BASE + 6 * MB, rows=4, cols=256, eps=1e-5, dtype=BF16):
     return glu.glu_add_rmsnorm_q(x, sx, r, sr, g, h, sh, q, sq, s, ss, rstd, rows, cols, eps, dtype, None)

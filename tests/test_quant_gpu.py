@@ -170,6 +170,25 @@ def test_quantize_past_32_bit_offsets():
     check_quantised(q[-112:], s[-1:], x[-112:].double(), 128, 4 * U)
 
 
+@pytest.mark.parametrize("dt,cols", [("f32", 1 << 28), ("bf16", (1 << 28) - 1), ("f32", (1 << 27) + 5)])
+def test_quantize_the_widest_rows(dt, cols):
+    """Rows with more stretches than one dimension of a grid counts: every block's scale and values."""
+    g = gen(cols % 1000)
+    x = torch.randint(-7, 8, (1, cols), generator=g, device="cuda", dtype=torch.int8).to(DT[dt])
+    at = torch.arange(0, cols, 128, device="cuda")
+    x[0, at] = (8 + at // 128 % 119).to(DT[dt])         # each block's maximum, 8 to 126
+    top = x[0, at].float()
+    sbuf = torch.full((1, at.numel() + 8), 3.0, device="cuda")
+    qbuf = torch.full((1, cols + 256), 0x55, dtype=torch.uint8, device="cuda")
+    q, s = glu.quantize(x, q=qbuf.view(FP8)[:, :cols], scale=sbuf[:, :at.numel()])
+    assert torch.equal(s[0], top / torch.full_like(top, 448))
+    assert torch.all(q[0, at].float() == 448)
+    assert torch.all(sbuf[0, at.numel():] == 3.0) and torch.all(qbuf[0, cols:] == 0x55)
+    for lo in range(0, cols, 1 << 24):
+        part = slice(lo, min(cols, lo + (1 << 24)))
+        check_quantised(q[:, part], s[:, lo // 128:-(-part.stop // 128)], x[:, part].double(), 1, 4 * U)
+
+
 # ---------------------------------------------------------------- add + RMSNorm
 
 # y = s * rstd * gamma: the sum of squares has at most 64 / 2 chained roundings
