@@ -455,6 +455,7 @@ extern "C" int glu_add_rmsnorm_q(const void *x, int64_t x_stride, const void *re
         for (int i = 0; i < o; ++i)
             if (glu::overlap(all[i], all[o])) return GLU_ERR_ALIAS;
     if (uintptr_t(scale) % 4 || (rstd && uintptr_t(rstd) % 4)) return GLU_ERR_STRIDE;
+    if ((uintptr_t(x) | uintptr_t(residual) | uintptr_t(gamma) | uintptr_t(h)) % uintptr_t(E)) return GLU_ERR_STRIDE;
 
     // q's accesses are V bytes wide: a quarter or half of the others'
     int vb = access_bytes(uintptr_t(x) | uintptr_t(residual) | uintptr_t(gamma) | uintptr_t(h) |
@@ -532,7 +533,7 @@ extern "C" int glu_quantize(const void *x, int64_t x_stride, void *q, int64_t q_
         !glu::span(scale, srows, scale_stride, groups, 4, &ss))
         return GLU_ERR_SHAPE;
     if (glu::overlap(sx, sq) || glu::overlap(sx, ss) || glu::overlap(sq, ss)) return GLU_ERR_ALIAS;
-    if (uintptr_t(scale) % 4) return GLU_ERR_STRIDE;
+    if (uintptr_t(scale) % 4 || uintptr_t(x) % uintptr_t(E)) return GLU_ERR_STRIDE;
     int vb = access_bytes(uintptr_t(x) | uint64_t(n_cols * E) | uint64_t(x_stride * E));
     if (vb && (uintptr_t(q) | uint64_t(q_stride)) % uint64_t(vb / E)) vb = 0;
     const int V = vb ? vb / E : 4;

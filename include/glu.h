@@ -538,10 +538,11 @@ int glu_add_rmsnorm_bwd(const void *dy, int64_t dy_stride,
  *     q     = e4m3(v / scale)                round to nearest, ties to even
  *
  * A NaN is held as NaN and takes no part in amax; a block with an infinity
- * holds NaN.  Scales are float matrices with their own row stride, in floats,
- * 4-byte aligned (GLU_ERR_STRIDE).  Strides of e4m3 matrices are in bytes.  In
- * this section an output's footprint, from its first to its last element, must
- * not overlap another operand's (GLU_ERR_ALIAS), except where a call says so.
+ * holds NaN.  Scales are float matrices with their own row stride, in floats.
+ * Strides of e4m3 matrices are in bytes.  Every operand lies at a multiple of its
+ * element's size (GLU_ERR_STRIDE).  In this section an output's footprint, from
+ * its first to its last element, must not overlap another operand's
+ * (GLU_ERR_ALIAS), except where a call says so.
  */
 
 /*

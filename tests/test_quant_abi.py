@@ -76,6 +76,19 @@ def test_add_rmsnorm_q():
     assert norm(h=BASE) == CUDA and norm(h=BASE + MB) == CUDA and norm(rstd=None) == CUDA and norm() == CUDA
 
 
+def test_operands_off_their_elements_boundary():
+    """An access of an element that is not at a multiple of its size would fault."""
+    for off in (1, 3):
+        assert quantize(x=BASE + off) == STRIDE and quantize(x=BASE + off, block=128, dtype=F16) == STRIDE
+        for k, at in (("x", BASE), ("r", BASE + MB), ("g", BASE + 2 * MB), ("h", BASE + 3 * MB)):
+            assert norm(**{k: at + off}) == STRIDE, k
+            assert norm(**{k: at + off}, dtype=F32, sx=300, sr=300, sh=300) == STRIDE, k
+    assert quantize(x=BASE + 2, dtype=F32) == STRIDE and norm(g=BASE + 2 * MB + 2, dtype=F32) == STRIDE
+    # on their boundary, and q anywhere
+    assert quantize(x=BASE + 2, q=BASE + MB + 1) == CUDA and quantize(x=BASE + 4, dtype=F32) == CUDA
+    assert norm(x=BASE + 2, r=BASE + MB + 6, g=BASE + 2 * MB + 2, h=BASE + 3 * MB + 2, q=BASE + 4 * MB + 3) == CUDA
+
+
 def nt(a=BASE, sa=256, s=BASE + MB, ss=2, b=BASE + 2 * MB, sb=256, t=BASE + 3 * MB, st=2, d=BASE + 4 * MB, sd=384,
        M=8, K=256, N=384, dtype=BF16):
     return glu.glu_gemm_q_nt(a, sa, s, ss, b, sb, t, st, d, sd, M, K, N, dtype, None)
