@@ -294,9 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit<CTAS>(saddr(&acc_full[ab]));     // the tile's accumulator is complete
                 }
                 mma_commit<CTAS>(saddr(done));
+                // no MMA may still read shared memory or write tensor memory
+                // (block 1 of a pair waits behind its epilogue: a wait from here
+                // would span the whole grid's work, longer than a wait may last)
+                if (!wait_parity(saddr(done), 0)) atomicAdd(&g_gemm_timeouts, 1u);
             }
-            // no MMA may still read this block's shared memory or write its tensor memory
-            if (!wait_parity(saddr(done), 0)) atomicAdd(&g_gemm_timeouts, 1u);
         }
     } else {
         // epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. +31, one row per thread
@@ -380,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every box this warp stored has left shared memory and reached global memory
         if (lane == 0 && n_boxes > 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (rank == 1 && warp == 2 && !wait_parity(saddr(done), 0) && lane == 0) atomicAdd(&g_gemm_timeouts, 1u);
         __syncwarp();
     }
 

@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     uint64_t *acc_empty = used + ST;        // [2]: both blocks' epilogues have read a buffer of sums
     uint64_t *sc_full = acc_empty + 2;      // [kChunks]: a chunk of scales is in shared memory
     uint64_t *sc_empty = sc_full + kChunks;
-    uint64_t *done = sc_empty + kChunks;
+    uint64_t *done = sc_empty + kChunks;    // every MMA of the pair done
     uint64_t *maxbar = done + 1;            // [4]: both column halves of 32 rows have their maxima
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(maxbar + 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(maxbar + 4) + 1;
@@ -516,8 +516,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 }
                 if (elect_one()) mma_commit<2>(saddr(done));
                 __syncwarp();
+                // (in block 1 a scale warp waits for this, below: a wait from
+                // here would span the whole grid's work, longer than a wait may
+                // last, and in the summing warps it would cost them registers)
+                if (!wait_parity(saddr(done), 0) && lane == 0) atomicAdd(&g_q_timeouts, 1u);
             }
-            if (!wait_parity(saddr(done), 0) && lane == 0) atomicAdd(&g_q_timeouts, 1u);
         } else if (warp >= 2) {
             // scales: this thread prepares two of the block's 128 rows
             const int id = (warp - 2) * 32 + lane;
@@ -562,6 +565,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     if (lane == 0) arrive_local(saddr(&sc_full[slot]));
                 }
             }
+            // two chunks of K blocks are left at most
+            if (rank == 1 && warp == 2 && !wait_parity(saddr(done), 0) && lane == 0) atomicAdd(&g_q_timeouts, 1u);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");

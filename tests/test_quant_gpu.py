@@ -828,6 +828,29 @@ def test_two_calls_at_once():
     assert all(torch.equal(d, c[4]) for k, c in enumerate(cases) for d in got[k])
 
 
+@pytest.mark.parametrize("bits", [8, 16])
+def test_a_long_product_counts_no_timeout(bits):
+    """A product that takes more than the second a wait may last (no single wait
+    does): the right result, and no timeout is counted."""
+    n, K = (131072, 163840) if bits == 8 else (98304, 131072)
+    need = 2 * n * K * bits // 8 + 2 * n * n
+    if torch.cuda.mem_get_info()[0] < need + (4 << 30):
+        pytest.skip(f"needs {need >> 30} GB")
+    before = glu.glu_wait_timeouts()
+    if bits == 8:
+        a, b = (torch.full((n, K), v, dtype=torch.uint8, device="cuda").view(FP8) for v in (0x38, 0x40))   # 1 and 2
+        d = glu.gemm_q_nt(a, torch.full((n, K // 128), 2.0 ** -10, device="cuda"), b,
+                          torch.full((n // 128, K // 128), 2.0 ** -8, device="cuda"))
+        want = 2 * K * 2.0 ** -18
+    else:
+        a, b = (torch.full((n, K), v, dtype=torch.bfloat16, device="cuda") for v in (1.0, 2.0 ** -18))
+        d = glu.gemm_nt(a, b)
+        want = K * 2.0 ** -18
+    torch.cuda.synchronize()
+    assert glu.glu_wait_timeouts() == before
+    assert float(d.min()) == float(d.max()) == want
+
+
 def test_modules():
     from glu_activation_mlps_gb300.autograd import FusedAddRMSNorm, GatedMLP, QuantGatedMLP
     torch.manual_seed(0)
