@@ -166,10 +166,13 @@ class QuantGatedMLP(nn.Module):
     scale for each 128 x 128 block, held as buffers, and activations quantised by
     rows.  ``from_mlp`` quantises a GatedMLP; ``from_mlps`` several into the
     experts of one module, whose forward takes the rows sorted by expert and
-    their offsets."""
+    their offsets.  Results come in ``dtype`` (float16 or bfloat16), by default
+    the weights' type, bfloat16 for float32 weights."""
 
     def __init__(self, gate, up, down, act: str = "silu", dtype=torch.bfloat16):
         super().__init__()
+        if dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError(f"dtype must be float16 or bfloat16, not {dtype}")
         self.act, self.dtype = _check_act(act), dtype
         for name, w in (("gate", gate), ("up", up), ("down", down)):
             # rows on 16-byte boundaries, the products' rule: quantize lays them out so
@@ -177,16 +180,24 @@ class QuantGatedMLP(nn.Module):
             self.register_buffer(f"{name}_weight", q)
             self.register_buffer(f"{name}_scale", s)
 
-    @classmethod
-    def from_mlp(cls, mlp: GatedMLP):
-        gate, up = mlp._gate_up_weights()
-        return cls(gate, up, mlp.down_proj.weight, mlp.act, mlp.down_proj.weight.dtype)
+    @staticmethod
+    def _result_type(weight, dtype):
+        if dtype is None:
+            return torch.bfloat16 if weight.dtype == torch.float32 else weight.dtype
+        return dtype
 
     @classmethod
-    def from_mlps(cls, mlps):
+    def from_mlp(cls, mlp: GatedMLP, dtype=None):
+        gate, up = mlp._gate_up_weights()
+        down = mlp.down_proj.weight
+        return cls(gate, up, down, mlp.act, cls._result_type(down, dtype))
+
+    @classmethod
+    def from_mlps(cls, mlps, dtype=None):
         gates, ups = zip(*(m._gate_up_weights() for m in mlps))
         down = [m.down_proj.weight for m in mlps]
-        return cls(torch.stack(gates), torch.stack(ups), torch.stack(down), mlps[0].act, down[0].dtype)
+        return cls(torch.stack(gates), torch.stack(ups), torch.stack(down), mlps[0].act,
+                   cls._result_type(down[0], dtype))
 
     @torch.no_grad()
     def forward(self, x, scale=None, offsets=None):

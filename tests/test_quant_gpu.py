@@ -882,6 +882,26 @@ def test_modules():
     assert set(one.state_dict()) == {f"{n}_{k}" for n in ("gate", "up", "down") for k in ("weight", "scale")}
 
 
+def test_module_from_f32_weights():
+    """Weights of torch's default type: results come in bf16, or in the type asked for."""
+    from glu_activation_mlps_gb300.autograd import GatedMLP, QuantGatedMLP
+    torch.manual_seed(1)
+    mlp = GatedMLP(256, 300, device="cuda")
+    x = torch.randn(9, 256, device="cuda")
+    for module, dt in ((QuantGatedMLP.from_mlp(mlp), torch.bfloat16),
+                       (QuantGatedMLP.from_mlps([mlp, mlp]), torch.bfloat16),
+                       (QuantGatedMLP.from_mlp(mlp, dtype=torch.float16), torch.float16)):
+        off = None if module.gate_weight.dim() == 2 else cuts([4, 5])
+        out = module(x, offsets=off)
+        q, s = glu.quantize(x)
+        names = ("gate", "up", "down")
+        want = glu.mlp_q_fwd(q, s, *(getattr(module, f"{n}_{k}") for n in names for k in ("weight", "scale")),
+                             dtype=dt, offsets=off)
+        assert out.dtype == dt and torch.equal(out, want)
+    with pytest.raises(ValueError):
+        QuantGatedMLP.from_mlp(mlp, dtype=torch.float32)
+
+
 def test_refusals():
     x = torch.zeros(4, 256, device="cuda", dtype=torch.bfloat16)
     q, s = glu.quantize(x)
