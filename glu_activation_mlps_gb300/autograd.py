@@ -161,13 +161,25 @@ class GatedMLP(nn.Module):
         return self.down_proj(h)
 
 
+def _rows16(q):
+    """q with rows on 16-byte boundaries (a copy to another device may pack them)."""
+    K = q.shape[-1]
+    if q.stride(-1) == 1 and all(s % 16 == 0 for s in q.stride()[:-1]):
+        return q
+    wide = torch.zeros((*q.shape[:-1], K + -K % 16), dtype=torch.uint8, device=q.device)
+    wide[..., :K] = q.view(torch.uint8)
+    return wide.view(q.dtype)[..., :K]
+
+
 class QuantGatedMLP(nn.Module):
     """A gated MLP in 8-bit floating point for inference: e4m3 weights with a
     scale for each 128 x 128 block, held as buffers, and activations quantised by
     rows.  ``from_mlp`` quantises a GatedMLP; ``from_mlps`` several into the
     experts of one module, whose forward takes the rows sorted by expert and
     their offsets.  Results come in ``dtype`` (float16 or bfloat16), by default
-    the weights' type, bfloat16 for float32 weights."""
+    the weights' type, bfloat16 for float32 weights.  Casting the module (to,
+    half, bfloat16) sets that type, where it is one of the two, and leaves the
+    weights and scales as they are."""
 
     def __init__(self, gate, up, down, act: str = "silu", dtype=torch.bfloat16):
         super().__init__()
@@ -198,6 +210,28 @@ class QuantGatedMLP(nn.Module):
         down = [m.down_proj.weight for m in mlps]
         return cls(torch.stack(gates), torch.stack(ups), torch.stack(down), mlps[0].act,
                    cls._result_type(down[0], dtype))
+
+    def _apply(self, fn, recurse=True):
+        # fn moves and casts floating-point tensors: weights and scales go through
+        # it as integers, which it only moves
+        bits = {torch.float8_e4m3fn: torch.uint8, torch.float32: torch.int32}
+        held = {k: b for k, b in self._buffers.items() if b is not None and b.dtype in bits}
+        done = {}
+        for k, b in held.items():
+            t = fn(b.view(bits[b.dtype]))
+            if t.dtype != bits[b.dtype]:
+                raise TypeError("8-bit weights and their scales keep their types")
+            t = t.view(b.dtype)
+            done[k] = _rows16(t) if b.dtype == torch.float8_e4m3fn else t
+        dtype = fn(torch.empty(0, dtype=self.dtype)).dtype
+        self._buffers.update(dict.fromkeys(held))       # what remains goes the usual way
+        try:
+            super()._apply(fn, recurse)
+        finally:
+            self._buffers.update(done)
+        if dtype in (torch.float16, torch.bfloat16):
+            self.dtype = dtype
+        return self
 
     @torch.no_grad()
     def forward(self, x, scale=None, offsets=None):

@@ -902,6 +902,42 @@ def test_module_from_f32_weights():
         QuantGatedMLP.from_mlp(mlp, dtype=torch.float32)
 
 
+def test_module_is_moved_and_cast():
+    """Casting the module leaves the 8-bit weights and their scales as they are
+    and sets the type of its results; moving it keeps rows on 16-byte boundaries
+    at sizes that are no multiple of 16."""
+    import copy
+    from glu_activation_mlps_gb300.autograd import GatedMLP, QuantGatedMLP
+    torch.manual_seed(2)
+    mlps = [GatedMLP(250, 301, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    x = torch.randn(9, 250, device="cuda", dtype=torch.bfloat16)
+    for module, off in ((QuantGatedMLP.from_mlp(mlps[0]), None), (QuantGatedMLP.from_mlps(mlps), cuts([4, 5]))):
+        held = {k: v.clone() for k, v in module.state_dict().items()}
+        want = {dt: copy.deepcopy(module) for dt in (torch.bfloat16, torch.float16)}
+        for dt, m in want.items():
+            m.dtype = dt
+        want = {dt: m(x, offsets=off) for dt, m in want.items()}
+        steps = [(lambda m: m.half(), torch.float16), (lambda m: m.to(torch.bfloat16), torch.bfloat16),
+                 (lambda m: m.float(), torch.bfloat16), (lambda m: m.double(), torch.bfloat16),
+                 (lambda m: m.cpu().cuda(), torch.bfloat16), (lambda m: m.to("cpu").to("cuda", torch.float16), torch.float16),
+                 (copy.deepcopy, torch.float16)]
+        for step, dt in steps:
+            module = step(module)
+            for k, v in module.state_dict().items():
+                assert v.dtype == held[k].dtype and torch.equal(v.view(torch.uint8), held[k].view(torch.uint8)), k
+            out = module(x, offsets=off)
+            assert out.dtype == dt and torch.equal(out, want[dt])
+        # inside another module, as a model casts its parts
+        model = torch.nn.Sequential(module).to(torch.bfloat16)
+        assert torch.equal(model[0](x, offsets=off), want[torch.bfloat16])
+        # another module's weights
+        other = QuantGatedMLP.from_mlp(mlps[1]) if off is None else QuantGatedMLP.from_mlps(mlps[::-1])
+        other.load_state_dict(module.state_dict())
+        assert torch.equal(other(x, offsets=off), want[torch.bfloat16])
+        with pytest.raises(TypeError):
+            module.type(torch.float16)
+
+
 def test_refusals():
     x = torch.zeros(4, 256, device="cuda", dtype=torch.bfloat16)
     q, s = glu.quantize(x)
