@@ -206,6 +206,8 @@ class QuantGatedMLP(nn.Module):
 
     @classmethod
     def from_mlps(cls, mlps, dtype=None):
+        if len({m.act for m in mlps}) > 1:
+            raise ValueError("the experts of a module have one activation")
         gates, ups = zip(*(m._gate_up_weights() for m in mlps))
         down = [m.down_proj.weight for m in mlps]
         return cls(torch.stack(gates), torch.stack(ups), torch.stack(down), mlps[0].act,

@@ -229,3 +229,13 @@ def test_python_layer_refuses():
         glu.add_rmsnorm_q(x, x, x[0])
     with pytest.raises(ValueError):
         glu.gemm_q_nt(q, s, q, s)
+
+
+def test_experts_of_one_activation():
+    """A module of experts has one activation: MLPs of different ones are refused."""
+    from glu_activation_mlps_gb300.autograd import GatedMLP, QuantGatedMLP
+    mlps = [GatedMLP(16, 32, act=act) for act in ("silu", "relu", "silu")]
+    with pytest.raises(ValueError, match="one activation"):
+        QuantGatedMLP.from_mlps(mlps)
+    with pytest.raises(ValueError, match="CUDA"):       # past that check, at weights that are not on a device
+        QuantGatedMLP.from_mlps([mlps[0], mlps[2]])
