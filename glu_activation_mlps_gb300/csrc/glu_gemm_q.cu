@@ -10,8 +10,9 @@
 // tcgen05.mma kind::f8f6f4 sums the 128 products of one block (fp32, in tensor
 // memory); the epilogue warps read that block's sums with tcgen05.ld and add
 // them, times sa * sw, to fp32 sums in registers, while the tensor cores work
-// on the next block in the other half of tensor memory.  So any float scale is
-// exact up to one rounding, and no sum over more than 128 terms is left to the
+// on the next block in the other half of tensor memory.  So scales need not be
+// powers of two: sa * sw is rounded once to fp32 (it loses bits below 2^-126) and
+// each block's sum once, and no sum over more than 128 terms is left to the
 // tensor core.
 //
 // Two kernels:

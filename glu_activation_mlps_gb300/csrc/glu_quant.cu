@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_q_kernel(const NormParams p)
     // y / scale = s gamma 448 / max |s gamma|: rstd cancels, and with it a
     // rounding of every value, and goes into the scale alone; where it is far
     // from 1 it stays with the values, whose products with gamma might leave the
-    // range of floats without it.
+    // range of floats without it (near 1, |s| < 2^18, so gamma may reach 2^100).
     const bool near1 = rstd > 0.0009765625f && rstd < 1024.0f;
     const float pre = near1 ? 1.0f : rstd, post = near1 ? rstd : 1.0f;
 #pragma unroll

@@ -569,7 +569,9 @@ int glu_quantize(const void *x, int64_t x_stride,
  *
  * x, residual, gamma, h, rstd, eps, n_cols <= 32768 and dtype as there: h may
  * be exactly x or exactly residual, rstd may be NULL.  q and scale as in
- * glu_quantize; they overlap nothing.  glu_last_launch reports path = 9.
+ * glu_quantize; they overlap nothing.  s * gamma has to be a finite float (rstd
+ * may be left to the scale): any gamma below 2^100 will do.  glu_last_launch
+ * reports path = 9.
  */
 int glu_add_rmsnorm_q(const void *x, int64_t x_stride,
                       const void *residual, int64_t res_stride,
@@ -587,7 +589,9 @@ int glu_add_rmsnorm_q(const void *x, int64_t x_stride,
  *                     a_scale[m, b] * b_scale[n / 128, b] * sum_{k in b} a[m, k] * b[n, k])
  *
  * the inner sums of 128 products in the tensor core's fp32, the outer ones in
- * fp32 with one rounding per block, one rounding to `dtype` at the end.
+ * fp32 with one rounding per block, one rounding to `dtype` at the end.  a_scale
+ * * b_scale is formed first, in fp32: scales whose product is no normal float
+ * (below 2^-126) lose bits, one that overflows makes the block infinite or NaN.
  *   a, a_stride              M x K e4m3, a_scale M x ceil(K / 128).
  *   b, b_stride              N x K e4m3 (row n holds output feature n), b_scale
  *                            ceil(N / 128) x ceil(K / 128).
@@ -611,7 +615,7 @@ int glu_gemm_q_nt(const void *a, int64_t a_stride, const float *a_scale, int64_t
  *     y, y_scale = quantised (act(x . w_gate) * (x . w_up))
  *
  * with both products as in glu_gemm_q_nt, kept in fp32 through the activation
- * and the quantisation.
+ * and the quantisation.  A NaN among the products is one in its own column of y.
  *   x, x_stride, x_scale         M x K.
  *   w_gate, w_up, w_stride       I x K each, one row stride; gate_scale and
  *                                up_scale with one row stride.

@@ -849,6 +849,8 @@ def test_a_long_product_counts_no_timeout(bits):
     torch.cuda.synchronize()
     assert glu.glu_wait_timeouts() == before
     assert float(d.min()) == float(d.max()) == want
+    del a, b, d
+    torch.cuda.empty_cache()
 
 
 def test_modules():
