@@ -265,6 +265,20 @@ def test_add_rmsnorm_q_tiny_values(dt):
         check_quantised(q[keep], s[keep], y[keep], 1, NORM_REL, 2.0 ** -120)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_add_rmsnorm_q_large_gammas(dt):
+    """Gammas just below 2^100 on rows from 2^-9 to 2^14 (rstd in the scale, or
+    with the values), one value of a row far above the rest."""
+    g = gen(78)
+    x = randn(g, 24, 8192) * torch.exp2(torch.arange(-9, 15, device="cuda").float())[:, None]
+    x[:, 77] *= 64
+    x = x.to(DT[dt])
+    gamma = (2.0 ** 100 * (1 - 2.0 ** -8) * (1 - torch.rand(8192, generator=g, device="cuda") / 4)).to(DT[dt])
+    assert float(gamma.max()) < 2.0 ** 100
+    h, q, s, rstd = glu.add_rmsnorm_q(x, torch.zeros_like(x), gamma, 1e-5, rstd=True)
+    check_norm(x, torch.zeros_like(x), gamma, 1e-5, h, q, s, rstd)
+
+
 def test_add_rmsnorm_q_zero_rows_and_nan():
     x = torch.zeros(3, 256, dtype=torch.bfloat16, device="cuda")
     x[1, 3] = float("nan")
