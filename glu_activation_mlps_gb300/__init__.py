@@ -39,7 +39,9 @@ EXPORTS = ("glu_fwd", "glu_bwd", "glu_fwd_host", "glu_bwd_host", "glu_fwd_host_n
            "glu_gemm_nt", "glu_mlp_fwd", "glu_mlp_workspace_bytes",
            "glu_add_rmsnorm_fwd", "glu_add_rmsnorm_bwd",
            "glu_quantize", "glu_add_rmsnorm_q", "glu_gemm_q_nt", "glu_gemm_q_fwd", "glu_gemm_q_grouped_nt",
-           "glu_gemm_q_grouped_fwd", "glu_mlp_q_fwd", "glu_mlp_q_workspace_bytes")
+           "glu_gemm_q_grouped_fwd", "glu_mlp_q_fwd", "glu_mlp_q_workspace_bytes",
+           "glu_linear_ce_fwd", "glu_linear_ce_bwd", "glu_linear_distill_fwd", "glu_linear_distill_bwd",
+           "glu_linear_ce_workspace_bytes", "glu_linear_distill_workspace_bytes")
 
 
 class GluError(RuntimeError):
@@ -152,6 +154,22 @@ def lib() -> ctypes.CDLL:
             L.glu_mlp_q_fwd.restype = ci
             L.glu_mlp_q_workspace_bytes.argtypes = [i64, i64]
             L.glu_mlp_q_workspace_bytes.restype = sz
+            L.glu_linear_ce_fwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, i64, i64, ci, vp, sz, vp]
+            L.glu_linear_ce_fwd.restype = ci
+            L.glu_linear_ce_bwd.argtypes = [vp, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, i64, i64, i64, ci, vp,
+                                            sz, vp]
+            L.glu_linear_ce_bwd.restype = ci
+            fl = ctypes.c_float
+            L.glu_linear_distill_fwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, fl, vp, vp, vp, i64, i64, i64,
+                                                 i64, ci, ci, vp, sz, vp]
+            L.glu_linear_distill_fwd.restype = ci
+            L.glu_linear_distill_bwd.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, i64, fl, vp, vp, vp, i64, vp, i64,
+                                                 i64, i64, i64, i64, ci, ci, vp, sz, vp]
+            L.glu_linear_distill_bwd.restype = ci
+            L.glu_linear_ce_workspace_bytes.argtypes = [i64, i64, i64, ci]
+            L.glu_linear_ce_workspace_bytes.restype = sz
+            L.glu_linear_distill_workspace_bytes.argtypes = [i64, i64, i64, i64, ci]
+            L.glu_linear_distill_workspace_bytes.restype = sz
             _lib = L
     return _lib
 
@@ -317,6 +335,41 @@ def glu_mlp_q_fwd(x, x_stride, x_scale, x_scale_stride, w_gate, w_up, w_stride, 
 
 def glu_mlp_q_workspace_bytes(M, I) -> int:
     return lib().glu_mlp_q_workspace_bytes(M, I)
+
+
+def glu_linear_ce_fwd(x, x_stride, w, w_stride, target, loss, lse, N, H, V, dtype, workspace, workspace_bytes,
+                      stream) -> int:
+    return lib().glu_linear_ce_fwd(x, x_stride, w, w_stride, target, loss, lse, N, H, V, dtype, workspace,
+                                   workspace_bytes, stream)
+
+
+def glu_linear_ce_bwd(dloss, x, x_stride, w, w_stride, target, loss, lse, dx, dx_stride, dw, dw_stride, N, H, V, dtype,
+                      workspace, workspace_bytes, stream) -> int:
+    return lib().glu_linear_ce_bwd(dloss, x, x_stride, w, w_stride, target, loss, lse, dx, dx_stride, dw, dw_stride, N,
+                                   H, V, dtype, workspace, workspace_bytes, stream)
+
+
+def glu_linear_distill_fwd(x, x_stride, w, w_stride, index, index_stride, logit, logit_stride, temperature, loss, lse,
+                           top_logits, N, H, V, K, dtype, logit_dtype, workspace, workspace_bytes, stream) -> int:
+    return lib().glu_linear_distill_fwd(x, x_stride, w, w_stride, index, index_stride, logit, logit_stride,
+                                        temperature, loss, lse, top_logits, N, H, V, K, dtype, logit_dtype, workspace,
+                                        workspace_bytes, stream)
+
+
+def glu_linear_distill_bwd(dloss, x, x_stride, w, w_stride, index, index_stride, logit, logit_stride, temperature,
+                           lse, top_logits, dx, dx_stride, dw, dw_stride, N, H, V, K, dtype, logit_dtype, workspace,
+                           workspace_bytes, stream) -> int:
+    return lib().glu_linear_distill_bwd(dloss, x, x_stride, w, w_stride, index, index_stride, logit, logit_stride,
+                                        temperature, lse, top_logits, dx, dx_stride, dw, dw_stride, N, H, V, K, dtype,
+                                        logit_dtype, workspace, workspace_bytes, stream)
+
+
+def glu_linear_ce_workspace_bytes(N, H, V, backward) -> int:
+    return lib().glu_linear_ce_workspace_bytes(N, H, V, backward)
+
+
+def glu_linear_distill_workspace_bytes(N, H, V, K, backward) -> int:
+    return lib().glu_linear_distill_workspace_bytes(N, H, V, K, backward)
 
 
 def glu_get_tuning() -> dict:
@@ -627,7 +680,8 @@ def _on_stream(stream, call, *args, **kw):
         if isinstance(t, torch.Tensor):
             t.record_stream(stream)
     for t in (out,) if isinstance(out, torch.Tensor) else out:
-        t.record_stream(here)
+        if t is not None:
+            t.record_stream(here)
     return out
 
 
@@ -895,6 +949,171 @@ def mlp_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, w_down, down_scale
     if st:
         raise GluError(st, "glu_mlp_q_fwd")
     return out
+
+
+# ---- losses over a vocabulary ------------------------------------------------------
+
+def _loss_in(x, w):
+    """(N, x's row stride, w's row stride, H, V, leading shape) of hidden rows and an output projection."""
+    if w.dim() != 2 or w.shape[1] != x.shape[-1] or w.dtype != x.dtype:
+        raise ValueError("w must be (V, H) with H = x.shape[-1] and x's dtype")
+    n_rows, x_stride = _mat(x, "x")
+    return n_rows, x_stride, _mat(w, "w")[1], x.shape[-1], w.shape[0], x.shape[:-1]
+
+
+def _per_row(t, shape, name, like):
+    """A float32 tensor of one entry a row: t, checked, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=torch.float32, device=like.device)
+    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)}")
+    return t
+
+
+def _target(target, lead):
+    import torch
+    if target.dtype != torch.int64 or target.shape != lead or not target.is_contiguous():
+        raise ValueError(f"target must be a contiguous int64 tensor of shape {tuple(lead)}")
+    return target.data_ptr()
+
+
+def _teacher(index, logit, lead):
+    """(K, index's row stride, logit's row stride, logit's dtype code)."""
+    import torch
+    if index.dtype != torch.int64 or index.dim() < 1 or index.shape[:-1] != lead or logit.shape != index.shape:
+        raise ValueError(f"index (int64) and logit must both be {(*lead, 'K')}")
+    return index.shape[-1], _mat(index, "index")[1], _mat(logit, "logit")[1], _dtype_code(logit)
+
+
+def _gradient(t, like, name):
+    """(tensor or None, its row stride) of a gradient: None allocates it, False leaves it out."""
+    import torch
+    if t is False:
+        return None, 0
+    if t is None:
+        t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    elif t.shape != like.shape or t.dtype != like.dtype:
+        raise ValueError(f"{name} has the wrong shape or dtype")
+    return t, _mat(t, name)[1]
+
+
+def _loss_workspace(workspace, n_bytes, like):
+    import torch
+    if workspace is None:
+        return torch.empty(max(256, n_bytes), dtype=torch.uint8, device=like.device)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    return workspace
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def linear_ce(x, w, target, *, loss=None, lse=None, workspace=None, stream=None):
+    """(loss, lse): softmax cross entropy of the rows x (..., H) under the output
+    projection w (V, H), whose logits x @ w^T are not kept.  ``target`` (int64,
+    x's leading shape): a value outside 0 .. V - 1 (such as -100) is none, and the
+    row's loss and lse are 0.  x and w are f16 or bf16, loss and lse float32.  The
+    workspace (a uint8 tensor of glu_linear_ce_workspace_bytes(N, H, V, 0) bytes) is
+    allocated here when not given."""
+    if stream is not None:
+        return _on_stream(stream, linear_ce, x, w, target, loss=loss, lse=lse, workspace=workspace)
+    dev = _same_device(x, w, target, loss, lse, workspace)
+    n_rows, x_stride, w_stride, H, V, lead = _loss_in(x, w)
+    code = _dtype_code(x)
+    t = _target(target, lead)
+    loss, lse = _per_row(loss, lead, "loss", x), _per_row(lse, lead, "lse", x)
+    workspace = _loss_workspace(workspace, glu_linear_ce_workspace_bytes(n_rows, H, V, 0), x)
+    st = glu_linear_ce_fwd(x.data_ptr(), x_stride, w.data_ptr(), w_stride, t, loss.data_ptr(), lse.data_ptr(), n_rows,
+                           H, V, code, workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
+    if st:
+        raise GluError(st, "glu_linear_ce_fwd")
+    return loss, lse
+
+
+def linear_ce_bwd(dloss, x, w, target, loss, lse, *, dx=None, dw=None, workspace=None, stream=None):
+    """(dx, dw): gradients of linear_ce's loss, given what it returned for the
+    same x, w and target.  ``dloss`` (float32, one a row) is the gradient arriving
+    at the loss.  ``dx`` and ``dw`` may be given, or False: not wanted (None is
+    returned in its place).  The workspace (uint8, glu_linear_ce_workspace_bytes(N,
+    H, V, 1) bytes, or less: smaller pieces of the vocabulary) is allocated here
+    when not given."""
+    if stream is not None:
+        return _on_stream(stream, linear_ce_bwd, dloss, x, w, target, loss, lse, dx=dx, dw=dw, workspace=workspace)
+    n_rows, x_stride, w_stride, H, V, lead = _loss_in(x, w)
+    code = _dtype_code(x)
+    t = _target(target, lead)
+    for v, name in ((dloss, "dloss"), (loss, "loss"), (lse, "lse")):
+        _per_row(v, lead, name, x)
+    dx, dx_stride = _gradient(dx, x, "dx")
+    dw, dw_stride = _gradient(dw, w, "dw")
+    dev = _same_device(x, w, target, dloss, loss, lse, dx, dw, workspace)
+    workspace = _loss_workspace(workspace, glu_linear_ce_workspace_bytes(n_rows, H, V, 1), x)
+    st = glu_linear_ce_bwd(dloss.data_ptr(), x.data_ptr(), x_stride, w.data_ptr(), w_stride, t, loss.data_ptr(),
+                           lse.data_ptr(), _ptr(dx), dx_stride, _ptr(dw), dw_stride, n_rows, H, V, code,
+                           workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
+    if st:
+        raise GluError(st, "glu_linear_ce_bwd")
+    return dx, dw
+
+
+def linear_distill(x, w, index, logit, temperature: float = 1.0, *, loss=None, lse=None, top_logits=None,
+                   workspace=None, stream=None):
+    """(loss, lse, top_logits): for each row of x (..., H) the divergence of the
+    student's softmax at ``temperature`` over the whole vocabulary, w (V, H), from
+    the softmax of the K top logits that a teacher kept: ``logit`` (..., K; float32,
+    f16 or bf16) of the tokens ``index`` (int64).  An entry outside 0 .. V - 1 or
+    with a logit of -inf is none; a row without entries has loss and lse 0.
+    ``top_logits`` (..., K) are the student's own logits of those tokens, which the
+    backward pass wants.  The workspace (uint8,
+    glu_linear_distill_workspace_bytes(N, H, V, K, 0) bytes) is allocated here when
+    not given."""
+    if stream is not None:
+        return _on_stream(stream, linear_distill, x, w, index, logit, temperature, loss=loss, lse=lse,
+                          top_logits=top_logits, workspace=workspace)
+    dev = _same_device(x, w, index, logit, loss, lse, top_logits, workspace)
+    n_rows, x_stride, w_stride, H, V, lead = _loss_in(x, w)
+    code = _dtype_code(x)
+    K, i_stride, l_stride, l_code = _teacher(index, logit, lead)
+    loss, lse = _per_row(loss, lead, "loss", x), _per_row(lse, lead, "lse", x)
+    top_logits = _per_row(top_logits, index.shape, "top_logits", x)
+    workspace = _loss_workspace(workspace, glu_linear_distill_workspace_bytes(n_rows, H, V, K, 0), x)
+    st = glu_linear_distill_fwd(x.data_ptr(), x_stride, w.data_ptr(), w_stride, index.data_ptr(), i_stride,
+                                logit.data_ptr(), l_stride, temperature, loss.data_ptr(), lse.data_ptr(),
+                                top_logits.data_ptr(), n_rows, H, V, K, code, l_code, workspace.data_ptr(),
+                                workspace.numel(), _raw_stream(dev))
+    if st:
+        raise GluError(st, "glu_linear_distill_fwd")
+    return loss, lse, top_logits
+
+
+def linear_distill_bwd(dloss, x, w, index, logit, lse, top_logits, temperature: float = 1.0, *, dx=None, dw=None,
+                       workspace=None, stream=None):
+    """(dx, dw): gradients of linear_distill's loss, given the lse and top_logits
+    it returned for the same arguments; dloss, dx, dw and the workspace
+    (glu_linear_distill_workspace_bytes(N, H, V, K, 1)) as in linear_ce_bwd."""
+    if stream is not None:
+        return _on_stream(stream, linear_distill_bwd, dloss, x, w, index, logit, lse, top_logits, temperature, dx=dx,
+                          dw=dw, workspace=workspace)
+    n_rows, x_stride, w_stride, H, V, lead = _loss_in(x, w)
+    code = _dtype_code(x)
+    K, i_stride, l_stride, l_code = _teacher(index, logit, lead)
+    _per_row(dloss, lead, "dloss", x)
+    _per_row(lse, lead, "lse", x)
+    _per_row(top_logits, index.shape, "top_logits", x)
+    dx, dx_stride = _gradient(dx, x, "dx")
+    dw, dw_stride = _gradient(dw, w, "dw")
+    dev = _same_device(x, w, index, logit, dloss, lse, top_logits, dx, dw, workspace)
+    workspace = _loss_workspace(workspace, glu_linear_distill_workspace_bytes(n_rows, H, V, K, 1), x)
+    st = glu_linear_distill_bwd(dloss.data_ptr(), x.data_ptr(), x_stride, w.data_ptr(), w_stride, index.data_ptr(),
+                                i_stride, logit.data_ptr(), l_stride, temperature, lse.data_ptr(),
+                                top_logits.data_ptr(), _ptr(dx), dx_stride, _ptr(dw), dw_stride, n_rows, H, V, K, code,
+                                l_code, workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
+    if st:
+        raise GluError(st, "glu_linear_distill_bwd")
+    return dx, dw
 
 
 # ---- host tensors ---------------------------------------------------------------

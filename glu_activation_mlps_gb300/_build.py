@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libglu_gb300.so")
 
 SOURCES = ["glu_api.cu", "glu_host.cu", "glu_noalloc.cu", "glu_bulk.cu", "glu_inst_bf16.cu",
            "glu_inst_f16.cu", "glu_inst_f32.cu", "glu_gemm.cu", "glu_rmsnorm.cu",
-           "glu_quant.cu", "glu_gemm_q.cu"]
+           "glu_quant.cu", "glu_gemm_q.cu", "glu_loss.cu"]
 HEADERS = ["glu_plan.h", "glu_internal.h", "glu_math.cuh", "glu_kernels.cuh", "glu_bulk.cuh", "glu_async.cuh",
            "glu_tensor.cuh", "glu_quant.cuh"]
 

@@ -733,10 +733,11 @@ int glu_version(void) { return GLU_VERSION; }
 int glu_wait_timeouts(unsigned int *count, int reset)
 {
     if (!count) return GLU_ERR_NULL;
-    unsigned int bulk = 0, gemm = 0, gemm_q = 0, rms = 0, self = 0;
+    unsigned int bulk = 0, gemm = 0, gemm_q = 0, loss = 0, rms = 0, self = 0;
     cudaError_t e = glu::bulk_timeouts(&bulk, reset != 0);
     if (e == cudaSuccess) e = glu::gemm::timeouts(&gemm, reset != 0);
     if (e == cudaSuccess) e = glu::gemmq::timeouts(&gemm_q, reset != 0);
+    if (e == cudaSuccess) e = glu::loss::timeouts(&loss, reset != 0);
     if (e == cudaSuccess) e = glu::rms::timeouts(&rms, reset != 0);
     if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&self, glu::g_selftest_timeouts, sizeof(unsigned int));
     if (e == cudaSuccess && reset) {
@@ -744,7 +745,7 @@ int glu_wait_timeouts(unsigned int *count, int reset)
         e = cudaMemcpyToSymbol(glu::g_selftest_timeouts, &zero, sizeof(unsigned int));
     }
     if (e != cudaSuccess) return cuda_fail(e);
-    *count = bulk + gemm + gemm_q + rms + self;
+    *count = bulk + gemm + gemm_q + loss + rms + self;
     return GLU_OK;
 }
 

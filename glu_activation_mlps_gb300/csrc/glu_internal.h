@@ -34,6 +34,9 @@ cudaError_t timeouts(unsigned int *count, bool reset);   // glu_rmsnorm.cu
 namespace gemmq {
 cudaError_t timeouts(unsigned int *count, bool reset);   // glu_gemm_q.cu
 }
+namespace loss {
+cudaError_t timeouts(unsigned int *count, bool reset);   // glu_loss.cu
+}
 void record_launch(const glu_launch_info_t &info);       // this thread's glu_last_launch
 // Whether p points into device memory (not pinned host or managed memory):
 // the tensor-memory accelerator and the bulk-copy engine are given device

@@ -1,0 +1,1859 @@
+// Losses over a vocabulary straight from the hidden rows x (N x H) and the output
+// projection w (V x H), on the fifth-generation tensor cores of sm_103a.  With
+// z = x w^T, s = z / T (T = 1 for the cross entropy), lse = log sum_v exp s_v:
+//
+//     cross entropy   loss = lse - z_target
+//     distillation    loss = sum_k p_k (log p_k - s_{index k} + lse),  p = softmax over k of t_k / T
+//     gradient        g_v  = dloss / T (exp(s_v - lse) - [target share of v])
+//                     dx   = g w,   dw = g^T x
+//
+// The logits are not kept.  The forward product's epilogue reduces each tile of
+// them to a maximum and a sum per row and picks the few logits the loss names;
+// the backward pass forms them again, a piece of the vocabulary at a time, and
+// its epilogue turns them into g in 16 bits, which the two gradient products
+// read: g rounds to the inputs' type because one tensor-core product takes one
+// type (relative 2^-9 or 2^-12 an entry, as the 16-bit gradients a user gets;
+// f16 entries are scaled by a power of two first, so that shares of 1 / V keep
+// their bits).  Sums are fp32 throughout.
+//
+// One kernel template runs the four products (stats, grad, data, weight) on the
+// structure of glu_gemm.cu: a persistent grid; warp 0 fills a ring of 64-deep K
+// slices with the tensor-memory accelerator (128-byte swizzle), one thread of
+// warp 1 issues tcgen05.mma, warps 2-5 read the other of two accumulators.  The
+// operands lie as the user has them: g w wants w's vocabulary as its K, g^T x
+// wants rows as K, so those operands come as MN-major tiles (64 columns x 64 K
+// to a swizzled box), which the MMA reads directly; nothing is transposed in
+// memory.
+//
+// Rows without a target take no part in any product: a first kernel lists the
+// rows that have one and, only where some have none, copies them side by side.
+// The count stays on the device; the grids are sized for all rows and their
+// tiles counted in the kernel.
+//
+// Waits are bounded as in glu_gemm.cu.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <type_traits>
+
+#include "glu.h"
+#include "glu_kernels.cuh"
+#include "glu_internal.h"
+#include "glu_tensor.cuh"
+
+namespace glu {
+namespace loss {
+
+using namespace glu::gemm;
+
+constexpr int BM = 128;                 // rows of a tile per block (tensor-memory lanes)
+constexpr int BK = 64;                  // K per stage: 64 x 2 bytes = one 128-byte swizzle row
+constexpr int kThreads = 192;           // warp 0 loads, warp 1 issues MMAs, warps 2-5 store
+constexpr int kEpiWarps = 4;
+constexpr int kRingBytes = 192 * 1024;
+constexpr int kBox = 32;                // outputs leave through 32 x 32 boxes
+constexpr int kChunkBytes = 64 * BK * 2;    // an MN-major box: 64 columns x 64 K
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+enum Mode {
+    kStats,     // z = x w^T -> per tile and row: maximum, sum of exponentials, named logits
+    kGrad,      // z = x w^T -> g
+    kData,      // g w     (K = the piece's vocabulary)
+    kWeight     // g^T x   (K = rows)
+};
+
+template <int MODE, int BN, int CTAS>
+struct Shape {
+    static constexpr bool kTransA = MODE == kWeight;
+    static constexpr bool kTransB = MODE == kData || MODE == kWeight;
+    static constexpr int kTileN = 2 * BN;                               // columns of a tile
+    static constexpr int kBRows = CTAS == 1 ? 2 * BN : BN;              // of them, loaded by one block
+    static constexpr int kTileA = BM * BK * 2;
+    static constexpr int kTileB = kBRows * BK * 2;
+    static constexpr int kStageBytes = kTileA + kTileB;
+    static constexpr int kStages = kRingBytes / kStageBytes > 8 ? 8 : kRingBytes / kStageBytes;
+    static constexpr int kTileM = BM * CTAS;
+    static constexpr int kTmemCols = 2 * kTileN <= 256 ? 256 : 512;     // two accumulators
+    static constexpr int kBars = 2 * kStages + 2 + 2 + 1;               // full, empty, acc_full, acc_empty, done
+    static constexpr int kBoxBytes = (MODE == kData || MODE == kWeight) ? kBox * kBox * 4 : kBox * kBox * 2;
+    static constexpr int kStageOut = MODE == kStats ? 0 : kEpiWarps * 2 * kBoxBytes;
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStageOut + kBars * 8 + 16;
+    static_assert(BN % 32 == 0 && kTileN <= 256, "one MMA covers the tile's columns");
+    static_assert(!kTransB || kBRows % 64 == 0, "MN-major operands come in chunks of 64 columns");
+    static_assert(kTileA % 1024 == 0 && kTileB % 1024 == 0, "swizzle atoms stay 1024-byte aligned");
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
+};
+
+struct Params {
+    const int *count;           // rows that take part; rows[] lists them
+    const int *rows;
+    int N;                      // rows of x
+    int cols;                   // columns of the output: the piece's vocabulary (stats, grad), H (data, weight)
+    int depth;                  // K: H (stats, grad), the piece's vocabulary (data); weight: the count
+    int m_rows;                 // rows of the output for weight: the piece's vocabulary
+    int n_blocks;
+    int splits;                 // data, weight: parts of K, one partial result each
+    int group_m;                // row blocks per group of the tile order
+    uint32_t a_bytes;           // bytes of the A box (stats, grad, data: rows that exist, up to 128)
+    // stats
+    float2 *part;               // [n_blocks][N]: maximum (in log2 units) and sum
+    float *named;               // cross entropy: the target's logit by listed row; distillation: [N][top] by row
+    const int64_t *target;      // cross entropy
+    const int *index;           // distillation: [N][top], sorted, INT_MAX where there is none
+    int top;
+    int64_t first;              // first token of the piece
+    float c1;                   // log2(e) / T
+    // grad
+    const float *lse, *loss, *dloss;
+    float inv_t;
+    const float *scale;         // [0] what g is scaled by, [1] its inverse
+    // data, weight
+    char *out;
+    int64_t out_stride;         // bytes
+    int vec_store, tma_store;
+    int partial;                // 1: fp32 partial results, 2: added to what is there
+    int split_rows;             // rows of one partial result
+};
+
+static __device__ unsigned int g_loss_timeouts;
+
+// Shared-memory matrix descriptor of an MN-major tile, 128-byte swizzle: atoms
+// of 64 columns x 8 K (1024 bytes); the stride byte offset is the step of 8 K,
+// the leading byte offset the step of 64 columns.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr)
+{
+    uint64_t d = 0;
+    d |= uint64_t((addr & 0x3FFFF) >> 4);
+    d |= uint64_t(kChunkBytes >> 4) << 16;
+    d |= uint64_t(1024 >> 4) << 32;
+    d |= uint64_t(1) << 46;
+    d |= uint64_t(2) << 61;
+    return d;
+}
+
+__device__ __forceinline__ void tma_add(const CUtensorMap *map, uint32_t src, int x, int y)
+{
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float v)
+{
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Element j of a row's 32 registers, j known at run time only.
+__device__ __forceinline__ float pick(const uint32_t (&g)[32], int j)
+{
+    uint32_t v = g[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) v = j == i ? g[i] : v;
+    return __uint_as_float(v);
+}
+
+// Tile t: which part of K, row block and column block.
+struct Tile {
+    int split, mb, nb;
+};
+
+__device__ __forceinline__ Tile tile_of(const Params &p, int t, int m_blocks)
+{
+    const int per_split = m_blocks * p.n_blocks;
+    Tile o;
+    o.split = t / per_split;
+    t -= o.split * per_split;
+    const int per_group = p.group_m * p.n_blocks;
+    const int first_m = (t / per_group) * p.group_m;
+    const int gsize = min(m_blocks - first_m, p.group_m);
+    const int r = t % per_group;
+    o.mb = first_m + r % gsize;
+    o.nb = r / gsize;
+    return o;
+}
+
+template <int MODE, class T, int BN, int CTAS>
+__global__ void __launch_bounds__(kThreads, 1)
+    loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                     const __grid_constant__ CUtensorMap tm_listed, const __grid_constant__ CUtensorMap tm_out,
+                     const Params p)
+{
+    using S = Shape<MODE, BN, CTAS>;
+    using Cd = Codec<T>;
+    constexpr int ST = S::kStages;
+    constexpr uint32_t kIdesc = idesc_f16(std::is_same<T, __nv_bfloat16>::value ? 1 : 0, S::kTileM, S::kTileN) |
+                                (S::kTransA ? 1u << 15 : 0u) | (S::kTransB ? 1u << 16 : 0u);
+
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = saddr(smem_raw);
+    unsigned char *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    unsigned char *ostage = smem + ST * S::kStageBytes;                 // 1024-byte aligned
+    uint64_t *full = reinterpret_cast<uint64_t *>(ostage + S::kStageOut);
+    uint64_t *empty = full + ST;
+    uint64_t *acc_full = empty + ST;
+    uint64_t *acc_empty = acc_full + 2;
+    uint64_t *done = acc_empty + 2;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(done + 1) + 1;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CTAS == 1 ? 0u : cluster_rank();
+    const int cluster = blockIdx.x / CTAS, n_clusters = gridDim.x / CTAS;
+
+    auto raise_abort = [&]() {
+        atomicAdd(&g_loss_timeouts, 1u);
+        *abort_flag = 1;
+        if constexpr (CTAS == 2) {
+            const uint32_t other = mapa(saddr(const_cast<int *>(abort_flag)), rank ^ 1u);
+            asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(other), "r"(1) : "memory");
+        }
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; ++s) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(saddr(&full[s])) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(saddr(&empty[s])) : "memory");
+        }
+        for (int b = 0; b < 2; ++b) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(saddr(&acc_full[b])) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(&acc_empty[b])),
+                         "r"(kEpiWarps * CTAS)
+                         : "memory");
+        }
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(saddr(done)) : "memory");
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<CTAS>(saddr(const_cast<uint32_t *>(tmem_slot)), S::kTmemCols);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    if constexpr (CTAS == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // What depends on how many rows take part.  With none there is still one
+    // block of rows (or one slice of K): it reads zeros and gives zeros.
+    const int count = *reinterpret_cast<const volatile int *>(p.count);
+    const bool all = count == p.N;
+    const int m_rows = MODE == kWeight ? p.m_rows : count;
+    const int m_blocks = max(1, (m_rows + S::kTileM - 1) / S::kTileM);
+    const int k_tiles = max(1, ((MODE == kWeight ? count : p.depth) + BK - 1) / BK);
+    const int per_split = (k_tiles + p.splits - 1) / p.splits;
+    const int n_tiles = m_blocks * p.n_blocks * p.splits;
+    // K slices of a part: one at least; the last parts of a K that shrank with
+    // the count read past the matrix, zeros
+    auto slices = [&](int split) { return max(1, min(per_split, k_tiles - split * per_split)); };
+    auto slice0 = [&](int split) {
+        return split * per_split < k_tiles ? split * per_split : (max(p.N, p.depth) + BK - 1) / BK;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const CUtensorMap *ma = (MODE == kStats || MODE == kGrad) && !all ? &tm_listed : &tm_a;
+            const CUtensorMap *mbp = MODE == kWeight && !all ? &tm_listed : &tm_b;
+            const uint32_t bytes = p.a_bytes + uint32_t(S::kTileB);
+            uint32_t it = 0;
+            for (int t = cluster; t < n_tiles && !*abort_flag; t += n_clusters) {
+                const Tile o = tile_of(p, t, m_blocks);
+                const int m0 = o.mb * S::kTileM + int(rank) * BM;
+                const int n0 = o.nb * S::kTileN + int(rank) * (CTAS == 1 ? 0 : BN);
+                const int n_k = slices(o.split), k0 = slice0(o.split);
+                for (int kt = 0; kt < n_k; ++kt, ++it) {
+                    const uint32_t s = it % ST, use = it / ST;
+                    if (*abort_flag) break;
+                    if (use > 0 && !wait_parity(saddr(&empty[s]), (use - 1) & 1)) {
+                        raise_abort();
+                        break;
+                    }
+                    const uint32_t st = saddr(smem + s * S::kStageBytes);
+                    const int k = (k0 + kt) * BK;
+                    // both blocks' copies count on block 0's barrier
+                    uint32_t bar = saddr(&full[s]);
+                    if (rank == 0)
+                        arrive_expect_tx_local(bar, bytes * CTAS);
+                    else
+                        bar = mapa(bar, 0);
+                    if constexpr (S::kTransA) {
+#pragma unroll
+                        for (int c = 0; c < BM / 64; ++c)
+                            tma_load<CTAS>(st + c * kChunkBytes, ma, m0 + 64 * c, k, bar);
+                    } else {
+                        tma_load<CTAS>(st, ma, k, m0, bar);
+                    }
+                    if constexpr (S::kTransB) {
+#pragma unroll
+                        for (int c = 0; c < S::kBRows / 64; ++c)
+                            tma_load<CTAS>(st + S::kTileA + c * kChunkBytes, mbp, n0 + 64 * c, k, bar);
+                    } else {
+                        tma_load<CTAS>(st + S::kTileA, mbp, k, n0, bar);
+                    }
+                }
+            }
+            // block 0 holds the barriers of every copy of the pair: wait for the
+            // last ones to land before the block may exit
+            if (rank == 0) {
+                const uint32_t first = it > uint32_t(ST) ? it - ST : 0;
+                for (uint32_t j = first; j < it; ++j)
+                    if (!wait_parity(saddr(&full[j % ST]), (j / ST) & 1)) {
+                        atomicAdd(&g_loss_timeouts, 1u);
+                        break;
+                    }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            uint32_t it = 0;
+            int lt = 0;
+            for (int t = cluster; t < n_tiles; t += n_clusters, ++lt) {
+                if (*abort_flag) break;
+                const int ab = lt & 1, use_acc = lt >> 1;
+                if (use_acc > 0 && !wait_parity(saddr(&acc_empty[ab]), (use_acc - 1) & 1)) {
+                    raise_abort();
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t d = tmem + uint32_t(ab * S::kTileN);
+                const int n_k = slices(tile_of(p, t, m_blocks).split);
+                bool ok = true;
+                for (int kt = 0; kt < n_k; ++kt, ++it) {
+                    const uint32_t s = it % ST, use = it / ST;
+                    if (!wait_parity(saddr(&full[s]), use & 1)) {
+                        raise_abort();
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t a0 = saddr(smem + s * S::kStageBytes);
+                    const uint64_t da = S::kTransA ? desc_mn_sw128(a0) : desc_sw128(a0);
+                    const uint64_t db = S::kTransB ? desc_mn_sw128(a0 + S::kTileA) : desc_sw128(a0 + S::kTileA);
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk) {
+                        // 16 K further: 32 bytes inside the swizzle row, or two
+                        // 1024-byte atoms of an MN-major tile
+                        const uint64_t sa = uint64_t(kk * (S::kTransA ? 2048 : 32) >> 4);
+                        const uint64_t sb = uint64_t(kk * (S::kTransB ? 2048 : 32) >> 4);
+                        mma<CTAS>(d, da + sa, db + sb, kIdesc, (kt | kk) != 0);
+                    }
+                    mma_commit<CTAS>(saddr(&empty[s]));
+                }
+                if (!ok) break;
+                mma_commit<CTAS>(saddr(&acc_full[ab]));
+            }
+            mma_commit<CTAS>(saddr(done));
+            if (!wait_parity(saddr(done), 0)) atomicAdd(&g_loss_timeouts, 1u);
+        }
+    } else {
+        // epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. +31, one row per thread
+        const int q = warp & 3;
+        const uint32_t lane_base = uint32_t(q * 32) << 16;
+        uint32_t n_boxes = 0;
+        float unscale = 1.0f, gscale = 1.0f;
+        if constexpr (MODE == kGrad) gscale = p.scale[0] * p.inv_t;
+        if constexpr (MODE == kData || MODE == kWeight) unscale = p.scale[1];
+        int lt = 0;
+        for (int t = cluster; t < n_tiles; t += n_clusters, ++lt) {
+            if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) break;
+            const int ab = lt & 1, use_acc = lt >> 1;
+            const Tile o = tile_of(p, t, m_blocks);
+            const int m = o.mb * S::kTileM + int(rank) * BM + q * 32 + lane;
+            const int n0 = o.nb * S::kTileN;
+            const bool live = m < m_rows;
+            // what this row needs, requested before the wait for its sums
+            int row = m;
+            int64_t tgt = -1;           // its target, from the tile's first column
+            float coef = 0.0f, shift = 0.0f, at_target = 0.0f;
+            int e = 0, next = INT32_MAX;
+            if constexpr (MODE == kStats || MODE == kGrad) {
+                if (live) {
+                    if (!all) row = p.rows[m];
+                    if (p.target) tgt = p.target[row] - p.first - n0;
+                }
+            }
+            if constexpr (MODE == kStats) {
+                if (p.index && live) {
+                    // the first of the row's sorted tokens that is not before this tile
+                    const int *list = p.index + int64_t(row) * p.top;
+                    int hi = p.top;
+                    while (e < hi) {
+                        const int mid = (e + hi) >> 1;
+                        if (list[mid] < n0)
+                            e = mid + 1;
+                        else
+                            hi = mid;
+                    }
+                    if (e < p.top) next = list[e];
+                }
+            }
+            if constexpr (MODE == kGrad) {
+                if (live) {
+                    coef = p.dloss[row] * gscale;
+                    shift = -p.lse[row] * kLog2e;
+                    // p - 1 at the target, without the cancellation
+                    if (p.target && coef != 0.0f) at_target = coef * expm1f(-p.loss[row]);
+                }
+            }
+            if constexpr (MODE == kData) {
+                if (live && !all) row = p.rows[m];
+            }
+            // tcgen05.ld is warp-collective: the whole warp takes one decision
+            const bool ok = __all_sync(0xFFFFFFFFu, wait_parity_sleep(saddr(&acc_full[ab]), use_acc & 1));
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (!ok) {
+                if (lane == 0) raise_abort();
+                break;
+            }
+            const uint32_t acc = tmem + lane_base + uint32_t(ab * S::kTileN);
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+            for (int c0 = 0; c0 < S::kTileN; c0 += 32) {
+                uint32_t g[32];
+                __syncwarp();
+                tmem_ld32(acc + uint32_t(c0), g);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                if (c0 + 32 == S::kTileN) {     // all of this tile read: hand the accumulator back
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CTAS == 1)
+                            arrive_local(saddr(&acc_empty[ab]));
+                        else
+                            arrive_cluster(mapa(saddr(&acc_empty[ab]), 0));
+                    }
+                }
+                const int left = p.cols - (n0 + c0);        // columns that exist
+                if (left <= 0) continue;
+                if constexpr (MODE == kStats) {
+                    if (tgt >= c0 && tgt < c0 + 32) p.named[m] = pick(g, int(tgt) - c0);
+                    while (next < n0 + c0 + 32) {
+                        p.named[int64_t(row) * p.top + e] = pick(g, next - n0 - c0);
+                        ++e;
+                        next = e < p.top ? p.index[int64_t(row) * p.top + e] : INT32_MAX;
+                    }
+                    if (left < 32) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) g[j] = j < left ? g[j] : 0xFF800000u;      // -inf
+                    }
+                    // running maximum and sum, in units of log2
+                    float hi = __uint_as_float(g[0]);
+#pragma unroll
+                    for (int j = 1; j < 32; ++j) hi = fmaxf(hi, __uint_as_float(g[j]));
+                    hi = fmaxf(hi * p.c1, top);
+                    const float base = hi == -INFINITY ? 0.0f : hi;
+                    float s0 = sum * exp2_fast(top - base), s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        s0 += exp2_fast(fmaf(__uint_as_float(g[j]), p.c1, -base));
+                        s1 += exp2_fast(fmaf(__uint_as_float(g[j + 1]), p.c1, -base));
+                        s2 += exp2_fast(fmaf(__uint_as_float(g[j + 2]), p.c1, -base));
+                        s3 += exp2_fast(fmaf(__uint_as_float(g[j + 3]), p.c1, -base));
+                    }
+                    sum = (s0 + s1) + (s2 + s3);
+                    top = hi;
+                } else if constexpr (MODE == kGrad) {
+                    uint32_t packed[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        float f[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float v = coef * exp2_fast(fmaf(__uint_as_float(g[j + i]), p.c1, shift));
+                            f[i] = coef == 0.0f || j + i >= left ? 0.0f : v;
+                            if (tgt == c0 + j + i) f[i] = at_target;
+                        }
+                        packed[j / 2] = Cd::put(f);
+                    }
+                    // this warp's 32 rows x 32 columns: row `lane` is 64 bytes, its
+                    // 16-byte chunk c stored at chunk c ^ ((lane / 2) % 4)
+                    const uint32_t buf = saddr(ostage) + uint32_t(q * 2 + (n_boxes & 1)) * S::kBoxBytes;
+                    if (lane == 0 && n_boxes >= 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    __syncwarp();
+                    const uint32_t at = buf + uint32_t(lane) * 64u, sw = (uint32_t(lane) >> 1) & 3u;
+#pragma unroll
+                    for (uint32_t c = 0; c < 4; ++c)
+                        st_shared16(at + ((c ^ sw) << 4), packed[4 * c], packed[4 * c + 1], packed[4 * c + 2],
+                                    packed[4 * c + 3]);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) tma_store(&tm_out, buf, n0 + c0, m - lane);
+                    ++n_boxes;
+                } else if (p.partial) {
+                    // fp32 sums of this part of K: rows of 128 bytes, chunk c at c ^ (lane % 8)
+                    const uint32_t buf = saddr(ostage) + uint32_t(q * 2 + (n_boxes & 1)) * S::kBoxBytes;
+                    if (lane == 0 && n_boxes >= 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    __syncwarp();
+                    const uint32_t at = buf + uint32_t(lane) * 128u, sw = uint32_t(lane) & 7u;
+#pragma unroll
+                    for (uint32_t c = 0; c < 8; ++c)
+                        st_shared16(at + ((c ^ sw) << 4), g[4 * c], g[4 * c + 1], g[4 * c + 2], g[4 * c + 3]);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int y = o.split * p.split_rows + m;
+                        if (p.partial == 1)
+                            tma_store(&tm_out, buf, n0 + c0, y);
+                        else
+                            tma_add(&tm_out, buf, n0 + c0, y);
+                    }
+                    ++n_boxes;
+                } else {
+                    uint32_t packed[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float f[2] = {__uint_as_float(g[j]) * unscale, __uint_as_float(g[j + 1]) * unscale};
+                        packed[j / 2] = Cd::put(f);
+                    }
+                    if (p.tma_store && (MODE == kWeight || all)) {
+                        const uint32_t buf = saddr(ostage) + uint32_t(q * 2 + (n_boxes & 1)) * S::kBoxBytes;
+                        if (lane == 0 && n_boxes >= 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        __syncwarp();
+                        const uint32_t at = buf + uint32_t(lane) * 64u, sw = (uint32_t(lane) >> 1) & 3u;
+#pragma unroll
+                        for (uint32_t c = 0; c < 4; ++c)
+                            st_shared16(at + ((c ^ sw) << 4), packed[4 * c], packed[4 * c + 1], packed[4 * c + 2],
+                                        packed[4 * c + 3]);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) tma_store(&tm_out, buf, n0 + c0, m - lane);
+                        ++n_boxes;
+                        continue;
+                    }
+                    if (!live) continue;
+                    char *dst = p.out + int64_t(row) * p.out_stride + int64_t(n0 + c0) * 2;
+                    if (p.vec_store && left >= 32) {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const uint32_t w4[4] = {packed[4 * v], packed[4 * v + 1], packed[4 * v + 2],
+                                                    packed[4 * v + 3]};
+                            Access<16>::store(dst + 16 * v, w4);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < left) Cd::store1(dst + j * 2, Cd::get(packed[j / 2], j % 2));
+                    }
+                }
+            }
+            if constexpr (MODE == kStats) {
+                if (live) p.part[int64_t(o.nb) * p.N + m] = make_float2(top, sum);
+            }
+        }
+        // every box this warp stored has left shared memory and reached global memory
+        if (lane == 0 && n_boxes > 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (rank == 1 && warp == 2 && !wait_parity(saddr(done), 0) && lane == 0) atomicAdd(&g_loss_timeouts, 1u);
+        __syncwarp();
+    }
+
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    if constexpr (CTAS == 2)
+        cluster_sync();
+    else
+        __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc<CTAS>(tmem, S::kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- the small kernels
+
+constexpr int kListThreads = 256;
+constexpr int kListRows = 4096;         // rows of one block of the listing kernel at most
+
+struct ListParams {
+    const int64_t *target;      // cross entropy: a row takes part if its target is in 0 .. V - 1
+    const int *entries;         // distillation: if it has entries
+    int64_t V;
+    int N, per_block;
+    const char *x;
+    int64_t x_stride;           // bytes
+    int H;
+    char *listed;               // the rows that take part, side by side
+    int64_t listed_stride;      // bytes
+    int *rows, *count;
+    float *loss, *lse;          // forward: set to 0 for the other rows
+    char *dx;                   // backward: the same
+    int64_t dx_stride;
+    const float *dloss;         // backward
+    float *scale;               // backward: what g is scaled by (and its inverse)
+    int f16;
+    float inv_t;
+};
+
+__device__ __forceinline__ bool takes_part(const ListParams &p, int i)
+{
+    return p.target ? uint64_t(p.target[i]) < uint64_t(p.V) : p.entries[i] > 0;
+}
+
+// Copies or clears a row of 16-bit values by one warp; 16 bytes at a time where
+// both sides allow.
+__device__ __forceinline__ void warp_row(char *dst, const char *src, int H, int lane)
+{
+    const bool vec = (uintptr_t(dst) % 16) == 0 && (!src || uintptr_t(src) % 16 == 0);
+    const int n = vec ? H / 8 : 0;
+    for (int i = lane; i < n; i += 32)
+        reinterpret_cast<uint4 *>(dst)[i] = src ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
+    for (int i = n * 8 + lane; i < H; i += 32)
+        reinterpret_cast<uint16_t *>(dst)[i] = src ? reinterpret_cast<const uint16_t *>(src)[i] : uint16_t(0);
+}
+
+// Lists the rows that take part, in order.  Each block counts the rows before
+// its own by itself (a row is 8 bytes, from L2): one launch and no order among
+// blocks.  Where every row takes part, nothing is copied.
+__global__ void __launch_bounds__(kListThreads) list_kernel(const ListParams p)
+{
+    __shared__ int s_before, s_total, s_pos[kListRows];
+    __shared__ unsigned int s_amax;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int first = blockIdx.x * p.per_block, last = min(p.N, first + p.per_block);
+    if (tid == 0) {
+        s_before = s_total = 0;
+        s_amax = 0;
+    }
+    __syncthreads();
+    int before = 0, total = 0;
+    float amax = 0.0f;
+    for (int i = tid; i < p.N; i += kListThreads) {
+        const bool a = takes_part(p, i);
+        total += a;
+        before += a && i < first;
+        // a gradient that is not finite takes no part in the scale
+        if (p.f16 && a) {
+            const float d = fabsf(p.dloss[i] * p.inv_t);
+            if (d < INFINITY) amax = fmaxf(amax, d);
+        }
+    }
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    total = __reduce_add_sync(0xFFFFFFFFu, total);
+    const unsigned int am = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax));    // amax >= 0: ordered as bits
+    if (lane == 0) {
+        atomicAdd(&s_before, before);
+        atomicAdd(&s_total, total);
+        atomicMax(&s_amax, am);
+    }
+    __syncthreads();
+    total = s_total;
+    if (warp == 0) {
+        int pos = s_before;
+        for (int i = first; i < last; i += 32) {
+            const bool a = i + lane < last && takes_part(p, i + lane);
+            const unsigned int set = __ballot_sync(0xFFFFFFFFu, a);
+            const int at = pos + __popc(set & ((1u << lane) - 1));
+            if (a) p.rows[at] = i + lane;
+            if (i + lane < last) s_pos[i + lane - first] = a ? at : -1;
+            pos += __popc(set);
+        }
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        *p.count = total;
+        if (p.scale) {
+            // f16 holds 2^-24 .. 2^16: the largest |dloss| / T goes to [2^13, 2^14)
+            float s = 1.0f;
+            const float a = __uint_as_float(s_amax);
+            if (p.f16 && a > 0.0f) s = exp2f(float(min(120, 13 - ilogbf(a))));
+            p.scale[0] = s;
+            p.scale[1] = 1.0f / s;
+        }
+    }
+    if (total == p.N) return;
+    __syncthreads();
+    for (int i = first + warp; i < last; i += kListThreads / 32) {
+        const int at = s_pos[i - first];
+        if (at >= 0) {
+            warp_row(p.listed + int64_t(at) * p.listed_stride, p.x + int64_t(i) * p.x_stride, p.H, lane);
+        } else {
+            if (p.dx) warp_row(p.dx + int64_t(i) * p.dx_stride, nullptr, p.H, lane);
+            if (lane == 0 && p.loss) p.loss[i] = 0.0f;
+            if (lane == 0 && p.lse) p.lse[i] = 0.0f;
+        }
+    }
+    // the last slice of rows of g^T x reads whole multiples of 64 rows
+    const int end = min(p.N, max(BK, (total + BK - 1) / BK * BK));
+    for (int i = total + blockIdx.x * (kListThreads / 32) + warp; i < end; i += gridDim.x * (kListThreads / 32))
+        warp_row(p.listed + int64_t(i) * p.listed_stride, nullptr, p.H, lane);
+}
+
+constexpr int kJoinRows = 32;
+constexpr int kJoinThreads = 1024;
+
+struct JoinParams {
+    const float2 *part;
+    int n_blocks, N;
+    const int *count, *rows;
+    const float *named;
+    const float *share;         // distillation: [N][top] teacher's probabilities, in the order of the sorted tokens
+    const int *order;           //               and where each stands in the caller's order
+    const int *entries;
+    const float *neg_entropy;   //               sum of p log p
+    int top;
+    float c1;
+    float *loss, *lse, *top_logits;
+};
+
+// The tiles' maxima and sums of one row joined, and the loss formed from them:
+// with s = sum_v 2^(c1 z_v - m) it is ln 2 (log2 s - (c1 z - m)), which keeps its
+// bits where the target's logit is the largest by far.
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p)
+{
+    __shared__ float2 s_part[kJoinThreads / 32][kJoinRows];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int count = *p.count;
+    const int m0 = blockIdx.x * kJoinRows, m = m0 + lane;
+    if (m0 >= count) return;
+    float top = -INFINITY, sum = 0.0f;
+    if (m < count) {
+        for (int b = warp; b < p.n_blocks; b += kJoinThreads / 32) {
+            const float2 v = p.part[int64_t(b) * p.N + m];
+            const float hi = fmaxf(top, v.x), base = hi == -INFINITY ? 0.0f : hi;
+            sum = sum * exp2f(top - base) + v.y * exp2f(v.x - base);
+            top = hi;
+        }
+    }
+    s_part[warp][lane] = make_float2(top, sum);
+    __syncthreads();
+    // warp w joins row w
+    const int r = warp;
+    if (m0 + r >= count) return;
+    const float2 v = s_part[lane][r];
+    float hi = v.x;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, d));
+    const float base = hi == -INFINITY ? 0.0f : hi;
+    float s = v.y * exp2f(v.x - base);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    const int row = count == p.N ? m0 + r : p.rows[m0 + r];
+    const float l2 = log2f(s);
+    if (!p.share) {
+        if (lane == 0) {
+            p.loss[row] = kLn2 * (l2 - fmaf(p.named[m0 + r], p.c1, -base));
+            p.lse[row] = kLn2 * (base + l2);
+        }
+        return;
+    }
+    const int n = p.entries[row];
+    const int64_t at = int64_t(row) * p.top;
+    float mean = 0.0f;          // sum of p_k (c1 z_k - m)
+    for (int e = lane; e < n; e += 32) {
+        const float z = p.named[at + e], share = p.share[at + e];
+        // a share of 0 has no part in the sum
+        if (share != 0.0f) mean = fmaf(share, fmaf(z, p.c1, -base), mean);
+        p.top_logits[at + p.order[at + e]] = z;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mean += __shfl_xor_sync(0xFFFFFFFFu, mean, d);
+    if (lane == 0) {
+        p.loss[row] = p.neg_entropy[row] + kLn2 * (l2 - mean);
+        p.lse[row] = kLn2 * (base + l2);
+    }
+}
+
+struct TeacherParams {
+    const int64_t *index;
+    const char *logit;
+    int64_t index_stride, logit_stride;     // elements
+    int dtype;
+    int64_t V;
+    int top, pow2;
+    float inv_t;
+    int *sorted, *order, *entries;
+    float *share, *neg_entropy;
+    float *top_logits;          // forward: set to 0 where there is no entry
+};
+
+__device__ __forceinline__ float teacher_logit(const TeacherParams &p, int64_t i)
+{
+    const char *at = p.logit + i * (p.dtype == GLU_F32 ? 4 : 2);
+    return p.dtype == GLU_F32 ? Codec<float>::load1(at)
+                              : p.dtype == GLU_F16 ? Codec<__half>::load1(at) : Codec<__nv_bfloat16>::load1(at);
+}
+
+__device__ __forceinline__ float block_reduce(float v, bool maximum, float *s_red)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float o = __shfl_xor_sync(0xFFFFFFFFu, v, d);
+        v = maximum ? fmaxf(v, o) : v + o;
+    }
+    __syncthreads();            // the last call's values have been read
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = s_red[0];
+    for (int w = 1; w < int(blockDim.x >> 5); ++w) v = maximum ? fmaxf(v, s_red[w]) : v + s_red[w];
+    return v;
+}
+
+// One row of the teacher's entries a block: sorted by token (a bitonic network in
+// shared memory; entries of one token stay in their order), the softmax of their
+// logits at T, and the sum of p log p.  An entry whose token is outside the
+// vocabulary or whose logit is -inf is none.
+__global__ void __launch_bounds__(512) teacher_kernel(const TeacherParams p)
+{
+    extern __shared__ uint64_t s_key[];             // token << 32 | place in the caller's order
+    __shared__ float s_red[16];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t row = blockIdx.x;
+    const int64_t *index = p.index + row * p.index_stride;
+    float hi = -INFINITY;
+    int n = 0, any_nan = 0;
+    for (int k = threadIdx.x; k < p.pow2; k += blockDim.x) {
+        uint64_t key = uint64_t(INT32_MAX) << 32 | uint32_t(k);
+        if (k < p.top) {
+            const int64_t v = index[k];
+            const float t = teacher_logit(p, row * p.logit_stride + k);
+            if (uint64_t(v) < uint64_t(p.V) && t != -INFINITY) {
+                key = uint64_t(v) << 32 | uint32_t(k);
+                any_nan |= t != t;
+                hi = fmaxf(hi, t);
+                ++n;
+            } else if (p.top_logits) {
+                p.top_logits[row * p.top + k] = 0.0f;
+            }
+        }
+        s_key[k] = key;
+    }
+    hi = block_reduce(hi, true, s_red);
+    n = int(block_reduce(float(n), false, s_red));
+    any_nan = __syncthreads_or(any_nan);
+    if (any_nan) hi = NAN;
+    for (int size = 2; size <= p.pow2; size <<= 1) {
+        for (int step = size >> 1; step > 0; step >>= 1) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < p.pow2 / 2; i += blockDim.x) {
+                const int a = 2 * i - (i & (step - 1)), b = a + step;
+                const uint64_t ka = s_key[a], kb = s_key[b];
+                if ((ka > kb) == ((a & size) == 0)) {
+                    s_key[a] = kb;
+                    s_key[b] = ka;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    // the sorted entries' shares; (t - hi) before / T: a lowest logit does not overflow
+    float sum = 0.0f;
+    for (int e = threadIdx.x; e < n; e += blockDim.x) {
+        const int k = int(uint32_t(s_key[e]));
+        sum += expf((teacher_logit(p, row * p.logit_stride + k) - hi) * p.inv_t);
+    }
+    sum = block_reduce(sum, false, s_red);
+    const float log_sum = logf(sum), inv = 1.0f / sum;
+    float ent = 0.0f;
+    for (int e = threadIdx.x; e < p.top; e += blockDim.x) {
+        const int64_t at = row * p.top + e;
+        const uint64_t key = s_key[e];
+        const int k = int(uint32_t(key));
+        p.sorted[at] = e < n ? int(key >> 32) : INT32_MAX;
+        p.order[at] = k;
+        if (e < n) {
+            const float d = (teacher_logit(p, row * p.logit_stride + k) - hi) * p.inv_t;
+            const float share = expf(d) * inv;
+            p.share[at] = share;
+            if (share != 0.0f) ent = fmaf(share, d - log_sum, ent);
+        }
+    }
+    ent = block_reduce(ent, false, s_red);
+    if (threadIdx.x == 0) {
+        p.entries[row] = n;
+        p.neg_entropy[row] = ent;
+    }
+}
+
+struct NamedParams {
+    const int *count, *rows, *sorted, *order, *entries;
+    const float *share, *top_logits, *lse, *dloss, *scale;
+    int N, top;
+    int64_t first, cols;        // the piece of the vocabulary
+    float c1, inv_t;
+    char *g;
+    int64_t g_stride;           // bytes
+};
+
+// Distillation: the entries of g that the teacher names, formed anew from the
+// forward pass's logits (g as stored is rounded: the share could not be taken off
+// it).  One block a row; the first of a token's entries sums its shares.
+template <class T>
+__global__ void __launch_bounds__(128) named_grad_kernel(const NamedParams p)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int count = *p.count, m = blockIdx.x;
+    if (m >= count) return;
+    const int row = count == p.N ? m : p.rows[m];
+    const int n = p.entries[row];
+    const int64_t at = int64_t(row) * p.top;
+    const float coef = p.dloss[row] * (p.scale[0] * p.inv_t);
+    if (coef == 0.0f) return;
+    const float shift = -p.lse[row] * kLog2e;
+    for (int e = threadIdx.x; e < n; e += blockDim.x) {
+        const int v = p.sorted[at + e];
+        if (v < p.first || v >= p.first + p.cols || (e > 0 && p.sorted[at + e - 1] == v)) continue;
+        float share = p.share[at + e];
+        for (int i = e + 1; i < n && p.sorted[at + i] == v; ++i) share += p.share[at + i];
+        const float z = p.top_logits[at + p.order[at + e]];
+        Codec<T>::store1(p.g + int64_t(m) * p.g_stride + (v - p.first) * 2,
+                         coef * (exp2_fast(fmaf(z, p.c1, shift)) - share));
+    }
+}
+
+struct SumParams {
+    const float *part;
+    int64_t ld;                 // floats
+    int split_rows, splits;
+    const int *count, *rows;    // NULL: every row, where it stands
+    int N, cols, m_rows;
+    const float *scale;
+    char *out;
+    int64_t out_stride;         // bytes
+};
+
+// Partial results added in the order of the parts and rounded once.
+template <class T>
+__global__ void __launch_bounds__(256) sum_kernel(const SumParams p)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int count = p.rows ? *p.count : p.m_rows;
+    const float unscale = p.scale[1];
+    const int quads = (p.cols + 3) / 4;
+    const bool vec = (uintptr_t(p.out) % 8) == 0 && p.out_stride % 8 == 0;
+    const int64_t n = int64_t(count) * quads;
+    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
+        const int m = int(i / quads), c = int(i % quads) * 4;
+        const float *src = p.part + int64_t(m) * p.ld + c;
+        float4 a = *reinterpret_cast<const float4 *>(src);
+        for (int s = 1; s < p.splits; ++s) {
+            const float4 b = *reinterpret_cast<const float4 *>(src + int64_t(s) * p.split_rows * p.ld);
+            a.x += b.x;
+            a.y += b.y;
+            a.z += b.z;
+            a.w += b.w;
+        }
+        const int row = p.rows && count != p.N ? p.rows[m] : m;
+        char *dst = p.out + int64_t(row) * p.out_stride + int64_t(c) * 2;
+        const float f[4] = {a.x * unscale, a.y * unscale, a.z * unscale, a.w * unscale};
+        if (vec && c + 4 <= p.cols) {
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(Codec<T>::put(f), Codec<T>::put(f + 2));
+        } else {
+            for (int j = 0; j < 4 && c + j < p.cols; ++j) Codec<T>::store1(dst + 2 * j, f[j]);
+        }
+    }
+}
+
+}  // namespace loss
+}  // namespace glu
+
+// ---------------------------------------------------------------- host side
+
+namespace glu {
+namespace loss {
+
+cudaError_t timeouts(unsigned int *count, bool reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(count, g_loss_timeouts, sizeof(unsigned int));
+    if (e == cudaSuccess && reset) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_loss_timeouts, &zero, sizeof(unsigned int));
+    }
+    return e;
+}
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxSize = INT32_MAX - 65536;
+constexpr int kMaxTop = 1024;
+// g of one piece of the vocabulary; a smaller workspace takes smaller pieces
+constexpr uint64_t kPieceBytes = uint64_t(1) << 30;
+constexpr int64_t kMinPiece = 256;
+
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+bool make_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, int64_t rows, int64_t cols,
+              int64_t stride_bytes, int box_cols, int box_rows, CUtensorMapSwizzle swizzle)
+{
+    EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(stride_bytes)};
+    const cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+using GemmFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Params);
+
+struct Variant {
+    GemmFn fn;
+    int smem, bn, ctas, id;
+};
+
+constexpr int kVariants = 18;
+
+template <int MODE, int BN, int CTAS>
+Variant variant(bool bf16, int id)
+{
+    return {bf16 ? loss_gemm_kernel<MODE, __nv_bfloat16, BN, CTAS> : loss_gemm_kernel<MODE, __half, BN, CTAS>,
+            Shape<MODE, BN, CTAS>::kSmemBytes, BN, CTAS, id};
+}
+
+// Blocks (or pairs) of a variant that fit on the device at once, and the
+// shared-memory opt-in, once per device.
+std::atomic<int> g_slots[kMaxDevices][2][kVariants];
+
+int slots_of(const Variant &v, bool bf16, int dev, int sms, int *out)
+{
+    std::atomic<int> &slots = g_slots[dev % kMaxDevices][bf16][v.id];
+    int n = slots.load(std::memory_order_acquire);
+    if (n == 0) {
+        cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(v.fn),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+        if (e != cudaSuccess) {
+            (void)cudaGetLastError();
+            return glu::cuda_fail(e);
+        }
+        n = sms;
+        if (v.ctas > 1) {
+            cudaLaunchConfig_t q{};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = unsigned(v.ctas);
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            q.blockDim = dim3(kThreads);
+            q.dynamicSmemBytes = size_t(v.smem);
+            q.gridDim = dim3(unsigned(sms - sms % v.ctas));
+            q.attrs = attr;
+            q.numAttrs = 1;
+            int clusters = 0;
+            e = cudaOccupancyMaxActiveClusters(&clusters, reinterpret_cast<const void *>(v.fn), &q);
+            if (e != cudaSuccess || clusters <= 0) {
+                (void)cudaGetLastError();
+                clusters = sms / v.ctas;
+            }
+            n = clusters;
+        }
+        slots.store(n, std::memory_order_release);
+    }
+    *out = n;
+    return GLU_OK;
+}
+
+// A launch that may overlap the tail of the one before it in the stream (every
+// kernel here waits for that grid before it touches memory).
+int launch(const void *fn, unsigned grid, unsigned threads, size_t smem, unsigned cluster, void **args, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+    if (e != cudaSuccess) {     // retry without the dependent-launch attribute
+        (void)cudaGetLastError();
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelExC(&cfg, fn, args);
+    }
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return glu::cuda_fail(e);
+    }
+    return GLU_OK;
+}
+
+int device(int *dev, int *sms)
+{
+    cudaError_t e = cudaGetDevice(dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return glu::cuda_fail(e);
+    }
+    return GLU_OK;
+}
+
+// Everything a pass gets; what it does not use stays empty.
+struct Call {
+    const void *x;
+    int64_t x_stride;
+    const void *w;
+    int64_t w_stride;
+    int64_t N, H, V;
+    int dtype;
+    const int64_t *target;      // cross entropy
+    const int64_t *index;       // distillation
+    int64_t index_stride;
+    const void *logit;
+    int64_t logit_stride;
+    int64_t top;
+    int logit_dtype;
+    float temperature;
+    float *loss, *lse, *top_logits;
+    const float *dloss;
+    void *dx;
+    int64_t dx_stride;
+    void *dw;
+    int64_t dw_stride;
+    void *workspace;
+    size_t workspace_bytes;
+    bool backward, distill;
+};
+
+// How a pass divides its work and its workspace (offsets in bytes).
+struct Plan {
+    int64_t piece;              // backward: tokens of a piece
+    int pieces;
+    int data_splits, weight_splits;
+    int64_t data_rows, weight_rows, ld;         // of a partial result; ld in floats
+    int64_t g_stride, listed_stride;            // bytes
+    uint64_t rows, listed, part, named, sorted, order, entries, share, entropy, g, data, weight, bytes;
+};
+
+// Column-tile width of the logits' product: the fewest rows of x and w moved,
+// counted in rounds of tiles over the GPU (the widest on a tie).
+int pick_bn(int64_t m_blocks, int64_t V, int64_t slots, int64_t a_rows)
+{
+    int best = 128;
+    int64_t best_cost = -1;
+    for (int bn : {128, 96, 64}) {
+        const int64_t tiles = m_blocks * ((V + 2 * bn - 1) / (2 * bn));
+        const int64_t cost = (tiles + slots - 1) / slots * (a_rows + 2 * bn);
+        if (best_cost < 0 || cost < best_cost) {
+            best = bn;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+// Parts of K for a product with few tiles: the fewest rounds, a part counted with
+// the 8 slices that it costs to start and to store; 8 slices a part at least.
+int pick_splits(int64_t tiles, int64_t k_tiles, int64_t slots)
+{
+    int best = 1;
+    int64_t best_cost = -1;
+    for (int s = 1; s <= 32 && (s == 1 || k_tiles / s >= 8); ++s) {
+        const int64_t cost = (tiles * s + slots - 1) / slots * ((k_tiles + s - 1) / s + 8);
+        if (best_cost < 0 || cost < best_cost) {
+            best = s;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+constexpr int kSms = 152;              // what the parts of K are counted for
+
+Plan make_plan(const Call &c, int64_t piece)
+{
+    Plan p{};
+    uint64_t at = 0;
+    const auto take = [&](uint64_t bytes) {
+        const uint64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    const uint64_t N = uint64_t(c.N), top = uint64_t(c.top);
+    p.listed_stride = round_up(c.H, 8) * 2;
+    p.rows = take(4 * N + 64);          // the count, the scale and its inverse, then the list (from byte 64)
+    p.listed = take(N * uint64_t(p.listed_stride));
+    if (c.distill) {
+        p.sorted = take(4 * N * top);
+        p.order = take(4 * N * top);
+        p.share = take(4 * N * top);
+        p.entries = take(4 * N);
+        p.entropy = take(4 * N);
+    }
+    if (!c.backward) {
+        p.part = take(8 * N * uint64_t((c.V + 127) / 128));
+        p.named = take(4 * N * (c.distill ? top : 1));
+    } else {
+        p.piece = piece;
+        p.pieces = int((c.V + piece - 1) / piece);
+        p.g_stride = round_up(piece, 64) * 2;
+        p.g = take(N * uint64_t(p.g_stride));
+        p.ld = round_up(c.H, 4);
+        const int ctas = c.N > BM ? 2 : 1;
+        const int64_t tile_m = BM * ctas, n_blocks = (c.H + 255) / 256;
+        const int64_t m_blocks = (c.N + tile_m - 1) / tile_m;
+        p.data_splits = pick_splits(m_blocks * n_blocks, (piece + BK - 1) / BK, kSms / ctas);
+        p.data_rows = m_blocks * tile_m;
+        if (c.dx && (p.data_splits > 1 || p.pieces > 1))
+            p.data = take(4 * uint64_t(p.data_splits) * uint64_t(p.data_rows) * uint64_t(p.ld));
+        const int64_t w_blocks = (piece + 255) / 256;
+        p.weight_splits = pick_splits(w_blocks * n_blocks, (c.N + BK - 1) / BK, kSms / 2);
+        p.weight_rows = w_blocks * 256;
+        if (c.dw && p.weight_splits > 1)
+            p.weight = take(4 * uint64_t(p.weight_splits) * uint64_t(p.weight_rows) * uint64_t(p.ld));
+    }
+    p.bytes = at;
+    return p;
+}
+
+// Pieces of at most kPieceBytes of g, about equal, whole tiles.
+int64_t default_piece(int64_t N, int64_t V)
+{
+    int64_t most = int64_t(kPieceBytes / (2 * uint64_t(N))) / kMinPiece * kMinPiece;
+    if (most < kMinPiece) most = kMinPiece;
+    const int64_t pieces = (V + most - 1) / most;
+    return round_up((V + pieces - 1) / pieces, kMinPiece) < V ? round_up((V + pieces - 1) / pieces, kMinPiece) : V;
+}
+
+bool plan_for(const Call &c, uint64_t bytes, Plan *out)
+{
+    int64_t piece = c.backward ? default_piece(c.N, c.V) : c.V;
+    while (true) {
+        *out = make_plan(c, piece);
+        if (out->bytes <= bytes) return true;
+        if (!c.backward || piece <= kMinPiece) return false;
+        piece = round_up((piece + 1) / 2, kMinPiece) < piece ? round_up((piece + 1) / 2, kMinPiece) : piece - kMinPiece;
+        if (piece < kMinPiece) piece = kMinPiece;
+    }
+}
+
+// Argument rules of the four entry points; no CUDA call.
+int validate(Call &c, bool *empty)
+{
+    *empty = false;
+    if (c.dtype != GLU_F16 && c.dtype != GLU_BF16) return GLU_ERR_ENUM;
+    if (c.distill && c.logit_dtype != GLU_F32 && c.logit_dtype != GLU_F16 && c.logit_dtype != GLU_BF16)
+        return GLU_ERR_ENUM;
+    if (c.N < 0 || c.H < 1 || c.V < 1 || c.N > kMaxSize || c.H > kMaxSize || c.V > kMaxSize) return GLU_ERR_SHAPE;
+    if (c.distill && (c.top < 1 || c.top > kMaxTop)) return GLU_ERR_SHAPE;
+    if (c.distill && !(c.temperature >= 0x1p-10f && c.temperature <= 0x1p10f)) return GLU_ERR_VALUE;
+    if (c.backward && !c.dx && !c.dw) {
+        *empty = true;
+        return GLU_OK;
+    }
+    if (c.N == 0) {             // dw is 0, nothing else is left to do
+        *empty = true;
+        if (c.backward && c.dw && c.dw_stride < c.H) return GLU_ERR_STRIDE;
+        if (uintptr_t(c.dw) % 2) return GLU_ERR_STRIDE;
+        return GLU_OK;
+    }
+    if (!c.x || !c.w || !c.lse || !c.workspace || (!c.distill && !c.target) ||
+        (c.distill && (!c.index || !c.logit || !c.top_logits)) || ((!c.backward || !c.distill) && !c.loss) ||
+        (c.backward && !c.dloss))
+        return GLU_ERR_NULL;
+    // strides that separate nothing
+    if (c.N == 1) {
+        c.x_stride = round_up(c.H, 8);
+        c.dx_stride = c.H;
+        c.index_stride = c.logit_stride = c.top;
+    }
+    if (c.V == 1) {
+        c.w_stride = round_up(c.H, 8);
+        c.dw_stride = c.H;
+    }
+    if (c.x_stride < c.H || c.w_stride < c.H || (c.dx && c.dx_stride < c.H) || (c.dw && c.dw_stride < c.H) ||
+        (c.distill && (c.index_stride < c.top || c.logit_stride < c.top)))
+        return GLU_ERR_STRIDE;
+    // the tensor-memory accelerator: 16-byte aligned bases and strides (below 2^40 bytes)
+    if (uintptr_t(c.x) % 16 || uintptr_t(c.w) % 16 || c.x_stride % 8 || c.w_stride % 8 ||
+        c.x_stride >= (int64_t(1) << 39) || c.w_stride >= (int64_t(1) << 39))
+        return GLU_ERR_STRIDE;
+    if (uintptr_t(c.target) % 8 || uintptr_t(c.index) % 8 || uintptr_t(c.loss) % 4 || uintptr_t(c.lse) % 4 ||
+        uintptr_t(c.top_logits) % 4 || uintptr_t(c.dloss) % 4 || uintptr_t(c.dx) % 2 || uintptr_t(c.dw) % 2 ||
+        uintptr_t(c.logit) % (c.logit_dtype == GLU_F32 ? 4 : 2) || uintptr_t(c.workspace) % 256)
+        return GLU_ERR_STRIDE;
+    // 0 .. 4 read only, the rest outputs and the workspace
+    enum { X, W, Names, Logit, Dloss, Loss, Lse, Top, Dx, Dw, Work, kSpans };
+    Span s[kSpans] = {};
+    const int64_t top = c.distill ? c.top : 0;
+    bool fits = span(c.x, c.N, c.x_stride, c.H, 2, &s[X]) && span(c.w, c.V, c.w_stride, c.H, 2, &s[W]) &&
+                span(c.loss, c.loss ? 1 : 0, 0, c.N, 4, &s[Loss]) && span(c.lse, 1, 0, c.N, 4, &s[Lse]) &&
+                span(c.dloss, c.backward ? 1 : 0, 0, c.N, 4, &s[Dloss]) &&
+                span(c.dx, c.dx ? c.N : 0, c.dx_stride, c.H, 2, &s[Dx]) &&
+                span(c.dw, c.dw ? c.V : 0, c.dw_stride, c.H, 2, &s[Dw]) &&
+                (c.distill ? span(c.index, c.N, c.index_stride, top, 8, &s[Names]) &&
+                                 span(c.logit, c.N, c.logit_stride, top, c.logit_dtype == GLU_F32 ? 4 : 2, &s[Logit]) &&
+                                 span(c.top_logits, c.N, top, top, 4, &s[Top])
+                           : span(c.target, 1, 0, c.N, 8, &s[Names]));
+    s[Work].lo = uintptr_t(c.workspace);
+    fits = fits && !__builtin_add_overflow(s[Work].lo, uint64_t(c.workspace_bytes), &s[Work].hi);
+    if (!fits) return GLU_ERR_SHAPE;
+    for (int o = c.backward ? int(Dx) : int(Loss); o < kSpans; ++o)
+        for (int i = 0; i < o; ++i)
+            if (overlap(s[o], s[i])) return GLU_ERR_ALIAS;
+    return GLU_OK;
+}
+
+// The operands of the tensor-memory accelerator are in the current device's memory.
+int check_device(const Call &c, int dev)
+{
+    for (const void *q : {c.x, c.w, static_cast<const void *>(c.workspace), static_cast<const void *>(c.dx),
+                          static_cast<const void *>(c.dw)}) {
+        if (!q) continue;
+        cudaPointerAttributes at{};
+        const cudaError_t e = cudaPointerGetAttributes(&at, q);
+        if (e != cudaSuccess) {
+            (void)cudaGetLastError();
+            return glu::cuda_fail(e);
+        }
+        if (at.type != cudaMemoryTypeDevice || at.device != dev) return GLU_ERR_VALUE;
+    }
+    return GLU_OK;
+}
+
+struct Run {
+    const Call &c;
+    const Plan &plan;
+    cudaStream_t s;
+    int dev, sms;
+    bool bf16;
+    char *ws;
+    CUtensorMapDataType type16;
+
+    int *count() const { return reinterpret_cast<int *>(ws + plan.rows); }
+    float *scale() const { return reinterpret_cast<float *>(ws + plan.rows + 8); }
+    int *rows() const { return reinterpret_cast<int *>(ws + plan.rows + 64); }
+    template <class P>
+    P *at(uint64_t offset) const { return reinterpret_cast<P *>(ws + offset); }
+    float inv_t() const { return c.distill ? 1.0f / c.temperature : 1.0f; }
+    float c1() const { return c.distill ? float(1.4426950408889634 / double(c.temperature)) : kLog2e; }
+
+    int teacher() const
+    {
+        TeacherParams t{};
+        t.index = c.index;
+        t.index_stride = c.index_stride;
+        t.logit = static_cast<const char *>(c.logit);
+        t.logit_stride = c.logit_stride;
+        t.dtype = c.logit_dtype;
+        t.V = c.V;
+        t.top = int(c.top);
+        t.pow2 = 2;
+        while (t.pow2 < t.top) t.pow2 *= 2;
+        t.inv_t = inv_t();
+        t.sorted = at<int>(plan.sorted);
+        t.order = at<int>(plan.order);
+        t.share = at<float>(plan.share);
+        t.entries = at<int>(plan.entries);
+        t.neg_entropy = at<float>(plan.entropy);
+        t.top_logits = c.backward ? nullptr : c.top_logits;
+        void *args[] = {&t};
+        const unsigned threads = unsigned(t.pow2 / 2 < 32 ? 32 : t.pow2 / 2);
+        return launch(reinterpret_cast<const void *>(&teacher_kernel), unsigned(c.N), threads, size_t(t.pow2) * 8, 1,
+                      args, s);
+    }
+
+    int list() const
+    {
+        ListParams l{};
+        l.target = c.distill ? nullptr : c.target;
+        l.entries = c.distill ? at<int>(plan.entries) : nullptr;
+        l.V = c.V;
+        l.N = int(c.N);
+        l.per_block = int((c.N + 511) / 512);
+        if (l.per_block < 16) l.per_block = 16;
+        if (l.per_block > kListRows) l.per_block = kListRows;
+        l.x = static_cast<const char *>(c.x);
+        l.x_stride = c.x_stride * 2;
+        l.H = int(c.H);
+        l.listed = at<char>(plan.listed);
+        l.listed_stride = plan.listed_stride;
+        l.rows = rows();
+        l.count = count();
+        l.inv_t = inv_t();
+        if (c.backward) {
+            l.dx = static_cast<char *>(c.dx);
+            l.dx_stride = c.dx_stride * 2;
+            l.dloss = c.dloss;
+            l.scale = scale();
+            l.f16 = !bf16;
+        } else {
+            l.loss = c.loss;
+            l.lse = c.lse;
+        }
+        void *args[] = {&l};
+        return launch(reinterpret_cast<const void *>(&list_kernel), unsigned((c.N + l.per_block - 1) / l.per_block),
+                      kListThreads, 0, 1, args, s);
+    }
+
+    bool map16(CUtensorMap *m, const void *base, int64_t r, int64_t cols, int64_t stride_bytes, int box_cols,
+               int box_rows, CUtensorMapSwizzle sw) const
+    {
+        return make_map(m, type16, base, r, cols, stride_bytes, box_cols, box_rows, sw);
+    }
+
+    // One product.  `tiles_rows` sizes the grid for all rows.
+    int product(const Variant &v, CUtensorMap &a, CUtensorMap &b, CUtensorMap &listed, CUtensorMap &out, Params &p,
+                int64_t all_rows, int64_t row_bytes, glu_launch_info_t *info) const
+    {
+        int n_slots = 0;
+        if (int st = slots_of(v, bf16, dev, sms, &n_slots)) return st;
+        const int64_t tile_m = int64_t(BM) * v.ctas;
+        const int64_t m_blocks = (all_rows + tile_m - 1) / tile_m;
+        p.count = count();
+        p.rows = rows();
+        p.N = int(c.N);
+        p.n_blocks = int((p.cols + 2 * v.bn - 1) / (2 * v.bn));
+        if (p.splits < 1) p.splits = 1;
+        // row blocks per group: their rows of A (about 48 MiB) stay in L2 while B
+        // streams past once; where one block row is more than that, tiles that run
+        // side by side form a square
+        int64_t group = (int64_t(48) << 20) / (tile_m * row_bytes);
+        if (group < 8) group = 8;
+        p.group_m = int(group > m_blocks ? m_blocks : group);
+        const int64_t tiles = m_blocks * p.n_blocks * p.splits;
+        if (tiles * v.ctas > INT32_MAX) return GLU_ERR_SHAPE;
+        const int64_t clusters = tiles < n_slots ? tiles : n_slots;
+        void *args[] = {&a, &b, &listed, &out, &p};
+        if (int st = launch(reinterpret_cast<const void *>(v.fn), unsigned(clusters * v.ctas), kThreads,
+                            size_t(v.smem), unsigned(v.ctas), args, s))
+            return st;
+        info->launched = 1;
+        info->unroll = v.ctas;
+        info->threads = kThreads;
+        info->grid = int32_t(clusters * v.ctas);
+        info->vector_units = tiles;
+        return GLU_OK;
+    }
+
+    // The logits' product over tokens first .. first + cols.
+    int logits(bool grad, int64_t first, int64_t cols, glu_launch_info_t *info) const
+    {
+        const int ctas = c.N > BM ? 2 : 1;
+        const int64_t tile_m = int64_t(BM) * ctas;
+        const int64_t a_rows = ctas == 1 ? round_up(c.N, 8) : tile_m;
+        const int bn = pick_bn((c.N + tile_m - 1) / tile_m, cols, sms / ctas, a_rows);
+        Variant v{};
+        if (!grad)
+            v = ctas == 1 ? (bn == 64   ? variant<kStats, 64, 1>(bf16, 0)
+                             : bn == 96 ? variant<kStats, 96, 1>(bf16, 1)
+                                        : variant<kStats, 128, 1>(bf16, 2))
+                          : (bn == 64   ? variant<kStats, 64, 2>(bf16, 3)
+                             : bn == 96 ? variant<kStats, 96, 2>(bf16, 4)
+                                        : variant<kStats, 128, 2>(bf16, 5));
+        else
+            v = ctas == 1 ? (bn == 64   ? variant<kGrad, 64, 1>(bf16, 6)
+                             : bn == 96 ? variant<kGrad, 96, 1>(bf16, 7)
+                                        : variant<kGrad, 128, 1>(bf16, 8))
+                          : (bn == 64   ? variant<kGrad, 64, 2>(bf16, 9)
+                             : bn == 96 ? variant<kGrad, 96, 2>(bf16, 10)
+                                        : variant<kGrad, 128, 2>(bf16, 11));
+        // one block holding every row copies only the rows that exist (rounded up to a
+        // swizzle atom): the MMA's other rows are never stored
+        const int box_a = ctas == 1 ? int(a_rows) : BM, box_b = ctas == 1 ? 2 * bn : bn;
+        CUtensorMap ta, tl, tb, to;
+        const char *w = static_cast<const char *>(c.w) + first * c.w_stride * 2;
+        if (!map16(&ta, c.x, c.N, c.H, c.x_stride * 2, BK, box_a, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !map16(&tl, at<char>(plan.listed), c.N, c.H, plan.listed_stride, BK, box_a, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !map16(&tb, w, cols, c.H, c.w_stride * 2, BK, box_b, CU_TENSOR_MAP_SWIZZLE_128B))
+            return glu::cuda_fail(cudaErrorInvalidValue);
+        Params p{};
+        p.cols = int(cols);
+        p.depth = int(c.H);
+        p.a_bytes = uint32_t(box_a) * BK * 2;
+        p.target = c.distill ? nullptr : c.target;
+        p.first = first;
+        p.c1 = c1();
+        if (grad) {
+            if (!map16(&to, at<char>(plan.g), c.N, round_up(cols, 8), plan.g_stride, kBox, kBox,
+                       CU_TENSOR_MAP_SWIZZLE_64B))
+                return glu::cuda_fail(cudaErrorInvalidValue);
+            p.lse = c.lse;
+            p.loss = c.loss;
+            p.dloss = c.dloss;
+            p.inv_t = inv_t();
+            p.scale = scale();
+        } else {
+            to = ta;
+            p.part = at<float2>(plan.part);
+            p.named = at<float>(plan.named);
+            p.index = c.distill ? at<int>(plan.sorted) : nullptr;
+            p.top = int(c.top);
+        }
+        return product(v, ta, tb, tl, to, p, c.N, c.H * 2, info);
+    }
+
+    int named(int64_t first, int64_t cols) const
+    {
+        NamedParams n{};
+        n.count = count();
+        n.rows = rows();
+        n.sorted = at<int>(plan.sorted);
+        n.order = at<int>(plan.order);
+        n.entries = at<int>(plan.entries);
+        n.share = at<float>(plan.share);
+        n.top_logits = c.top_logits;
+        n.lse = c.lse;
+        n.dloss = c.dloss;
+        n.scale = scale();
+        n.N = int(c.N);
+        n.top = int(c.top);
+        n.first = first;
+        n.cols = cols;
+        n.c1 = c1();
+        n.inv_t = inv_t();
+        n.g = at<char>(plan.g);
+        n.g_stride = plan.g_stride;
+        void *args[] = {&n};
+        const void *fn = bf16 ? reinterpret_cast<const void *>(&named_grad_kernel<__nv_bfloat16>)
+                              : reinterpret_cast<const void *>(&named_grad_kernel<__half>);
+        return launch(fn, unsigned(c.N), 128, 0, 1, args, s);
+    }
+
+    // Where a gradient product's result goes: a 16-bit matrix or fp32 partial results.
+    int output(Params &p, CUtensorMap *to, const CUtensorMap &unused, void *out, int64_t out_stride, int64_t r,
+               bool partial, uint64_t buffer, int64_t split_rows, bool add) const
+    {
+        if (partial) {
+            p.partial = add ? 2 : 1;
+            p.split_rows = int(split_rows);
+            if (!make_map(to, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, at<char>(buffer), split_rows * p.splits, plan.ld,
+                          plan.ld * 4, kBox, kBox, CU_TENSOR_MAP_SWIZZLE_128B))
+                return glu::cuda_fail(cudaErrorInvalidValue);
+            return GLU_OK;
+        }
+        p.out = static_cast<char *>(out);
+        p.out_stride = out_stride * 2;
+        p.vec_store = uintptr_t(out) % 16 == 0 && out_stride % 8 == 0;
+        // the copy engine clips a box at the last column in 16-byte units
+        p.tma_store = p.vec_store && c.H % 8 == 0 &&
+                      map16(to, out, r, c.H, out_stride * 2, kBox, kBox, CU_TENSOR_MAP_SWIZZLE_64B);
+        if (!p.tma_store) *to = unused;
+        return GLU_OK;
+    }
+
+    // dx (+)= g w over the piece.
+    int data(int64_t first, int64_t cols, bool add, glu_launch_info_t *info) const
+    {
+        const int ctas = c.N > BM ? 2 : 1;
+        const int bn = c.H <= 128 ? 64 : 128;
+        const Variant v = ctas == 1 ? (bn == 64 ? variant<kData, 64, 1>(bf16, 12) : variant<kData, 128, 1>(bf16, 13))
+                                    : (bn == 64 ? variant<kData, 64, 2>(bf16, 14) : variant<kData, 128, 2>(bf16, 15));
+        const int box_a = ctas == 1 ? int(round_up(c.N, 8)) : BM;
+        CUtensorMap ta, tb, to;
+        const char *w = static_cast<const char *>(c.w) + first * c.w_stride * 2;
+        if (!map16(&ta, at<char>(plan.g), c.N, cols, plan.g_stride, BK, box_a, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !map16(&tb, w, cols, c.H, c.w_stride * 2, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B))
+            return glu::cuda_fail(cudaErrorInvalidValue);
+        Params p{};
+        p.cols = int(c.H);
+        p.depth = int(cols);
+        p.splits = plan.data_splits;
+        p.a_bytes = uint32_t(box_a) * BK * 2;
+        p.scale = scale();
+        if (int st = output(p, &to, ta, c.dx, c.dx_stride, c.N, plan.data_splits > 1 || plan.pieces > 1, plan.data,
+                            plan.data_rows, add))
+            return st;
+        return product(v, ta, tb, ta, to, p, c.N, plan.g_stride, info);
+    }
+
+    // dw = g^T x for the piece.
+    int weight(int64_t first, int64_t cols, glu_launch_info_t *info) const
+    {
+        const Variant v = c.H <= 128 ? variant<kWeight, 64, 2>(bf16, 16) : variant<kWeight, 128, 2>(bf16, 17);
+        CUtensorMap ta, tb, tl, to;
+        if (!map16(&ta, at<char>(plan.g), c.N, cols, plan.g_stride, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !map16(&tb, c.x, c.N, c.H, c.x_stride * 2, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !map16(&tl, at<char>(plan.listed), c.N, c.H, plan.listed_stride, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B))
+            return glu::cuda_fail(cudaErrorInvalidValue);
+        Params p{};
+        p.cols = int(c.H);
+        p.m_rows = int(cols);
+        p.splits = plan.weight_splits;
+        p.a_bytes = uint32_t(Shape<kWeight, 128, 2>::kTileA);
+        p.scale = scale();
+        char *out = static_cast<char *>(c.dw) + first * c.dw_stride * 2;
+        if (int st = output(p, &to, ta, out, c.dw_stride, cols, plan.weight_splits > 1, plan.weight, plan.weight_rows,
+                            false))
+            return st;
+        if (int st = product(v, ta, tb, tl, to, p, cols, c.N * 2, info)) return st;
+        if (plan.weight_splits == 1) return GLU_OK;
+        return sum(plan.weight, plan.weight_rows, plan.weight_splits, false, cols, out, c.dw_stride);
+    }
+
+    int sum(uint64_t buffer, int64_t split_rows, int splits, bool listed, int64_t m_rows, void *out,
+            int64_t out_stride) const
+    {
+        SumParams q{};
+        q.part = at<float>(buffer);
+        q.ld = plan.ld;
+        q.split_rows = int(split_rows);
+        q.splits = splits;
+        q.count = count();
+        q.rows = listed ? rows() : nullptr;
+        q.N = int(c.N);
+        q.cols = int(c.H);
+        q.m_rows = int(m_rows);
+        q.scale = scale();
+        q.out = static_cast<char *>(out);
+        q.out_stride = out_stride * 2;
+        void *args[] = {&q};
+        const int64_t blocks = (m_rows * ((c.H + 3) / 4) + 255) / 256;
+        const void *fn = bf16 ? reinterpret_cast<const void *>(&sum_kernel<__nv_bfloat16>)
+                              : reinterpret_cast<const void *>(&sum_kernel<__half>);
+        return launch(fn, unsigned(blocks < 16 * sms ? blocks : 16 * sms), 256, 0, 1, args, s);
+    }
+
+    int forward(glu_launch_info_t *info) const
+    {
+        if (c.distill)
+            if (int st = teacher()) return st;
+        if (int st = list()) return st;
+        if (int st = logits(false, 0, c.V, info)) return st;
+        JoinParams j{};
+        j.part = at<float2>(plan.part);
+        // the tiles the product formed: as many as its launch counted over all rows
+        const int64_t m_blocks = (c.N + BM * info->unroll - 1) / (BM * info->unroll);
+        j.n_blocks = int(info->vector_units / m_blocks);
+        j.N = int(c.N);
+        j.count = count();
+        j.rows = rows();
+        j.named = at<float>(plan.named);
+        j.c1 = c1();
+        j.loss = c.loss;
+        j.lse = c.lse;
+        if (c.distill) {
+            j.share = at<float>(plan.share);
+            j.order = at<int>(plan.order);
+            j.entries = at<int>(plan.entries);
+            j.neg_entropy = at<float>(plan.entropy);
+            j.top = int(c.top);
+            j.top_logits = c.top_logits;
+        }
+        void *args[] = {&j};
+        return launch(reinterpret_cast<const void *>(&join_kernel), unsigned((c.N + kJoinRows - 1) / kJoinRows),
+                      kJoinThreads, 0, 1, args, s);
+    }
+
+    int backward(glu_launch_info_t *info) const
+    {
+        if (c.distill)
+            if (int st = teacher()) return st;
+        if (int st = list()) return st;
+        for (int i = 0; i < plan.pieces; ++i) {
+            const int64_t first = i * plan.piece, cols = c.V - first < plan.piece ? c.V - first : plan.piece;
+            if (int st = logits(true, first, cols, info)) return st;
+            if (c.distill)
+                if (int st = named(first, cols)) return st;
+            if (c.dw)
+                if (int st = weight(first, cols, info)) return st;
+            if (c.dx)
+                if (int st = data(first, cols, i > 0, info)) return st;
+        }
+        if (c.dx && (plan.data_splits > 1 || plan.pieces > 1))
+            return sum(plan.data, plan.data_rows, plan.data_splits, true, c.N, c.dx, c.dx_stride);
+        return GLU_OK;
+    }
+};
+
+int run(Call c, glu_stream_t stream)
+{
+    bool empty = false;
+    if (int st = validate(c, &empty)) return st;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (empty) {
+        if (c.backward && c.dw) {       // no rows: dw = 0
+            const cudaError_t e =
+                cudaMemset2DAsync(c.dw, size_t(c.dw_stride) * 2, 0, size_t(c.H) * 2, size_t(c.V), s);
+            if (e != cudaSuccess) {
+                (void)cudaGetLastError();
+                return glu::cuda_fail(e);
+            }
+        }
+        glu::record_launch(glu_launch_info_t{});
+        return GLU_OK;
+    }
+    Plan plan;
+    if (!plan_for(c, c.workspace_bytes, &plan)) return GLU_ERR_WORKSPACE;
+    Run r{c, plan};
+    if (int st = device(&r.dev, &r.sms)) return st;
+    if (int st = check_device(c, r.dev)) return st;
+    r.s = s;
+    r.bf16 = c.dtype == GLU_BF16;
+    r.ws = static_cast<char *>(c.workspace);
+    r.type16 = r.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    glu_launch_info_t info{};
+    if (int st = c.backward ? r.backward(&info) : r.forward(&info)) return st;
+    info.backward = c.backward;
+    info.path = c.distill ? 14 : 13;
+    glu::record_launch(info);
+    return GLU_OK;
+}
+
+size_t workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t top, bool backward)
+{
+    Call c{};
+    if (N < 1 || H < 1 || V < 1 || N > kMaxSize || H > kMaxSize || V > kMaxSize || top < 0 || top > kMaxTop) return 0;
+    c.N = N;
+    c.H = H;
+    c.V = V;
+    c.top = top;
+    c.distill = top > 0;
+    c.backward = backward;
+    if (backward) {             // room for both gradients
+        c.dx = &c;
+        c.dw = &c;
+    }
+    Plan p;
+    (void)plan_for(c, UINT64_MAX, &p);
+    return size_t(p.bytes);
+}
+
+}  // namespace
+}  // namespace loss
+}  // namespace glu
+
+extern "C" int glu_linear_ce_fwd(const void *x, int64_t x_stride, const void *w, int64_t w_stride,
+                                 const int64_t *target, float *loss, float *lse, int64_t N, int64_t H, int64_t V,
+                                 glu_dtype_t dtype, void *workspace, size_t workspace_bytes, glu_stream_t stream)
+{
+    glu::loss::Call c{};
+    c.x = x;
+    c.x_stride = x_stride;
+    c.w = w;
+    c.w_stride = w_stride;
+    c.N = N;
+    c.H = H;
+    c.V = V;
+    c.dtype = dtype;
+    c.target = target;
+    c.temperature = 1.0f;
+    c.loss = loss;
+    c.lse = lse;
+    c.workspace = workspace;
+    c.workspace_bytes = workspace_bytes;
+    return glu::loss::run(c, stream);
+}
+
+extern "C" int glu_linear_ce_bwd(const float *dloss, const void *x, int64_t x_stride, const void *w, int64_t w_stride,
+                                 const int64_t *target, const float *loss, const float *lse, void *dx,
+                                 int64_t dx_stride, void *dw, int64_t dw_stride, int64_t N, int64_t H, int64_t V,
+                                 glu_dtype_t dtype, void *workspace, size_t workspace_bytes, glu_stream_t stream)
+{
+    glu::loss::Call c{};
+    c.x = x;
+    c.x_stride = x_stride;
+    c.w = w;
+    c.w_stride = w_stride;
+    c.N = N;
+    c.H = H;
+    c.V = V;
+    c.dtype = dtype;
+    c.target = target;
+    c.temperature = 1.0f;
+    c.loss = const_cast<float *>(loss);
+    c.lse = const_cast<float *>(lse);
+    c.dloss = dloss;
+    c.dx = dx;
+    c.dx_stride = dx_stride;
+    c.dw = dw;
+    c.dw_stride = dw_stride;
+    c.workspace = workspace;
+    c.workspace_bytes = workspace_bytes;
+    c.backward = true;
+    return glu::loss::run(c, stream);
+}
+
+extern "C" int glu_linear_distill_fwd(const void *x, int64_t x_stride, const void *w, int64_t w_stride,
+                                      const int64_t *index, int64_t index_stride, const void *logit,
+                                      int64_t logit_stride, float temperature, float *loss, float *lse,
+                                      float *top_logits, int64_t N, int64_t H, int64_t V, int64_t K,
+                                      glu_dtype_t dtype, glu_dtype_t logit_dtype, void *workspace,
+                                      size_t workspace_bytes, glu_stream_t stream)
+{
+    glu::loss::Call c{};
+    c.x = x;
+    c.x_stride = x_stride;
+    c.w = w;
+    c.w_stride = w_stride;
+    c.N = N;
+    c.H = H;
+    c.V = V;
+    c.dtype = dtype;
+    c.distill = true;
+    c.index = index;
+    c.index_stride = index_stride;
+    c.logit = logit;
+    c.logit_stride = logit_stride;
+    c.logit_dtype = logit_dtype;
+    c.top = K;
+    c.temperature = temperature;
+    c.loss = loss;
+    c.lse = lse;
+    c.top_logits = top_logits;
+    c.workspace = workspace;
+    c.workspace_bytes = workspace_bytes;
+    return glu::loss::run(c, stream);
+}
+
+extern "C" int glu_linear_distill_bwd(const float *dloss, const void *x, int64_t x_stride, const void *w,
+                                      int64_t w_stride, const int64_t *index, int64_t index_stride,
+                                      const void *logit, int64_t logit_stride, float temperature, const float *lse,
+                                      const float *top_logits, void *dx, int64_t dx_stride, void *dw,
+                                      int64_t dw_stride, int64_t N, int64_t H, int64_t V, int64_t K,
+                                      glu_dtype_t dtype, glu_dtype_t logit_dtype, void *workspace,
+                                      size_t workspace_bytes, glu_stream_t stream)
+{
+    glu::loss::Call c{};
+    c.x = x;
+    c.x_stride = x_stride;
+    c.w = w;
+    c.w_stride = w_stride;
+    c.N = N;
+    c.H = H;
+    c.V = V;
+    c.dtype = dtype;
+    c.distill = true;
+    c.index = index;
+    c.index_stride = index_stride;
+    c.logit = logit;
+    c.logit_stride = logit_stride;
+    c.logit_dtype = logit_dtype;
+    c.top = K;
+    c.temperature = temperature;
+    c.lse = const_cast<float *>(lse);
+    c.top_logits = const_cast<float *>(top_logits);
+    c.dloss = dloss;
+    c.dx = dx;
+    c.dx_stride = dx_stride;
+    c.dw = dw;
+    c.dw_stride = dw_stride;
+    c.workspace = workspace;
+    c.workspace_bytes = workspace_bytes;
+    c.backward = true;
+    return glu::loss::run(c, stream);
+}
+
+extern "C" size_t glu_linear_ce_workspace_bytes(int64_t N, int64_t H, int64_t V, int backward)
+{
+    return glu::loss::workspace_bytes(N, H, V, 0, backward != 0);
+}
+
+extern "C" size_t glu_linear_distill_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K, int backward)
+{
+    return K < 1 ? 0 : glu::loss::workspace_bytes(N, H, V, K, backward != 0);
+}

@@ -26,8 +26,8 @@
  *     (cudaHostAlloc, cudaHostRegister) is device memory in this sense: the
  *     kernels then read and write it in place over the host link (zero-copy),
  *     except the operands of the tensor-core entry points (glu_gemm_fwd,
- *     glu_gemm_nt, glu_mlp_fwd, glu_gemm_q_*, glu_mlp_q_fwd) and glu_add_rmsnorm_bwd's dgamma, which must
- *     be in device memory.
+ *     glu_gemm_nt, glu_mlp_fwd, glu_gemm_q_*, glu_mlp_q_fwd, glu_linear_*) and glu_add_rmsnorm_bwd's dgamma,
+ *     which must be in device memory.
  *   - Matrices are row-major with a contiguous last dimension: element (r, c)
  *     of operand X is at X + r * X_stride + c.  Strides are in ELEMENTS of
  *     `dtype`, not bytes, and are ignored when n_rows == 1.
@@ -691,6 +691,117 @@ int glu_mlp_q_fwd(const void *x, int64_t x_stride, const float *x_scale, int64_t
 
 /* M * (round_up(I, 16) + 4 * ceil(I / 128)); 0 for invalid arguments. */
 size_t glu_mlp_q_workspace_bytes(int64_t M, int64_t I);
+
+/*
+ * ---- Losses over a vocabulary, straight from the hidden rows ----
+ *
+ * x (N x H) are a model's rows behind its last norm, w (V x H) its output
+ * projection (row v holds token v, the nn.Linear layout), and z = x w^T the
+ * logits: products of 16-bit values, summed in fp32 on the tensor cores, reduced
+ * in the product's epilogue and never stored.  A row that names no token (its
+ * target, or every one of its entries, lies outside 0 .. V - 1) takes no part:
+ * its loss, lse and dx are 0, it adds nothing to dw, and its x, dloss and lse
+ * are not used (they may hold anything, NaN included).  Rows without a token
+ * cost next to nothing: they are left out of the products.
+ *
+ * Shared rules:
+ *   x, x_stride, w, w_stride   16-byte aligned, strides multiples of 8 elements
+ *                 (GLU_ERR_STRIDE); H itself may be any size.
+ *   dx, dw        N x H and V x H of `dtype`, any alignment of 2 bytes.
+ *   loss, lse, dloss   N floats each.
+ *   dtype         GLU_F16 or GLU_BF16 (GLU_ERR_ENUM).
+ *   N, H, V       N >= 0, H and V >= 1, below 2^31 - 65536 (GLU_ERR_SHAPE).
+ *                 N == 0: no work, except that a backward call sets dw to 0.
+ *   workspace     device memory, 256-byte aligned (GLU_ERR_STRIDE), of the bytes
+ *                 the *_workspace_bytes function gives.  A backward call works
+ *                 through the vocabulary in pieces and may be given less (more
+ *                 pieces); GLU_ERR_WORKSPACE where a piece of 256 tokens does
+ *                 not fit.  Two calls that may run at once need two workspaces.
+ * x, w, dx, dw and the workspace are in the current device's memory
+ * (GLU_ERR_VALUE).  Outputs and the workspace overlap nothing (GLU_ERR_ALIAS).
+ * Results do not depend on what else runs: sums are formed in a fixed order.
+ * Several launches on `stream`; glu_last_launch describes the last product
+ * (vector_units = its tiles, unroll = blocks that share a tile).
+ */
+
+/*
+ * Softmax cross entropy:
+ *
+ *     lse[n] = log sum_v exp z[n, v],   loss[n] = lse[n] - z[n, target[n]]
+ *
+ *   target        N int64 in device memory; any value outside 0 .. V - 1 is none.
+ * glu_last_launch reports path = 13.
+ */
+int glu_linear_ce_fwd(const void *x, int64_t x_stride, const void *w, int64_t w_stride,
+                      const int64_t *target, float *loss, float *lse,
+                      int64_t N, int64_t H, int64_t V, glu_dtype_t dtype,
+                      void *workspace, size_t workspace_bytes, glu_stream_t stream);
+
+/*
+ * Its gradient, dloss[n] arriving at loss[n] (nothing arrives at lse):
+ *
+ *     g[n, v] = dloss[n] (exp(z[n, v] - lse[n]) - [v = target[n]])
+ *     dx = round(g w),   dw = round(g^T x)
+ *
+ * z is formed again from x and w.  g is rounded to `dtype` (f16: after scaling by
+ * the power of two that brings the largest |dloss| to 2^13 .. 2^14, undone in
+ * fp32: rows whose dloss is below 2^-20 of the largest lose bits), the products
+ * are summed in fp32.
+ *   loss, lse     as glu_linear_ce_fwd gave them for the same x, w and target.
+ *   dx, dw        either may be NULL: not wanted.
+ */
+int glu_linear_ce_bwd(const float *dloss, const void *x, int64_t x_stride, const void *w, int64_t w_stride,
+                      const int64_t *target, const float *loss, const float *lse,
+                      void *dx, int64_t dx_stride, void *dw, int64_t dw_stride,
+                      int64_t N, int64_t H, int64_t V, glu_dtype_t dtype,
+                      void *workspace, size_t workspace_bytes, glu_stream_t stream);
+
+/*
+ * Distillation from the K top logits a teacher kept for each row: with T the
+ * temperature, p[n] = softmax over k of logit[n, k] / T and
+ * lse[n] = log sum_v exp(z[n, v] / T),
+ *
+ *     loss[n] = sum_k p[n, k] (log p[n, k] - z[n, index[n, k]] / T + lse[n])
+ *
+ * the divergence of the student's softmax at T (over the whole vocabulary) from
+ * the teacher's (over its K tokens).  No factor T^2 is applied.
+ *   index         N x K int64, index_stride >= K; an entry outside 0 .. V - 1 is
+ *                 none, and so is one whose logit is -inf: it has no share of p.
+ *                 A token may occur twice: its shares add up.
+ *   logit         N x K of `logit_dtype` (any glu_dtype_t), in any order.
+ *   top_logits    output, N x K floats: z[n, index[n, k]], 0 where there is no
+ *                 entry; kept for the backward call.
+ *   K             1 .. 1024 (GLU_ERR_SHAPE).
+ *   temperature   2^-10 .. 2^10 (GLU_ERR_VALUE).
+ * glu_last_launch reports path = 14.
+ */
+int glu_linear_distill_fwd(const void *x, int64_t x_stride, const void *w, int64_t w_stride,
+                           const int64_t *index, int64_t index_stride, const void *logit, int64_t logit_stride,
+                           float temperature, float *loss, float *lse, float *top_logits,
+                           int64_t N, int64_t H, int64_t V, int64_t K,
+                           glu_dtype_t dtype, glu_dtype_t logit_dtype,
+                           void *workspace, size_t workspace_bytes, glu_stream_t stream);
+
+/*
+ * Its gradient for x and w (none for the teacher's logits):
+ *
+ *     g[n, v] = dloss[n] / T (exp(z[n, v] / T - lse[n]) - sum over k with index[n, k] = v of p[n, k])
+ *
+ * and dx, dw as in glu_linear_ce_bwd.  lse and top_logits as the forward call
+ * gave them.
+ */
+int glu_linear_distill_bwd(const float *dloss, const void *x, int64_t x_stride, const void *w, int64_t w_stride,
+                           const int64_t *index, int64_t index_stride, const void *logit, int64_t logit_stride,
+                           float temperature, const float *lse, const float *top_logits,
+                           void *dx, int64_t dx_stride, void *dw, int64_t dw_stride,
+                           int64_t N, int64_t H, int64_t V, int64_t K,
+                           glu_dtype_t dtype, glu_dtype_t logit_dtype,
+                           void *workspace, size_t workspace_bytes, glu_stream_t stream);
+
+/* Workspace bytes of a forward (backward == 0) or backward call; 0 for invalid
+ * arguments.  A backward call's pieces are of at most 1 GiB. */
+size_t glu_linear_ce_workspace_bytes(int64_t N, int64_t H, int64_t V, int backward);
+size_t glu_linear_distill_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K, int backward);
 
 #ifdef __cplusplus
 }

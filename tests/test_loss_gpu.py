@@ -1,0 +1,415 @@
+"""The losses over a vocabulary (linear_ce, linear_distill and their gradients)
+against the formulas in 64 bits.
+
+Bounds, with u the largest relative rounding of the type (bf16 2^-8, f16 2^-11)
+and A = |x| |w|^T:
+  * a logit, summed in fp32 over H products, is off by dz <= H 2^-23 A (0 on
+    grids whose sums are exact in fp32);
+  * log sum exp moves by at most max dz (with dz / T); forming it: 300 terms are
+    added one after the other at most (2^-24 each), exp2 and its argument are off
+    by less than 2^-20 relative, and the result's own rounding is a few 2^-24 of
+    its size;
+  * an entry g = c (p - t) with |c p| (2 max dz + 2^-19) from the exponential, the
+    rounding u |g|, and in f16 half a step of its smallest value under the scale,
+    2^-25 max |c| / 2^13;
+  * dx = g w: what g is off by times |w|, V 2^-23 |g| |w| of the fp32 sums, one
+    rounding u; dw alike.
+"""
+import math
+
+import pytest
+import torch
+
+import glu_activation_mlps_gb300 as glu
+
+pytestmark = pytest.mark.gpu
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+SIZES = [(1, 1, 1), (1, 8, 1), (3, 9, 2), (1, 64, 1000), (7, 40, 130), (128, 64, 256), (129, 100, 257), (300, 72, 1000),
+         (64, 512, 5000), (257, 1030, 3001), (1000, 130, 129), (5, 2048, 20000), (520, 256, 40), (2000, 192, 700)]
+
+
+def matrix(rows, cols, dtype, g, scale=1.0, pad=True, grid=False):
+    if grid:
+        v = torch.randint(-8, 9, (rows, cols), generator=g, device="cuda") / 8
+    else:
+        v = torch.randn(rows, cols, generator=g, device="cuda") * scale
+    wide = torch.zeros(rows, cols + (-cols % 8 if pad else 0), dtype=dtype, device="cuda")
+    wide[:, :cols] = v
+    return wide[:, :cols]
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def shares_of(index, logit, V, T):
+    """(valid rows, dense (N, V) shares, sum of p log p) in 64 bits."""
+    N = index.shape[0]
+    has = (index >= 0) & (index < V) & (logit != -math.inf)
+    valid = has.any(1)
+    t = logit.double()
+    top = torch.where(has, t, -math.inf).amax(1)
+    d = torch.where(has, (t - torch.where(valid, top, 0.0)[:, None]) / T, -math.inf)
+    p = torch.softmax(torch.where(valid[:, None], d, 0.0), 1) * valid[:, None]
+    dense = torch.zeros(N, V, dtype=torch.float64, device=index.device)
+    r, k = has.nonzero(as_tuple=True)
+    dense.index_put_((r, index[r, k]), p[r, k], accumulate=True)
+    return has, valid, dense, -torch.special.entr(p).sum(1)
+
+
+def reference(x, w, shares, valid, ent, T, dloss=None, exact=False):
+    x64 = torch.where(valid[:, None], x.double(), 0.0)
+    w64 = w.double()
+    H, V = w.shape[1], w.shape[0]
+    s = x64 @ w64.T / T
+    lse = torch.logsumexp(s, 1) * valid
+    log_q = s - lse[:, None]
+    loss = (ent - (shares * log_q).sum(1)) * valid
+    A = x64.abs() @ w64.abs().T
+    dz = (0.0 if exact else 1.0) * H * 2.0 ** -23 * A / T
+    off = dz.amax(1)
+    tol = 2 * off + 300 * 2.0 ** -24 + 2.0 ** -20 + 8 * 2.0 ** -24 * (lse.abs() + ent.abs() + s.abs().amax(1))
+    out = {"loss": loss, "lse": lse, "tol": tol, "z": s * T, "z_tol": dz * T + 2.0 ** -23 * (s * T).abs()}
+    if dloss is not None:
+        c = torch.where(valid, dloss.double(), 0.0) / T
+        p = torch.exp(log_q)
+        g = c[:, None] * (p - shares) * valid[:, None]
+        u = U[x.dtype]
+        # at a named token the exponential or, for the cross entropy, expm1 of the loss
+        eg = c.abs()[:, None] * p * (2 * off[:, None] + tol[:, None] + 2.0 ** -19)
+        eg = eg + c.abs()[:, None] * shares * (tol[:, None] + 2.0 ** -20)
+        eg = eg + u * (g.abs() + eg)
+        if x.dtype == torch.float16:
+            eg = eg + (2.0 ** -25 * c.abs().max() / 2.0 ** 13) * valid[:, None]
+        ga = g.abs() + eg
+        for name, val, err in (("dx", g @ w64, eg @ w64.abs() + V * 2.0 ** -23 * (ga @ w64.abs())),
+                               ("dw", g.T @ x64, eg.T @ x64.abs() + len(x) * 2.0 ** -23 * (ga.T @ x64.abs()))):
+            tiny = 2.0 ** -25 if x.dtype == torch.float16 else 2.0 ** -134
+            out[name] = val
+            out[name + "_tol"] = err + u * (val.abs() + err) + tiny
+    return out
+
+
+def close(got, want, tol, what):
+    bad = ~((got.double() - want).abs() <= tol)
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[0].tolist()}: "
+                           f"{got[bad][0].item()} for {want[bad][0].item()}, allowed {tol.expand_as(want)[bad][0].item()}")
+
+
+def targets(N, V, g, masked):
+    t = torch.randint(0, V, (N,), generator=g, device="cuda")
+    if masked == "some":
+        t[torch.rand(N, generator=g, device="cuda") < 0.5] = -100
+        t[N // 2] = V           # just behind the vocabulary
+        t[0] = -1
+    elif masked == "all":
+        t[:] = -100
+    elif masked == "last":
+        t[:] = -1
+        t[-1] = V - 1
+    return t
+
+
+def check_ce(x, w, target, dloss, exact=False, **kw):
+    V = w.shape[0]
+    valid = (target >= 0) & (target < V)
+    shares = torch.zeros(len(x), V, dtype=torch.float64, device="cuda")
+    shares[valid.nonzero()[:, 0], target[valid]] = 1.0
+    ref = reference(x, w, shares, valid, torch.zeros(len(x), device="cuda").double(), 1.0, dloss, exact)
+    loss, lse = glu.linear_ce(x, w, target)
+    close(loss, ref["loss"], ref["tol"], "loss")
+    close(lse, ref["lse"], ref["tol"], "lse")
+    dx, dw = glu.linear_ce_bwd(dloss, x, w, target, loss, lse, **kw)
+    close(dx, ref["dx"], ref["dx_tol"], "dx")
+    close(dw, ref["dw"], ref["dw_tol"], "dw")
+    assert glu.glu_wait_timeouts() == 0
+    return loss, lse, dx, dw
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,H,V", SIZES)
+def test_ce(N, H, V, dtype):
+    g = gen(N * 7 + H * 3 + V)
+    x, w = matrix(N, H, dtype, g), matrix(V, H, dtype, g, 2.0 / math.sqrt(H))
+    t = targets(N, V, g, "none")
+    check_ce(x, w, t, torch.randn(N, generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,H,V", [(1, 64, 300), (100, 64, 1000), (300, 72, 1000), (700, 136, 515), (2000, 64, 200)])
+@pytest.mark.parametrize("masked", ["some", "all", "last"])
+def test_ce_rows_without_target(N, H, V, masked, dtype):
+    g = gen(N + V)
+    x, w = matrix(N, H, dtype, g), matrix(V, H, dtype, g, 0.3)
+    t = targets(N, V, g, masked)
+    dloss = torch.randn(N, generator=g, device="cuda")
+    none = (t < 0) | (t >= V)
+    x[none] = math.nan          # what such rows hold is not used
+    dloss[none] = math.nan
+    loss, lse, dx, _ = check_ce(x, w, t, dloss)
+    for v in (loss, lse, dx):
+        assert torch.all(v[none] == 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,H,V", [(33, 64, 777), (200, 200, 1500), (400, 1024, 300)])
+def test_ce_on_exact_sums(N, H, V, dtype):
+    g = gen(5)
+    x, w = matrix(N, H, dtype, g, grid=True), matrix(V, H, dtype, g, grid=True)
+    check_ce(x, w, targets(N, V, g, "some"), torch.randint(1, 5, (N,), generator=g, device="cuda").float(), exact=True)
+
+
+def test_ce_confident_rows():
+    """Where the target has nearly all the probability the loss and the target's
+    gradient are small differences: to 2^-10 relative of what 64 bits give, on exact sums."""
+    N, H, V = 64, 128, 2000
+    g = gen(9)
+    w = matrix(V, H, torch.float16, g, grid=True)
+    t = torch.randint(0, V, (N,), generator=g, device="cuda")
+    x = (w[t].float() * (torch.arange(N, device="cuda")[:, None] % 4 + 1) / 4).half()
+    x = torch.round(x.float() * 8).div(8).half()
+    loss, lse = glu.linear_ce(x, w, t)
+    s = x.double() @ w.double().T
+    s_t = s.gather(1, t[:, None])
+    others = torch.exp(s - s_t).scatter_(1, t[:, None], 0.0).sum(1)
+    want = torch.log1p(others)
+    assert want.min() < 1e-3
+    # the sum is 1 + others in fp32, off by 300 roundings of 2^-24 at most
+    assert torch.all((loss.double() - want).abs() <= 300 * 2.0 ** -24 + 2.0 ** -20 * want)
+    # g's entry at the target, -(1 - exp(-loss)) = expm1(-loss), seen alone: dw of a token that only it names
+    dx, dw = glu.linear_ce_bwd(torch.ones(N, device="cuda"), x, w, t, loss, lse)
+    p = torch.exp(s - torch.logsumexp(s, 1)[:, None])
+    gg = p.scatter(1, t[:, None], torch.expm1(-loss.double())[:, None])
+    err = (2.0 ** -11 + 2.0 ** -18) * gg.abs() + 2.0 ** -38
+    for got, val, tol in ((dx, gg @ w.double(), err @ w.double().abs()), (dw, gg.T @ x.double(), err.T @ x.double().abs())):
+        close(got, val, tol * 1.01 + 2.0 ** -11 * val.abs() + 2.0 ** -24 + V * 2.0 ** -23 * 1e-3, "gradient")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,H,V", [(50, 64, 3000), (300, 256, 5000)])
+def test_ce_in_pieces(N, H, V, dtype):
+    """A small workspace: many pieces of the vocabulary, partial results added up."""
+    g = gen(11)
+    x, w = matrix(N, H, dtype, g), matrix(V, H, dtype, g, 0.2)
+    t = targets(N, V, g, "some")
+    dloss = torch.rand(N, generator=g, device="cuda")
+    full = glu.glu_linear_ce_workspace_bytes(N, H, V, 1)
+    for part in (0.9, 0.6, 0.4):
+        ws = torch.full((int(full * part),), 255, dtype=torch.uint8, device="cuda")
+        try:
+            check_ce(x, w, t, dloss, workspace=ws)
+        except glu.GluError as e:
+            assert e.status == -7 and part < 0.9
+    with pytest.raises(glu.GluError):
+        loss, lse = glu.linear_ce(x, w, t)
+        glu.linear_ce_bwd(dloss, x, w, t, loss, lse, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+def teacher(N, V, K, g, logit_dtype, kind):
+    index = torch.randint(0, V, (N, K), generator=g, device="cuda")        # tokens may occur twice
+    logit = (torch.randn(N, K, generator=g, device="cuda") * 3).to(logit_dtype)
+    if kind == "ragged":
+        index[torch.rand(N, K, generator=g, device="cuda") < 0.4] = -1
+        logit[torch.rand(N, K, generator=g, device="cuda") < 0.1] = -math.inf
+        index[0] = V            # rows without an entry
+        logit[N // 2] = -math.inf
+        logit[N - 1] = torch.finfo(logit_dtype).min
+        index[N - 1, 0] = 0
+    elif kind == "same":
+        index[:] = index[:, :1]
+    return index, logit
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,H,V,K", [(1, 8, 1, 1), (5, 40, 130, 3), (64, 128, 1000, 8), (130, 72, 2000, 33), (300, 256, 515, 100),
+                                     (40, 64, 300, 1024), (600, 64, 1000, 64)])
+@pytest.mark.parametrize("kind,T", [("plain", 1.0), ("ragged", 2.0), ("same", 0.5), ("ragged", 1.0)])
+def test_distill(N, H, V, K, kind, T, dtype):
+    g = gen(N + K)
+    x, w = matrix(N, H, dtype, g), matrix(V, H, dtype, g, 0.3)
+    logit_dtype = {"plain": torch.float32, "ragged": torch.bfloat16, "same": torch.float16}[kind]
+    index, logit = teacher(N, V, K, g, logit_dtype, kind)
+    dloss = torch.randn(N, generator=g, device="cuda")
+    has, valid, shares, ent = shares_of(index, logit, V, T)
+    x[~valid] = math.nan
+    dloss[~valid] = math.nan
+    ref = reference(x, w, shares, valid, ent, T, dloss)
+    loss, lse, top = glu.linear_distill(x, w, index, logit, T)
+    close(loss, ref["loss"], ref["tol"], "loss")
+    close(lse, ref["lse"], ref["tol"], "lse")
+    at = torch.where(has, index, 0)
+    close(top, torch.where(has, ref["z"].gather(1, at), 0.0), ref["z_tol"].gather(1, at) + 2.0 ** -126, "top_logits")
+    dx, dw = glu.linear_distill_bwd(dloss, x, w, index, logit, lse, top, T)
+    close(dx, ref["dx"], ref["dx_tol"], "dx")
+    close(dw, ref["dw"], ref["dw_tol"], "dw")
+    assert glu.glu_wait_timeouts() == 0
+
+
+def test_distill_strided_entries_and_pieces():
+    N, H, V, K, T = 70, 64, 3000, 20, 1.5
+    g = gen(3)
+    x, w = matrix(N, H, torch.bfloat16, g), matrix(V, H, torch.bfloat16, g, 0.3)
+    index = torch.randint(-1, V, (N, K + 7), generator=g, device="cuda")[:, 3:3 + K]
+    logit = torch.randn(N, 2 * K, generator=g, device="cuda")[:, :K]
+    dloss = torch.randn(N, generator=g, device="cuda")
+    has, valid, shares, ent = shares_of(index, logit, V, T)
+    ref = reference(x, w, shares, valid, ent, T, dloss)
+    loss, lse, top = glu.linear_distill(x, w, index, logit, T)
+    close(loss, ref["loss"], ref["tol"], "loss")
+    full = glu.glu_linear_distill_workspace_bytes(N, H, V, K, 1)
+    ws = torch.full((int(full * 0.8),), 255, dtype=torch.uint8, device="cuda")
+    dx, dw = glu.linear_distill_bwd(dloss, x, w, index, logit, lse, top, T, workspace=ws)
+    close(dx, ref["dx"], ref["dx_tol"], "dx")
+    close(dw, ref["dw"], ref["dw_tol"], "dw")
+
+
+@pytest.mark.parametrize("N", [60, 300])
+def test_outputs_at_odd_places(N):
+    """dx and dw off 16-byte boundaries and with gaps; what lies around them stays."""
+    H, V = 77, 333
+    g = gen(21)
+    x, w = matrix(N, H, torch.bfloat16, g), matrix(V, H, torch.bfloat16, g, 0.3)
+    for masked in ("none", "some"):
+        t = targets(N, V, g, masked)
+        dloss = torch.rand(N, generator=g, device="cuda")
+        bx = torch.full((N + 2, H + 6), 7.0, dtype=torch.bfloat16, device="cuda")
+        bw = torch.full((V + 2, H + 4), 7.0, dtype=torch.bfloat16, device="cuda")
+        check_ce(x, w, t, dloss, dx=bx[1:-1, 3:3 + H], dw=bw[1:-1, 1:1 + H])
+        bx[1:-1, 3:3 + H] = 7.0
+        bw[1:-1, 1:1 + H] = 7.0
+        assert torch.all(bx == 7.0) and torch.all(bw == 7.0)
+
+
+def test_one_gradient_only():
+    N, H, V = 200, 128, 900
+    g = gen(1)
+    x, w = matrix(N, H, torch.bfloat16, g), matrix(V, H, torch.bfloat16, g, 0.3)
+    t = targets(N, V, g, "some")
+    loss, lse = glu.linear_ce(x, w, t)
+    d = torch.rand(N, generator=g, device="cuda")
+    dx, dw = glu.linear_ce_bwd(d, x, w, t, loss, lse)
+    only_x, none = glu.linear_ce_bwd(d, x, w, t, loss, lse, dw=False)
+    assert none is None and torch.equal(only_x, dx)
+    none, only_w = glu.linear_ce_bwd(d, x, w, t, loss, lse, dx=False)
+    assert none is None and torch.equal(only_w, dw)
+    assert glu.linear_ce_bwd(d, x, w, t, loss, lse, dx=False, dw=False) == (None, None)
+
+
+def test_same_results_again_and_from_a_graph():
+    N, H, V, K = 300, 256, 3000, 16
+    g = gen(2)
+    x, w = matrix(N, H, torch.bfloat16, g), matrix(V, H, torch.bfloat16, g, 0.1)
+    t = targets(N, V, g, "some")
+    index, logit = teacher(N, V, K, g, torch.float32, "ragged")
+    d = torch.rand(N, generator=g, device="cuda")
+
+    def step():
+        loss, lse = glu.linear_ce(x, w, t)
+        a = (loss, lse, *glu.linear_ce_bwd(d, x, w, t, loss, lse))
+        loss, lse, top = glu.linear_distill(x, w, index, logit, 2.0)
+        return (*a, loss, lse, top, *glu.linear_distill_bwd(d, x, w, index, logit, lse, top, 2.0))
+
+    first = [v.clone() for v in step()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for _ in range(2):
+        graph.replay()
+        for a, b in zip(first, captured):
+            assert torch.equal(a, b)
+    # new inputs in the same places
+    x.copy_(matrix(N, H, torch.bfloat16, g))
+    t.copy_(targets(N, V, g, "none"))
+    graph.replay()
+    again = step()
+    for a, b in zip(again, captured):
+        assert torch.equal(a, b)
+    assert glu.glu_wait_timeouts() == 0
+
+
+def test_another_stream():
+    N, H, V = 200, 128, 900
+    g = gen(4)
+    x, w = matrix(N, H, torch.float16, g), matrix(V, H, torch.float16, g, 0.3)
+    t = targets(N, V, g, "some")
+    d = torch.rand(N, generator=g, device="cuda")
+    loss, lse = glu.linear_ce(x, w, t)
+    want = (loss, lse, *glu.linear_ce_bwd(d, x, w, t, loss, lse))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    loss2, lse2 = glu.linear_ce(x, w, t, stream=side)
+    got = (loss2, lse2, *glu.linear_ce_bwd(d, x, w, t, loss2, lse2, stream=side))
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_no_rows():
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(100, 64, dtype=torch.bfloat16, device="cuda")
+    t = torch.empty(0, dtype=torch.int64, device="cuda")
+    loss, lse = glu.linear_ce(x, w, t)
+    assert loss.shape == (0,)
+    dw = torch.full_like(w, 3.0)
+    dx, dw = glu.linear_ce_bwd(loss, x, w, t, loss, lse, dw=dw)
+    assert dx.shape == (0, 64) and torch.all(dw == 0)
+
+
+def test_leading_shapes():
+    g = gen(6)
+    x = matrix(24, 64, torch.bfloat16, g).view(2, 3, 4, 64)
+    w = matrix(500, 64, torch.bfloat16, g, 0.3)
+    t = targets(24, 500, g, "none")
+    a = glu.linear_ce(x, w, t.view(2, 3, 4))
+    b = glu.linear_ce(x.view(24, 64), w, t)
+    assert a[0].shape == (2, 3, 4) and torch.equal(a[0].flatten(), b[0])
+    one = glu.linear_ce(x[0, 0, 0], w, t[0])
+    assert one[0].shape == () and abs(one[0].item() - b[0][0].item()) < 1e-4
+
+
+def test_directional_difference():
+    """The gradients against differences of the loss itself, along one direction, on
+    exact sums: the step is a grid step, the curvature bounded by its square."""
+    N, H, V = 40, 64, 300
+    g = gen(8)
+    x, w = matrix(N, H, torch.float16, g, grid=True), matrix(V, H, torch.float16, g, grid=True)
+    x, w = x * 0.25, w * 0.25
+    t = targets(N, V, g, "none")
+    loss, lse = glu.linear_ce(x, w, t)
+    dx, dw = glu.linear_ce_bwd(torch.ones(N, device="cuda"), x, w, t, loss, lse)
+    h = 2.0 ** -9
+    v = torch.randint(0, 2, x.shape, generator=g, device="cuda").half() * 2 - 1
+    up, down = glu.linear_ce(x + h * v, w, t)[0].double(), glu.linear_ce(x - h * v, w, t)[0].double()
+    slope = (dx.double() * v.double()).sum(1)
+    # third derivative of log sum exp along v: at most 8 max |w v|^3 / 6 h^2; the losses' own 2^-15 / h; 64 f16 entries of dx
+    step = (v.double() @ w.double().T).abs().amax(1)
+    tol = 8 * step ** 3 / 6 * h * h + 2.0 ** -15 / h + 64 * 2.0 ** -10 * dx.double().abs().amax(1)
+    assert torch.all(((up - down) / (2 * h) - slope).abs() <= tol)
+
+
+def test_offsets_past_32_bits():
+    """A projection of more than 2^31 elements: the last tokens' logits and gradients."""
+    N, H, V = 16, 4096, 540000
+    x = torch.randn(N, H, generator=gen(1), device="cuda").bfloat16()
+    w = torch.zeros(V, H, dtype=torch.bfloat16, device="cuda")
+    last = V - 600
+    w[last:] = torch.randn(600, H, generator=gen(2), device="cuda").bfloat16() * 0.05
+    t = torch.arange(V - N, V, device="cuda")
+    loss, lse = glu.linear_ce(x, w, t)
+    d = torch.ones(N, device="cuda")
+    dx, dw = glu.linear_ce_bwd(d, x, w, t, loss, lse)
+    s = x.double() @ w[last:].double().T
+    want = torch.logsumexp(torch.cat([s, torch.full((N, 1), math.log(last), device="cuda", dtype=torch.float64)], 1), 1)
+    dz = (H * 2.0 ** -23 * (x.double().abs() @ w[last:].double().abs().T)).amax(1)
+    # 4219 tiles: 132 in a chain of the join, 300 added at most elsewhere
+    tol = 2 * dz + 500 * 2.0 ** -24 + 8 * 2.0 ** -24 * want
+    assert torch.all((lse.double() - want).abs() <= tol)
+    p = torch.exp(s - want[:, None])
+    p[torch.arange(N), t - last] -= 1
+    err = p.abs() * (2.0 ** -8 + 2 * tol[:, None] + 2.0 ** -18) + tol[:, None] * (p + 1).abs() * 2.0 ** -3
+    val = p.T @ x.double()
+    close(dw[last:], val, err.T @ x.double().abs() + 2.0 ** -8 * val.abs() + 1e-6, "dw")
+    val = p @ w[last:].double()
+    # the tokens before hold zeros and add nothing
+    close(dx, val, err @ w[last:].double().abs() * 1.01 + 2.0 ** -8 * val.abs() + 1e-6, "dx")
