@@ -19,7 +19,8 @@
 // One kernel template runs the four products (stats, grad, data, weight) on the
 // structure of glu_gemm.cu: a persistent grid; warp 0 fills a ring of 64-deep K
 // slices with the tensor-memory accelerator (128-byte swizzle), one thread of
-// warp 1 issues tcgen05.mma, warps 2-5 read the other of two accumulators.  The
+// warp 1 issues tcgen05.mma, two warpgroups
+// add the segments of K into registers, from the other of two accumulators.  The
 // operands lie as the user has them: g w wants w's vocabulary as its K, g^T x
 // wants rows as K, so those operands come as MN-major tiles (64 columns x 64 K
 // to a swizzled box), which the MMA reads directly; nothing is transposed in
@@ -52,10 +53,16 @@ using namespace glu::gemm;
 
 constexpr int BM = 128;                 // rows of a tile per block (tensor-memory lanes)
 constexpr int BK = 64;                  // K per stage: 64 x 2 bytes = one 128-byte swizzle row
-constexpr int kThreads = 192;           // warp 0 loads, warp 1 issues MMAs, warps 2-5 store
-constexpr int kEpiWarps = 4;
+constexpr int kThreads = 384;           // warp 0 loads, warp 1 issues MMAs, warps 4-11 take the sums
+constexpr int kEpiWarps = 8;            // 32 rows each, in two halves of the columns
+// Registers of a thread: launched with 168 (65536 over 384 threads); warps 0-3
+// give theirs up to 72, the others take 216 for a row's 128 sums and what forms
+// the results: 128 x 72 + 256 x 216 = 384 x 168.
+constexpr int kRegsLaunch = 168, kRegsFew = 72, kRegsMany = 216;
+static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads * kRegsLaunch, "the split fits the launch");
 constexpr int kRingBytes = 192 * 1024;
 constexpr int kBox = 32;                // outputs leave through 32 x 32 boxes
+constexpr int kBoxBytes = 4096;         // staging of a warp: one box of floats or two of 16 bits
 constexpr int kChunkBytes = 64 * BK * 2;    // an MN-major box: 64 columns x 64 K
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -80,8 +87,10 @@ struct Shape {
     static constexpr int kTileM = BM * CTAS;
     static constexpr int kTmemCols = 2 * kTileN <= 256 ? 256 : 512;     // two accumulators
     static constexpr int kBars = 2 * kStages + 2 + 2 + 1;               // full, empty, acc_full, acc_empty, done
-    static constexpr int kBoxBytes = (MODE == kData || MODE == kWeight) ? kBox * kBox * 4 : kBox * kBox * 2;
-    static constexpr int kStageOut = MODE == kStats ? 0 : kEpiWarps * 2 * kBoxBytes;
+    static constexpr int kStageOut = MODE == kStats ? 0 : kEpiWarps * kBoxBytes;
+    static constexpr int kCols = kTileN / 2;                            // columns of one epilogue thread
+    // K slices summed in tensor memory before their sum goes to registers
+    static constexpr int kSegment = MODE == kStats || MODE == kGrad ? 16 : 64;
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStageOut + kBars * 8 + 16;
     static_assert(BN % 32 == 0 && kTileN <= 256, "one MMA covers the tile's columns");
     static_assert(!kTransB || kBRows % 64 == 0, "MN-major operands come in chunks of 64 columns");
@@ -101,7 +110,7 @@ struct Params {
     int group_m;                // row blocks per group of the tile order
     uint32_t a_bytes;           // bytes of the A box (stats, grad, data: rows that exist, up to 128)
     // stats
-    float2 *part;               // [n_blocks][N]: maximum (in log2 units) and sum
+    float2 *part;               // [2 n_blocks][N]: maximum (in log2 units) and sum of half a tile's columns
     float *named;               // cross entropy: the target's logit by listed row; distillation: [N][top] by row
     const int64_t *target;      // cross entropy
     const int *index;           // distillation: [N][top], sorted, INT_MAX where there is none
@@ -262,120 +271,148 @@ __global__ void __launch_bounds__(kThreads, 1)
         return split * per_split < k_tiles ? split * per_split : (max(p.N, p.depth) + BK - 1) / BK;
     };
 
-    if (warp == 0) {
-        if (lane == 0) {
-            const CUtensorMap *ma = (MODE == kStats || MODE == kGrad) && !all ? &tm_listed : &tm_a;
-            const CUtensorMap *mbp = MODE == kWeight && !all ? &tm_listed : &tm_b;
-            const uint32_t bytes = p.a_bytes + uint32_t(S::kTileB);
-            uint32_t it = 0;
-            for (int t = cluster; t < n_tiles && !*abort_flag; t += n_clusters) {
-                const Tile o = tile_of(p, t, m_blocks);
-                const int m0 = o.mb * S::kTileM + int(rank) * BM;
-                const int n0 = o.nb * S::kTileN + int(rank) * (CTAS == 1 ? 0 : BN);
-                const int n_k = slices(o.split), k0 = slice0(o.split);
-                for (int kt = 0; kt < n_k; ++kt, ++it) {
-                    const uint32_t s = it % ST, use = it / ST;
-                    if (*abort_flag) break;
-                    if (use > 0 && !wait_parity(saddr(&empty[s]), (use - 1) & 1)) {
-                        raise_abort();
-                        break;
-                    }
-                    const uint32_t st = saddr(smem + s * S::kStageBytes);
-                    const int k = (k0 + kt) * BK;
-                    // both blocks' copies count on block 0's barrier
-                    uint32_t bar = saddr(&full[s]);
-                    if (rank == 0)
-                        arrive_expect_tx_local(bar, bytes * CTAS);
-                    else
-                        bar = mapa(bar, 0);
-                    if constexpr (S::kTransA) {
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+        if (warp == 0) {
+            if (lane == 0) {
+                const CUtensorMap *ma = (MODE == kStats || MODE == kGrad) && !all ? &tm_listed : &tm_a;
+                const CUtensorMap *mbp = MODE == kWeight && !all ? &tm_listed : &tm_b;
+                const uint32_t bytes = p.a_bytes + uint32_t(S::kTileB);
+                uint32_t it = 0;
+                for (int t = cluster; t < n_tiles && !*abort_flag; t += n_clusters) {
+                    const Tile o = tile_of(p, t, m_blocks);
+                    const int m0 = o.mb * S::kTileM + int(rank) * BM;
+                    const int n0 = o.nb * S::kTileN + int(rank) * (CTAS == 1 ? 0 : BN);
+                    const int n_k = slices(o.split), k0 = slice0(o.split);
+                    for (int kt = 0; kt < n_k; ++kt, ++it) {
+                        const uint32_t s = it % ST, use = it / ST;
+                        if (*abort_flag) break;
+                        if (use > 0 && !wait_parity(saddr(&empty[s]), (use - 1) & 1)) {
+                            raise_abort();
+                            break;
+                        }
+                        const uint32_t st = saddr(smem + s * S::kStageBytes);
+                        const int k = (k0 + kt) * BK;
+                        // both blocks' copies count on block 0's barrier
+                        uint32_t bar = saddr(&full[s]);
+                        if (rank == 0)
+                            arrive_expect_tx_local(bar, bytes * CTAS);
+                        else
+                            bar = mapa(bar, 0);
+                        if constexpr (S::kTransA) {
 #pragma unroll
-                        for (int c = 0; c < BM / 64; ++c)
-                            tma_load<CTAS>(st + c * kChunkBytes, ma, m0 + 64 * c, k, bar);
-                    } else {
-                        tma_load<CTAS>(st, ma, k, m0, bar);
-                    }
-                    if constexpr (S::kTransB) {
+                            for (int c = 0; c < BM / 64; ++c)
+                                tma_load<CTAS>(st + c * kChunkBytes, ma, m0 + 64 * c, k, bar);
+                        } else {
+                            tma_load<CTAS>(st, ma, k, m0, bar);
+                        }
+                        if constexpr (S::kTransB) {
 #pragma unroll
-                        for (int c = 0; c < S::kBRows / 64; ++c)
-                            tma_load<CTAS>(st + S::kTileA + c * kChunkBytes, mbp, n0 + 64 * c, k, bar);
-                    } else {
-                        tma_load<CTAS>(st + S::kTileA, mbp, k, n0, bar);
+                            for (int c = 0; c < S::kBRows / 64; ++c)
+                                tma_load<CTAS>(st + S::kTileA + c * kChunkBytes, mbp, n0 + 64 * c, k, bar);
+                        } else {
+                            tma_load<CTAS>(st + S::kTileA, mbp, k, n0, bar);
+                        }
                     }
                 }
-            }
-            // block 0 holds the barriers of every copy of the pair: wait for the
-            // last ones to land before the block may exit
-            if (rank == 0) {
-                const uint32_t first = it > uint32_t(ST) ? it - ST : 0;
-                for (uint32_t j = first; j < it; ++j)
-                    if (!wait_parity(saddr(&full[j % ST]), (j / ST) & 1)) {
-                        atomicAdd(&g_loss_timeouts, 1u);
-                        break;
-                    }
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            uint32_t it = 0;
-            int lt = 0;
-            for (int t = cluster; t < n_tiles; t += n_clusters, ++lt) {
-                if (*abort_flag) break;
-                const int ab = lt & 1, use_acc = lt >> 1;
-                if (use_acc > 0 && !wait_parity(saddr(&acc_empty[ab]), (use_acc - 1) & 1)) {
-                    raise_abort();
-                    break;
+                // block 0 holds the barriers of every copy of the pair: wait for the
+                // last ones to land before the block may exit
+                if (rank == 0) {
+                    const uint32_t first = it > uint32_t(ST) ? it - ST : 0;
+                    for (uint32_t j = first; j < it; ++j)
+                        if (!wait_parity(saddr(&full[j % ST]), (j / ST) & 1)) {
+                            atomicAdd(&g_loss_timeouts, 1u);
+                            break;
+                        }
                 }
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t d = tmem + uint32_t(ab * S::kTileN);
-                const int n_k = slices(tile_of(p, t, m_blocks).split);
-                bool ok = true;
-                for (int kt = 0; kt < n_k; ++kt, ++it) {
-                    const uint32_t s = it % ST, use = it / ST;
-                    if (!wait_parity(saddr(&full[s]), use & 1)) {
-                        raise_abort();
-                        ok = false;
-                        break;
-                    }
-                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t a0 = saddr(smem + s * S::kStageBytes);
-                    const uint64_t da = S::kTransA ? desc_mn_sw128(a0) : desc_sw128(a0);
-                    const uint64_t db = S::kTransB ? desc_mn_sw128(a0 + S::kTileA) : desc_sw128(a0 + S::kTileA);
+            }
+        } else if (warp == 1) {
+            if (lane == 0 && rank == 0) {
+                uint32_t it = 0;
+                int use = 0;                // accumulators filled so far
+                for (int t = cluster; t < n_tiles && !*abort_flag; t += n_clusters) {
+                    const int n_k = slices(tile_of(p, t, m_blocks).split);
+                    bool ok = true;
+                    for (int kt = 0; kt < n_k; ++use) {
+                        const int ab = use & 1, use_acc = use >> 1, end = min(n_k, kt + S::kSegment);
+                        if (*abort_flag) {
+                            ok = false;
+                            break;
+                        }
+                        if (use_acc > 0 && !wait_parity(saddr(&acc_empty[ab]), (use_acc - 1) & 1)) {
+                            raise_abort();
+                            ok = false;
+                            break;
+                        }
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        const uint32_t d = tmem + uint32_t(ab * S::kTileN);
+                        for (bool more = false; kt < end; ++kt, ++it, more = true) {
+                            const uint32_t s = it % ST;
+                            if (!wait_parity(saddr(&full[s]), (it / ST) & 1)) {
+                                raise_abort();
+                                ok = false;
+                                break;
+                            }
+                            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                            const uint32_t a0 = saddr(smem + s * S::kStageBytes);
+                            const uint64_t da = S::kTransA ? desc_mn_sw128(a0) : desc_sw128(a0);
+                            const uint64_t db = S::kTransB ? desc_mn_sw128(a0 + S::kTileA) : desc_sw128(a0 + S::kTileA);
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk) {
-                        // 16 K further: 32 bytes inside the swizzle row, or two
-                        // 1024-byte atoms of an MN-major tile
-                        const uint64_t sa = uint64_t(kk * (S::kTransA ? 2048 : 32) >> 4);
-                        const uint64_t sb = uint64_t(kk * (S::kTransB ? 2048 : 32) >> 4);
-                        mma<CTAS>(d, da + sa, db + sb, kIdesc, (kt | kk) != 0);
+                            for (int kk = 0; kk < BK / 16; ++kk) {
+                                // 16 K further: 32 bytes inside the swizzle row, or two
+                                // 1024-byte atoms of an MN-major tile
+                                const uint64_t sa = uint64_t(kk * (S::kTransA ? 2048 : 32) >> 4);
+                                const uint64_t sb = uint64_t(kk * (S::kTransB ? 2048 : 32) >> 4);
+                                mma<CTAS>(d, da + sa, db + sb, kIdesc, more || kk != 0);
+                            }
+                            mma_commit<CTAS>(saddr(&empty[s]));
+                        }
+                        if (!ok) break;
+                        mma_commit<CTAS>(saddr(&acc_full[ab]));
                     }
-                    mma_commit<CTAS>(saddr(&empty[s]));
+                    if (!ok) break;
                 }
-                if (!ok) break;
-                mma_commit<CTAS>(saddr(&acc_full[ab]));
+                mma_commit<CTAS>(saddr(done));
+                if (!wait_parity(saddr(done), 0)) atomicAdd(&g_loss_timeouts, 1u);
             }
-            mma_commit<CTAS>(saddr(done));
-            if (!wait_parity(saddr(done), 0)) atomicAdd(&g_loss_timeouts, 1u);
         }
     } else {
-        // epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. +31, one row per thread
-        const int q = warp & 3;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+        // epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. +31, one row per
+        // thread, half of the columns.  The sums of each segment of K are added to
+        // the thread's registers: the tensor core's own fp32 sums drop bits towards
+        // zero at every step, an error that grows with the steps in one accumulator.
+        const int q = warp & 3, col0 = ((warp - 4) >> 2) * S::kCols;
         const uint32_t lane_base = uint32_t(q * 32) << 16;
+        const uint32_t boxes = saddr(ostage) + uint32_t(warp - 4) * kBoxBytes;
         uint32_t n_boxes = 0;
         float unscale = 1.0f, gscale = 1.0f;
         if constexpr (MODE == kGrad) gscale = p.scale[0] * p.inv_t;
         if constexpr (MODE == kData || MODE == kWeight) unscale = p.scale[1];
-        int lt = 0;
-        for (int t = cluster; t < n_tiles; t += n_clusters, ++lt) {
-            if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) break;
-            const int ab = lt & 1, use_acc = lt >> 1;
+        // a 32 x 32 box of 16-bit values in shared memory: row `lane` is 64 bytes, its
+        // 16-byte chunk c stored at chunk c ^ ((lane / 2) % 4)
+        const auto stage16 = [&](const uint32_t (&packed)[16]) {
+            const uint32_t buf = boxes + (n_boxes & 1) * (kBoxBytes / 2);
+            if (lane == 0 && n_boxes >= 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            __syncwarp();
+            const uint32_t at = buf + uint32_t(lane) * 64u, sw = (uint32_t(lane) >> 1) & 3u;
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c)
+                st_shared16(at + ((c ^ sw) << 4), packed[4 * c], packed[4 * c + 1], packed[4 * c + 2],
+                            packed[4 * c + 3]);
+            return buf;
+        };
+        int use = 0;
+        bool ok = true;
+        for (int t = cluster; t < n_tiles; t += n_clusters) {
             const Tile o = tile_of(p, t, m_blocks);
+            const int n_seg = (slices(o.split) + S::kSegment - 1) / S::kSegment;
             const int m = o.mb * S::kTileM + int(rank) * BM + q * 32 + lane;
-            const int n0 = o.nb * S::kTileN;
+            const int n0 = o.nb * S::kTileN + col0;         // this thread's first column
             const bool live = m < m_rows;
             // what this row needs, requested before the wait for its sums
             int row = m;
-            int64_t tgt = -1;           // its target, from the tile's first column
+            int64_t tgt = -1;           // its target, from the first column
             float coef = 0.0f, shift = 0.0f, at_target = 0.0f;
             int e = 0, next = INT32_MAX;
             if constexpr (MODE == kStats || MODE == kGrad) {
@@ -386,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if constexpr (MODE == kStats) {
                 if (p.index && live) {
-                    // the first of the row's sorted tokens that is not before this tile
+                    // the first of the row's sorted tokens that is not before this column
                     const int *list = p.index + int64_t(row) * p.top;
                     int hi = p.top;
                     while (e < hi) {
@@ -410,151 +447,161 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (MODE == kData) {
                 if (live && !all) row = p.rows[m];
             }
-            // tcgen05.ld is warp-collective: the whole warp takes one decision
-            const bool ok = __all_sync(0xFFFFFFFFu, wait_parity_sleep(saddr(&acc_full[ab]), use_acc & 1));
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            if (!ok) {
-                if (lane == 0) raise_abort();
-                break;
-            }
-            const uint32_t acc = tmem + lane_base + uint32_t(ab * S::kTileN);
-            float top = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-            for (int c0 = 0; c0 < S::kTileN; c0 += 32) {
-                uint32_t g[32];
-                __syncwarp();
-                tmem_ld32(acc + uint32_t(c0), g);
-                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                if (c0 + 32 == S::kTileN) {     // all of this tile read: hand the accumulator back
-                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CTAS == 1)
-                            arrive_local(saddr(&acc_empty[ab]));
-                        else
-                            arrive_cluster(mapa(saddr(&acc_empty[ab]), 0));
+            __syncwarp();
+            constexpr int kChunks = S::kCols / 32;
+            uint32_t sums[kChunks][32];
+            for (int seg = 0; seg < n_seg; ++seg, ++use) {
+                const int ab = use & 1, use_acc = use >> 1;
+                // tcgen05.ld is warp-collective: the whole warp takes one decision
+                ok = !__any_sync(0xFFFFFFFFu, *abort_flag != 0);
+                if (!ok) break;
+                ok = __all_sync(0xFFFFFFFFu, wait_parity_sleep(saddr(&acc_full[ab]), use_acc & 1));
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                if (!ok) {
+                    if (lane == 0) raise_abort();
+                    break;
+                }
+                const uint32_t acc = tmem + lane_base + uint32_t(ab * S::kTileN + col0);
+                if (seg == 0) {
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) tmem_ld32(acc + uint32_t(32 * c), sums[c]);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        uint32_t g[32];
+                        tmem_ld32(acc + uint32_t(32 * c), g);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            sums[c][j] = __float_as_uint(__uint_as_float(sums[c][j]) + __uint_as_float(g[j]));
                     }
                 }
-                const int left = p.cols - (n0 + c0);        // columns that exist
-                if (left <= 0) continue;
-                if constexpr (MODE == kStats) {
-                    if (tgt >= c0 && tgt < c0 + 32) p.named[m] = pick(g, int(tgt) - c0);
-                    while (next < n0 + c0 + 32) {
-                        p.named[int64_t(row) * p.top + e] = pick(g, next - n0 - c0);
+                // all of it read: hand the accumulator back
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CTAS == 1)
+                        arrive_local(saddr(&acc_empty[ab]));
+                    else
+                        arrive_cluster(mapa(saddr(&acc_empty[ab]), 0));
+                }
+            }
+            if (!ok) break;
+            if constexpr (MODE == kStats) {
+                const int width = p.cols - n0;              // columns that exist
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    uint32_t (&g)[32] = sums[c];
+                    if (tgt >= 32 * c && tgt < 32 * c + 32) p.named[m] = pick(g, int(tgt) - 32 * c);
+                    while (next < n0 + 32 * c + 32) {
+                        p.named[int64_t(row) * p.top + e] = pick(g, next - n0 - 32 * c);
                         ++e;
                         next = e < p.top ? p.index[int64_t(row) * p.top + e] : INT32_MAX;
                     }
-                    if (left < 32) {
+                    __syncwarp();
+                    if (width < 32 * c + 32) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) g[j] = j < left ? g[j] : 0xFF800000u;      // -inf
+                        for (int j = 0; j < 32; ++j) g[j] = 32 * c + j < width ? g[j] : 0xFF800000u;    // -inf
                     }
-                    // running maximum and sum, in units of log2
-                    float hi = __uint_as_float(g[0]);
 #pragma unroll
-                    for (int j = 1; j < 32; ++j) hi = fmaxf(hi, __uint_as_float(g[j]));
-                    hi = fmaxf(hi * p.c1, top);
-                    const float base = hi == -INFINITY ? 0.0f : hi;
-                    float s0 = sum * exp2_fast(top - base), s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+                    for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(g[j]));
+                }
+                // maximum and sum of exponentials, in units of log2
+                top *= p.c1;
+                const float base = top == -INFINITY ? 0.0f : top;
+                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        s0 += exp2_fast(fmaf(__uint_as_float(g[j]), p.c1, -base));
-                        s1 += exp2_fast(fmaf(__uint_as_float(g[j + 1]), p.c1, -base));
-                        s2 += exp2_fast(fmaf(__uint_as_float(g[j + 2]), p.c1, -base));
-                        s3 += exp2_fast(fmaf(__uint_as_float(g[j + 3]), p.c1, -base));
-                    }
-                    sum = (s0 + s1) + (s2 + s3);
-                    top = hi;
-                } else if constexpr (MODE == kGrad) {
+                for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        s[j & 3] += exp2_fast(fmaf(__uint_as_float(sums[c][j]), p.c1, -base));
+                if (live)
+                    p.part[int64_t(2 * o.nb + (col0 != 0)) * p.N + m] = make_float2(top, (s[0] + s[1]) + (s[2] + s[3]));
+            } else {
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const uint32_t (&g)[32] = sums[c];
+                    const int left = p.cols - (n0 + 32 * c);    // columns that exist
+                    if (left <= 0) continue;
+                    const int m_box = m - lane;
                     uint32_t packed[16];
+                    if constexpr (MODE == kGrad) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float f[2];
+                        for (int j = 0; j < 32; j += 2) {
+                            float f[2];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float v = coef * exp2_fast(fmaf(__uint_as_float(g[j + i]), p.c1, shift));
-                            f[i] = coef == 0.0f || j + i >= left ? 0.0f : v;
-                            if (tgt == c0 + j + i) f[i] = at_target;
+                            for (int i = 0; i < 2; ++i) {
+                                const float v = coef * exp2_fast(fmaf(__uint_as_float(g[j + i]), p.c1, shift));
+                                f[i] = coef == 0.0f || j + i >= left ? 0.0f : v;
+                                if (tgt == 32 * c + j + i) f[i] = at_target;
+                            }
+                            packed[j / 2] = Cd::put(f);
                         }
-                        packed[j / 2] = Cd::put(f);
-                    }
-                    // this warp's 32 rows x 32 columns: row `lane` is 64 bytes, its
-                    // 16-byte chunk c stored at chunk c ^ ((lane / 2) % 4)
-                    const uint32_t buf = saddr(ostage) + uint32_t(q * 2 + (n_boxes & 1)) * S::kBoxBytes;
-                    if (lane == 0 && n_boxes >= 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                    __syncwarp();
-                    const uint32_t at = buf + uint32_t(lane) * 64u, sw = (uint32_t(lane) >> 1) & 3u;
-#pragma unroll
-                    for (uint32_t c = 0; c < 4; ++c)
-                        st_shared16(at + ((c ^ sw) << 4), packed[4 * c], packed[4 * c + 1], packed[4 * c + 2],
-                                    packed[4 * c + 3]);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) tma_store(&tm_out, buf, n0 + c0, m - lane);
-                    ++n_boxes;
-                } else if (p.partial) {
-                    // fp32 sums of this part of K: rows of 128 bytes, chunk c at c ^ (lane % 8)
-                    const uint32_t buf = saddr(ostage) + uint32_t(q * 2 + (n_boxes & 1)) * S::kBoxBytes;
-                    if (lane == 0 && n_boxes >= 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                    __syncwarp();
-                    const uint32_t at = buf + uint32_t(lane) * 128u, sw = uint32_t(lane) & 7u;
-#pragma unroll
-                    for (uint32_t c = 0; c < 8; ++c)
-                        st_shared16(at + ((c ^ sw) << 4), g[4 * c], g[4 * c + 1], g[4 * c + 2], g[4 * c + 3]);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) {
-                        const int y = o.split * p.split_rows + m;
-                        if (p.partial == 1)
-                            tma_store(&tm_out, buf, n0 + c0, y);
-                        else
-                            tma_add(&tm_out, buf, n0 + c0, y);
-                    }
-                    ++n_boxes;
-                } else {
-                    uint32_t packed[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float f[2] = {__uint_as_float(g[j]) * unscale, __uint_as_float(g[j + 1]) * unscale};
-                        packed[j / 2] = Cd::put(f);
-                    }
-                    if (p.tma_store && (MODE == kWeight || all)) {
-                        const uint32_t buf = saddr(ostage) + uint32_t(q * 2 + (n_boxes & 1)) * S::kBoxBytes;
-                        if (lane == 0 && n_boxes >= 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    } else if (p.partial) {
+                        // fp32 sums of this part of K: rows of 128 bytes, chunk c at c ^ (lane % 8)
+                        if (lane == 0 && n_boxes >= 1) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                         __syncwarp();
-                        const uint32_t at = buf + uint32_t(lane) * 64u, sw = (uint32_t(lane) >> 1) & 3u;
+                        const uint32_t at = boxes + uint32_t(lane) * 128u, sw = uint32_t(lane) & 7u;
 #pragma unroll
-                        for (uint32_t c = 0; c < 4; ++c)
-                            st_shared16(at + ((c ^ sw) << 4), packed[4 * c], packed[4 * c + 1], packed[4 * c + 2],
-                                        packed[4 * c + 3]);
+                        for (uint32_t v = 0; v < 8; ++v)
+                            st_shared16(at + ((v ^ sw) << 4), g[4 * v], g[4 * v + 1], g[4 * v + 2], g[4 * v + 3]);
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
-                        if (lane == 0) tma_store(&tm_out, buf, n0 + c0, m - lane);
+                        if (lane == 0) {
+                            if (p.partial == 1)
+                                tma_store(&tm_out, boxes, n0 + 32 * c, o.split * p.split_rows + m_box);
+                            else
+                                tma_add(&tm_out, boxes, n0 + 32 * c, o.split * p.split_rows + m_box);
+                        }
+                        ++n_boxes;
+                        continue;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float f[2] = {__uint_as_float(g[j]) * unscale, __uint_as_float(g[j + 1]) * unscale};
+                            packed[j / 2] = Cd::put(f);
+                        }
+                    }
+                    if (MODE == kGrad || (p.tma_store && (MODE == kWeight || all))) {
+                        const uint32_t buf = stage16(packed);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) tma_store(&tm_out, buf, n0 + 32 * c, m_box);
                         ++n_boxes;
                         continue;
                     }
-                    if (!live) continue;
-                    char *dst = p.out + int64_t(row) * p.out_stride + int64_t(n0 + c0) * 2;
+                    char *dst = p.out + int64_t(row) * p.out_stride + int64_t(n0 + 32 * c) * 2;
                     if (p.vec_store && left >= 32) {
+                        if (!live) continue;
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
-                            const uint32_t w4[4] = {packed[4 * v], packed[4 * v + 1], packed[4 * v + 2],
-                                                    packed[4 * v + 3]};
+                            const uint32_t w4[4] = {packed[4 * v], packed[4 * v + 1], packed[4 * v + 2], packed[4 * v + 3]};
                             Access<16>::store(dst + 16 * v, w4);
                         }
-                    } else {
+                        continue;
+                    }
+                    // rows at any place: through shared memory, a row of 32 values to one access of the warp
+                    const uint32_t at = boxes + uint32_t(lane) * 68u;
+                    __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < left) Cd::store1(dst + j * 2, Cd::get(packed[j / 2], j % 2));
+                    for (int v = 0; v < 16; ++v)
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4u * v), "r"(packed[v]) : "memory");
+                    __syncwarp();
+                    const int rows_here = min(32, m_rows - m_box);
+                    for (int r = 0; r < rows_here; ++r) {
+                        const uint64_t to = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(dst), r);
+                        unsigned short v;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(boxes + uint32_t(r) * 68u + 2u * lane));
+                        if (lane < left) asm volatile("st.global.b16 [%0], %1;" ::"l"(to + 2 * lane), "h"(v) : "memory");
                     }
                 }
-            }
-            if constexpr (MODE == kStats) {
-                if (live) p.part[int64_t(o.nb) * p.N + m] = make_float2(top, sum);
             }
         }
         // every box this warp stored has left shared memory and reached global memory
         if (lane == 0 && n_boxes > 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        if (rank == 1 && warp == 2 && !wait_parity(saddr(done), 0) && lane == 0) atomicAdd(&g_loss_timeouts, 1u);
+        if (rank == 1 && warp == 4 && !wait_parity(saddr(done), 0) && lane == 0) atomicAdd(&g_loss_timeouts, 1u);
         __syncwarp();
     }
 
@@ -695,7 +742,7 @@ constexpr int kJoinThreads = 1024;
 
 struct JoinParams {
     const float2 *part;
-    int n_blocks, N;
+    int n_parts, N;
     const int *count, *rows;
     const float *named;
     const float *share;         // distillation: [N][top] teacher's probabilities, in the order of the sorted tokens
@@ -721,7 +768,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p)
     if (m0 >= count) return;
     float top = -INFINITY, sum = 0.0f;
     if (m < count) {
-        for (int b = warp; b < p.n_blocks; b += kJoinThreads / 32) {
+        for (int b = warp; b < p.n_parts; b += kJoinThreads / 32) {
             const float2 v = p.part[int64_t(b) * p.N + m];
             const float hi = fmaxf(top, v.x), base = hi == -INFINITY ? 0.0f : hi;
             sum = sum * exp2f(top - base) + v.y * exp2f(v.x - base);
@@ -1027,8 +1074,13 @@ int slots_of(const Variant &v, bool bf16, int dev, int sms, int *out)
     std::atomic<int> &slots = g_slots[dev % kMaxDevices][bf16][v.id];
     int n = slots.load(std::memory_order_acquire);
     if (n == 0) {
-        cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(v.fn),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+        // the warps' register split draws on what the kernel is launched with
+        cudaFuncAttributes fa{};
+        cudaError_t e = cudaFuncGetAttributes(&fa, reinterpret_cast<const void *>(v.fn));
+        if (e == cudaSuccess && fa.numRegs < kRegsLaunch) e = cudaErrorInvalidKernelImage;
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(reinterpret_cast<const void *>(v.fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     v.smem);
         if (e != cudaSuccess) {
             (void)cudaGetLastError();
             return glu::cuda_fail(e);
@@ -1129,10 +1181,13 @@ struct Call {
     bool backward, distill;
 };
 
+constexpr int kSms = 152;              // what the parts of K are counted for
+
 // How a pass divides its work and its workspace (offsets in bytes).
 struct Plan {
     int64_t piece;              // backward: tokens of a piece
     int pieces;
+    int ctas, bn;               // of the logits' product: blocks a tile, half its columns
     int data_splits, weight_splits;
     int64_t data_rows, weight_rows, ld;         // of a partial result; ld in floats
     int64_t g_stride, listed_stride;            // bytes
@@ -1172,7 +1227,6 @@ int pick_splits(int64_t tiles, int64_t k_tiles, int64_t slots)
     return best;
 }
 
-constexpr int kSms = 152;              // what the parts of K are counted for
 
 Plan make_plan(const Call &c, int64_t piece)
 {
@@ -1194,8 +1248,13 @@ Plan make_plan(const Call &c, int64_t piece)
         p.entries = take(4 * N);
         p.entropy = take(4 * N);
     }
+    // sized for the whole GPU whatever the device, so that the bytes asked for hold
+    p.ctas = c.N > BM ? 2 : 1;
+    const int64_t tile_m = BM * p.ctas, m_blocks = (c.N + tile_m - 1) / tile_m;
+    p.bn = pick_bn(m_blocks, c.backward ? piece : c.V, kSms / p.ctas, p.ctas == 1 ? round_up(c.N, 8) : tile_m);
     if (!c.backward) {
-        p.part = take(8 * N * uint64_t((c.V + 127) / 128));
+        // two halves of a tile, each joined by itself
+        p.part = take(16 * N * uint64_t((c.V + 2 * p.bn - 1) / (2 * p.bn)));
         p.named = take(4 * N * (c.distill ? top : 1));
     } else {
         p.piece = piece;
@@ -1203,10 +1262,8 @@ Plan make_plan(const Call &c, int64_t piece)
         p.g_stride = round_up(piece, 64) * 2;
         p.g = take(N * uint64_t(p.g_stride));
         p.ld = round_up(c.H, 4);
-        const int ctas = c.N > BM ? 2 : 1;
-        const int64_t tile_m = BM * ctas, n_blocks = (c.H + 255) / 256;
-        const int64_t m_blocks = (c.N + tile_m - 1) / tile_m;
-        p.data_splits = pick_splits(m_blocks * n_blocks, (piece + BK - 1) / BK, kSms / ctas);
+        const int64_t n_blocks = (c.H + 255) / 256;
+        p.data_splits = pick_splits(m_blocks * n_blocks, (piece + BK - 1) / BK, kSms / p.ctas);
         p.data_rows = m_blocks * tile_m;
         if (c.dx && (p.data_splits > 1 || p.pieces > 1))
             p.data = take(4 * uint64_t(p.data_splits) * uint64_t(p.data_rows) * uint64_t(p.ld));
@@ -1443,10 +1500,7 @@ struct Run {
     // The logits' product over tokens first .. first + cols.
     int logits(bool grad, int64_t first, int64_t cols, glu_launch_info_t *info) const
     {
-        const int ctas = c.N > BM ? 2 : 1;
-        const int64_t tile_m = int64_t(BM) * ctas;
-        const int64_t a_rows = ctas == 1 ? round_up(c.N, 8) : tile_m;
-        const int bn = pick_bn((c.N + tile_m - 1) / tile_m, cols, sms / ctas, a_rows);
+        const int ctas = plan.ctas, bn = plan.bn;
         Variant v{};
         if (!grad)
             v = ctas == 1 ? (bn == 64   ? variant<kStats, 64, 1>(bf16, 0)
@@ -1464,7 +1518,7 @@ struct Run {
                                         : variant<kGrad, 128, 2>(bf16, 11));
         // one block holding every row copies only the rows that exist (rounded up to a
         // swizzle atom): the MMA's other rows are never stored
-        const int box_a = ctas == 1 ? int(a_rows) : BM, box_b = ctas == 1 ? 2 * bn : bn;
+        const int box_a = ctas == 1 ? int(round_up(c.N, 8)) : BM, box_b = ctas == 1 ? 2 * bn : bn;
         CUtensorMap ta, tl, tb, to;
         const char *w = static_cast<const char *>(c.w) + first * c.w_stride * 2;
         if (!map16(&ta, c.x, c.N, c.H, c.x_stride * 2, BK, box_a, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -1549,7 +1603,7 @@ struct Run {
     // dx (+)= g w over the piece.
     int data(int64_t first, int64_t cols, bool add, glu_launch_info_t *info) const
     {
-        const int ctas = c.N > BM ? 2 : 1;
+        const int ctas = plan.ctas;
         const int bn = c.H <= 128 ? 64 : 128;
         const Variant v = ctas == 1 ? (bn == 64 ? variant<kData, 64, 1>(bf16, 12) : variant<kData, 128, 1>(bf16, 13))
                                     : (bn == 64 ? variant<kData, 64, 2>(bf16, 14) : variant<kData, 128, 2>(bf16, 15));
@@ -1626,9 +1680,7 @@ struct Run {
         if (int st = logits(false, 0, c.V, info)) return st;
         JoinParams j{};
         j.part = at<float2>(plan.part);
-        // the tiles the product formed: as many as its launch counted over all rows
-        const int64_t m_blocks = (c.N + BM * info->unroll - 1) / (BM * info->unroll);
-        j.n_blocks = int(info->vector_units / m_blocks);
+        j.n_parts = 2 * int((c.V + 2 * plan.bn - 1) / (2 * plan.bn));
         j.N = int(c.N);
         j.count = count();
         j.rows = rows();
