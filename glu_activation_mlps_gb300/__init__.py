@@ -18,6 +18,7 @@ Two levels:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -385,10 +386,14 @@ def glu_get_tuning() -> dict:
 
 def _dtype_code(t) -> int:
     import torch
-    m = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-    if t.dtype not in m:
-        raise TypeError(f"unsupported dtype {t.dtype}; expected float32, float16 or bfloat16")
-    return m[t.dtype]
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
+        return 2
+    if dtype is torch.float16:
+        return 1
+    if dtype is torch.float32:
+        return 0
+    raise TypeError(f"unsupported dtype {dtype}; expected float32, float16 or bfloat16")
 
 
 def _rows(t, name):
@@ -954,11 +959,21 @@ def mlp_q_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, w_down, down_scale
 # ---- losses over a vocabulary ------------------------------------------------------
 
 def _loss_in(x, w):
-    """(N, x's row stride, w's row stride, H, V, leading shape) of hidden rows and an output projection."""
-    if w.dim() != 2 or w.shape[1] != x.shape[-1] or w.dtype != x.dtype:
+    """(N, x's row stride, w's row stride, H, V, leading shape, dtype code) of hidden rows and an output projection."""
+    xs, ws = x.shape, w.shape
+    H = xs[-1]
+    if len(ws) != 2 or ws[1] != H or w.dtype != x.dtype:
         raise ValueError("w must be (V, H) with H = x.shape[-1] and x's dtype")
     n_rows, x_stride = _mat(x, "x")
-    return n_rows, x_stride, _mat(w, "w")[1], x.shape[-1], w.shape[0], x.shape[:-1]
+    return n_rows, x_stride, _mat(w, "w")[1], H, ws[0], xs[:-1], _dtype_code(x)
+
+
+@functools.lru_cache(maxsize=1024)
+def _loss_bytes(N, H, V, K, backward):
+    """Workspace bytes of a call (K = 0: cross entropy), 256 at least."""
+    if K:
+        return max(256, glu_linear_distill_workspace_bytes(N, H, V, K, backward))
+    return max(256, glu_linear_ce_workspace_bytes(N, H, V, backward))
 
 
 def _per_row(t, shape, name, like):
@@ -998,10 +1013,10 @@ def _gradient(t, like, name):
     return t, _mat(t, name)[1]
 
 
-def _loss_workspace(workspace, n_bytes, like):
+def _loss_workspace(workspace, like, *sizes):
     import torch
     if workspace is None:
-        return torch.empty(max(256, n_bytes), dtype=torch.uint8, device=like.device)
+        return torch.empty(_loss_bytes(*sizes), dtype=torch.uint8, device=like.device)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     return workspace
@@ -1021,11 +1036,10 @@ def linear_ce(x, w, target, *, loss=None, lse=None, workspace=None, stream=None)
     if stream is not None:
         return _on_stream(stream, linear_ce, x, w, target, loss=loss, lse=lse, workspace=workspace)
     dev = _same_device(x, w, target, loss, lse, workspace)
-    n_rows, x_stride, w_stride, H, V, lead = _loss_in(x, w)
-    code = _dtype_code(x)
+    n_rows, x_stride, w_stride, H, V, lead, code = _loss_in(x, w)
     t = _target(target, lead)
     loss, lse = _per_row(loss, lead, "loss", x), _per_row(lse, lead, "lse", x)
-    workspace = _loss_workspace(workspace, glu_linear_ce_workspace_bytes(n_rows, H, V, 0), x)
+    workspace = _loss_workspace(workspace, x, n_rows, H, V, 0, 0)
     st = glu_linear_ce_fwd(x.data_ptr(), x_stride, w.data_ptr(), w_stride, t, loss.data_ptr(), lse.data_ptr(), n_rows,
                            H, V, code, workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
     if st:
@@ -1042,15 +1056,14 @@ def linear_ce_bwd(dloss, x, w, target, loss, lse, *, dx=None, dw=None, workspace
     when not given."""
     if stream is not None:
         return _on_stream(stream, linear_ce_bwd, dloss, x, w, target, loss, lse, dx=dx, dw=dw, workspace=workspace)
-    n_rows, x_stride, w_stride, H, V, lead = _loss_in(x, w)
-    code = _dtype_code(x)
+    n_rows, x_stride, w_stride, H, V, lead, code = _loss_in(x, w)
     t = _target(target, lead)
     for v, name in ((dloss, "dloss"), (loss, "loss"), (lse, "lse")):
         _per_row(v, lead, name, x)
     dx, dx_stride = _gradient(dx, x, "dx")
     dw, dw_stride = _gradient(dw, w, "dw")
     dev = _same_device(x, w, target, dloss, loss, lse, dx, dw, workspace)
-    workspace = _loss_workspace(workspace, glu_linear_ce_workspace_bytes(n_rows, H, V, 1), x)
+    workspace = _loss_workspace(workspace, x, n_rows, H, V, 0, 1)
     st = glu_linear_ce_bwd(dloss.data_ptr(), x.data_ptr(), x_stride, w.data_ptr(), w_stride, t, loss.data_ptr(),
                            lse.data_ptr(), _ptr(dx), dx_stride, _ptr(dw), dw_stride, n_rows, H, V, code,
                            workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
@@ -1074,12 +1087,11 @@ def linear_distill(x, w, index, logit, temperature: float = 1.0, *, loss=None, l
         return _on_stream(stream, linear_distill, x, w, index, logit, temperature, loss=loss, lse=lse,
                           top_logits=top_logits, workspace=workspace)
     dev = _same_device(x, w, index, logit, loss, lse, top_logits, workspace)
-    n_rows, x_stride, w_stride, H, V, lead = _loss_in(x, w)
-    code = _dtype_code(x)
+    n_rows, x_stride, w_stride, H, V, lead, code = _loss_in(x, w)
     K, i_stride, l_stride, l_code = _teacher(index, logit, lead)
     loss, lse = _per_row(loss, lead, "loss", x), _per_row(lse, lead, "lse", x)
     top_logits = _per_row(top_logits, index.shape, "top_logits", x)
-    workspace = _loss_workspace(workspace, glu_linear_distill_workspace_bytes(n_rows, H, V, K, 0), x)
+    workspace = _loss_workspace(workspace, x, n_rows, H, V, K, 0)
     st = glu_linear_distill_fwd(x.data_ptr(), x_stride, w.data_ptr(), w_stride, index.data_ptr(), i_stride,
                                 logit.data_ptr(), l_stride, temperature, loss.data_ptr(), lse.data_ptr(),
                                 top_logits.data_ptr(), n_rows, H, V, K, code, l_code, workspace.data_ptr(),
@@ -1097,8 +1109,7 @@ def linear_distill_bwd(dloss, x, w, index, logit, lse, top_logits, temperature: 
     if stream is not None:
         return _on_stream(stream, linear_distill_bwd, dloss, x, w, index, logit, lse, top_logits, temperature, dx=dx,
                           dw=dw, workspace=workspace)
-    n_rows, x_stride, w_stride, H, V, lead = _loss_in(x, w)
-    code = _dtype_code(x)
+    n_rows, x_stride, w_stride, H, V, lead, code = _loss_in(x, w)
     K, i_stride, l_stride, l_code = _teacher(index, logit, lead)
     _per_row(dloss, lead, "dloss", x)
     _per_row(lse, lead, "lse", x)
@@ -1106,7 +1117,7 @@ def linear_distill_bwd(dloss, x, w, index, logit, lse, top_logits, temperature: 
     dx, dx_stride = _gradient(dx, x, "dx")
     dw, dw_stride = _gradient(dw, w, "dw")
     dev = _same_device(x, w, index, logit, dloss, lse, top_logits, dx, dw, workspace)
-    workspace = _loss_workspace(workspace, glu_linear_distill_workspace_bytes(n_rows, H, V, K, 1), x)
+    workspace = _loss_workspace(workspace, x, n_rows, H, V, K, 1)
     st = glu_linear_distill_bwd(dloss.data_ptr(), x.data_ptr(), x_stride, w.data_ptr(), w_stride, index.data_ptr(),
                                 i_stride, logit.data_ptr(), l_stride, temperature, lse.data_ptr(),
                                 top_logits.data_ptr(), _ptr(dx), dx_stride, _ptr(dw), dw_stride, n_rows, H, V, K, code,

@@ -61,8 +61,7 @@ constexpr int kEpiWarps = 8;            // 32 rows each, in two halves of the co
 constexpr int kRegsLaunch = 168, kRegsFew = 72, kRegsMany = 216;
 static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads * kRegsLaunch, "the split fits the launch");
 constexpr int kRingBytes = 192 * 1024;
-constexpr int kBox = 32;                // outputs leave through 32 x 32 boxes
-constexpr int kBoxBytes = 4096;         // staging of a warp: one box of floats or two of 16 bits
+constexpr int kBoxBytes = 4096;         // fp32 sums leave through boxes of 32 rows x 32 columns
 constexpr int kChunkBytes = 64 * BK * 2;    // an MN-major box: 64 columns x 64 K
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -87,7 +86,7 @@ struct Shape {
     static constexpr int kTileM = BM * CTAS;
     static constexpr int kTmemCols = 2 * kTileN <= 256 ? 256 : 512;     // two accumulators
     static constexpr int kBars = 2 * kStages + 2 + 2 + 1;               // full, empty, acc_full, acc_empty, done
-    static constexpr int kStageOut = MODE == kStats ? 0 : kEpiWarps * kBoxBytes;
+    static constexpr int kStageOut = MODE == kData || MODE == kWeight ? kEpiWarps * kBoxBytes : 0;
     static constexpr int kCols = kTileN / 2;                            // columns of one epilogue thread
     // K slices summed in tensor memory before their sum goes to registers
     static constexpr int kSegment = MODE == kStats || MODE == kGrad ? 16 : 64;
@@ -98,6 +97,14 @@ struct Shape {
     static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
 };
 
+// The last tiles of a gradient's product, which would leave most of the GPU idle
+// for a round, are cut along K: tiles from `whole` on into `parts` parts each,
+// whose fp32 sums are kept apart (part q of tile whole + i is number q * tail +
+// i) and added in their order by sum_kernel.
+struct Cut {
+    int whole, parts;
+};
+
 struct Params {
     const int *count;           // rows that take part; rows[] lists them
     const int *rows;
@@ -106,7 +113,7 @@ struct Params {
     int depth;                  // K: H (stats, grad), the piece's vocabulary (data); weight: the count
     int m_rows;                 // rows of the output for weight: the piece's vocabulary
     int n_blocks;
-    int splits;                 // data, weight: parts of K, one partial result each
+    const Cut *cut;             // data, weight
     int group_m;                // row blocks per group of the tile order
     uint32_t a_bytes;           // bytes of the A box (stats, grad, data: rows that exist, up to 128)
     // stats
@@ -124,9 +131,8 @@ struct Params {
     // data, weight
     char *out;
     int64_t out_stride;         // bytes
-    int vec_store, tma_store;
-    int partial;                // 1: fp32 partial results, 2: added to what is there
-    int split_rows;             // rows of one partial result
+    int vec_store;              // rows are 32- or 16-byte aligned; 0: at any place
+    int sums;                   // fp32 sums of this piece instead of results: 1 stored, 2 added to the last piece's
 };
 
 static __device__ unsigned int g_loss_timeouts;
@@ -154,11 +160,32 @@ __device__ __forceinline__ void tma_add(const CUtensorMap *map, uint32_t src, in
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
+// An arrival on the other block's barrier that hands back tensor memory.  What it
+// orders, the tensor-memory reads, is complete (wait::ld); a release to the cluster
+// would wait for this thread's global stores of the tile before as well.
+__device__ __forceinline__ void arrive_remote(uint32_t bar_cluster)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 __device__ __forceinline__ float exp2_fast(float v)
 {
     float r;
     asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
+}
+
+// 32 values of 16 bits to 64 bytes of a row, 32-byte aligned.  A thread writes its
+// own row: whole 32-byte sectors, no staging and no fence before a copy engine
+// (64 rows of x, 32768 x 4096 of dw: XXX us through staged boxes, YYY like this).
+__device__ __forceinline__ void store_row(char *dst, const uint32_t (&w)[16])
+{
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        const uint32_t w8[8] = {w[8 * v],     w[8 * v + 1], w[8 * v + 2], w[8 * v + 3],
+                                w[8 * v + 4], w[8 * v + 5], w[8 * v + 6], w[8 * v + 7]};
+        Access<32>::store(dst + 32 * v, w8);
+    }
 }
 
 // Element j of a row's 32 registers, j known at run time only.
@@ -170,31 +197,60 @@ __device__ __forceinline__ float pick(const uint32_t (&g)[32], int j)
     return __uint_as_float(v);
 }
 
-// Tile t: which part of K, row block and column block.
+// Tile t: row block and column block.
 struct Tile {
-    int split, mb, nb;
+    int mb, nb;
 };
 
-__device__ __forceinline__ Tile tile_of(const Params &p, int t, int m_blocks)
+__device__ __forceinline__ Tile tile_of(int group_m, int n_blocks, int t, int m_blocks)
 {
-    const int per_split = m_blocks * p.n_blocks;
-    Tile o;
-    o.split = t / per_split;
-    t -= o.split * per_split;
-    const int per_group = p.group_m * p.n_blocks;
-    const int first_m = (t / per_group) * p.group_m;
-    const int gsize = min(m_blocks - first_m, p.group_m);
+    const int per_group = group_m * n_blocks;
+    const int first_m = (t / per_group) * group_m;
+    const int gsize = min(m_blocks - first_m, group_m);
     const int r = t % per_group;
-    o.mb = first_m + r % gsize;
-    o.nb = r / gsize;
-    return o;
+    return {first_m + r % gsize, r / gsize};
 }
+
+constexpr int kMaxParts = 16;
+constexpr int kTailRounds = 4;          // tail parts: at most this many rounds of the GPU
+
+// The cheapest cut, counted in slices of K of a slot, a round costing 8 more to
+// start and to store; parts of 4 slices at least.  No cut for less than 4 %.  Lane
+// s tries s parts, of the last round's tiles or of the last two rounds'.
+__device__ __forceinline__ Cut cut_of(int tiles, int k_tiles, int slots, int lane)
+{
+    const int rem = tiles % slots;
+    const uint32_t none = uint32_t((tiles + slots - 1) / slots) * uint32_t(k_tiles + 8);
+    uint32_t cost = UINT32_MAX;
+    int whole = tiles;
+    if (rem != 0 && lane >= 2 && lane <= kMaxParts && k_tiles >= 4 * lane && tiles < 26 * slots) {
+        for (int tail = rem; tail <= tiles && tail <= rem + slots && tail * lane <= kTailRounds * slots; tail += slots) {
+            const uint32_t v = uint32_t((tiles - tail) / slots) * uint32_t(k_tiles + 8) +
+                               uint32_t((tail * lane + slots - 1) / slots) * uint32_t((k_tiles + lane - 1) / lane + 8);
+            if (v < cost) {
+                cost = v;
+                whole = tiles - tail;
+            }
+        }
+    }
+    const uint32_t best = __reduce_min_sync(0xFFFFFFFFu, cost);
+    if (best >= none - none / 25) return {tiles, 1};
+    const int from = __ffs(__ballot_sync(0xFFFFFFFFu, cost == best)) - 1;
+    return {__shfl_sync(0xFFFFFFFFu, whole, from), from};
+}
+
+// A block's work item: its tile, the slices of K, and its number among the parts
+// kept apart (-1: none).
+struct Item {
+    Tile tile;
+    int k0, n_k, part;
+};
 
 template <int MODE, class T, int BN, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1)
     loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_listed, const __grid_constant__ CUtensorMap tm_out,
-                     const Params p)
+                     const __grid_constant__ CUtensorMap tm_tail, const Params p)
 {
     using S = Shape<MODE, BN, CTAS>;
     using Cd = Codec<T>;
@@ -257,18 +313,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // What depends on how many rows take part.  With none there is still one
     // block of rows (or one slice of K): it reads zeros and gives zeros.
-    const int count = *reinterpret_cast<const volatile int *>(p.count);
+    const int count = p.count ? *reinterpret_cast<const volatile int *>(p.count) : p.N;
     const bool all = count == p.N;
     const int m_rows = MODE == kWeight ? p.m_rows : count;
     const int m_blocks = max(1, (m_rows + S::kTileM - 1) / S::kTileM);
     const int k_tiles = max(1, ((MODE == kWeight ? count : p.depth) + BK - 1) / BK);
-    const int per_split = (k_tiles + p.splits - 1) / p.splits;
-    const int n_tiles = m_blocks * p.n_blocks * p.splits;
-    // K slices of a part: one at least; the last parts of a K that shrank with
-    // the count read past the matrix, zeros
-    auto slices = [&](int split) { return max(1, min(per_split, k_tiles - split * per_split)); };
-    auto slice0 = [&](int split) {
-        return split * per_split < k_tiles ? split * per_split : (max(p.N, p.depth) + BK - 1) / BK;
+    const int n_tiles = m_blocks * p.n_blocks;
+    const Cut cut = MODE == kData || MODE == kWeight ? *p.cut : Cut{n_tiles, 1};
+    const int tail = n_tiles - cut.whole, per_part = (k_tiles + cut.parts - 1) / cut.parts;
+    const int n_items = cut.whole + tail * cut.parts;
+    const auto item_of = [&](int t) {
+        Item o;
+        o.part = t < cut.whole ? -1 : t - cut.whole;
+        const int q = o.part < 0 ? 0 : o.part / tail;
+        o.tile = tile_of(p.group_m, p.n_blocks, t - q * tail, m_blocks);
+        o.k0 = q * per_part;
+        o.n_k = o.part < 0 ? k_tiles : min(per_part, k_tiles - o.k0);
+        return o;
     };
 
     if (warp < 4) {
@@ -279,12 +340,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const CUtensorMap *mbp = MODE == kWeight && !all ? &tm_listed : &tm_b;
                 const uint32_t bytes = p.a_bytes + uint32_t(S::kTileB);
                 uint32_t it = 0;
-                for (int t = cluster; t < n_tiles && !*abort_flag; t += n_clusters) {
-                    const Tile o = tile_of(p, t, m_blocks);
-                    const int m0 = o.mb * S::kTileM + int(rank) * BM;
-                    const int n0 = o.nb * S::kTileN + int(rank) * (CTAS == 1 ? 0 : BN);
-                    const int n_k = slices(o.split), k0 = slice0(o.split);
-                    for (int kt = 0; kt < n_k; ++kt, ++it) {
+                for (int t = cluster; t < n_items && !*abort_flag; t += n_clusters) {
+                    const Item o = item_of(t);
+                    const int m0 = o.tile.mb * S::kTileM + int(rank) * BM;
+                    const int n0 = o.tile.nb * S::kTileN + int(rank) * (CTAS == 1 ? 0 : BN);
+                    for (int kt = 0; kt < o.n_k; ++kt, ++it) {
                         const uint32_t s = it % ST, use = it / ST;
                         if (*abort_flag) break;
                         if (use > 0 && !wait_parity(saddr(&empty[s]), (use - 1) & 1)) {
@@ -292,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                         const uint32_t st = saddr(smem + s * S::kStageBytes);
-                        const int k = (k0 + kt) * BK;
+                        const int k = (o.k0 + kt) * BK;
                         // both blocks' copies count on block 0's barrier
                         uint32_t bar = saddr(&full[s]);
                         if (rank == 0)
@@ -330,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0 && rank == 0) {
                 uint32_t it = 0;
                 int use = 0;                // accumulators filled so far
-                for (int t = cluster; t < n_tiles && !*abort_flag; t += n_clusters) {
-                    const int n_k = slices(tile_of(p, t, m_blocks).split);
+                for (int t = cluster; t < n_items && !*abort_flag; t += n_clusters) {
+                    const int n_k = item_of(t).n_k;
                     bool ok = true;
                     for (int kt = 0; kt < n_k; ++use) {
                         const int ab = use & 1, use_acc = use >> 1, end = min(n_k, kt + S::kSegment);
@@ -385,30 +445,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3, col0 = ((warp - 4) >> 2) * S::kCols;
         const uint32_t lane_base = uint32_t(q * 32) << 16;
         const uint32_t boxes = saddr(ostage) + uint32_t(warp - 4) * kBoxBytes;
-        uint32_t n_boxes = 0;
+        bool boxed = false;             // a box of this warp is with the copy engine
         float unscale = 1.0f, gscale = 1.0f;
         if constexpr (MODE == kGrad) gscale = p.scale[0] * p.inv_t;
         if constexpr (MODE == kData || MODE == kWeight) unscale = p.scale[1];
-        // a 32 x 32 box of 16-bit values in shared memory: row `lane` is 64 bytes, its
-        // 16-byte chunk c stored at chunk c ^ ((lane / 2) % 4)
-        const auto stage16 = [&](const uint32_t (&packed)[16]) {
-            const uint32_t buf = boxes + (n_boxes & 1) * (kBoxBytes / 2);
-            if (lane == 0 && n_boxes >= 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            __syncwarp();
-            const uint32_t at = buf + uint32_t(lane) * 64u, sw = (uint32_t(lane) >> 1) & 3u;
-#pragma unroll
-            for (uint32_t c = 0; c < 4; ++c)
-                st_shared16(at + ((c ^ sw) << 4), packed[4 * c], packed[4 * c + 1], packed[4 * c + 2],
-                            packed[4 * c + 3]);
-            return buf;
-        };
         int use = 0;
         bool ok = true;
-        for (int t = cluster; t < n_tiles; t += n_clusters) {
-            const Tile o = tile_of(p, t, m_blocks);
-            const int n_seg = (slices(o.split) + S::kSegment - 1) / S::kSegment;
-            const int m = o.mb * S::kTileM + int(rank) * BM + q * 32 + lane;
-            const int n0 = o.nb * S::kTileN + col0;         // this thread's first column
+        for (int t = cluster; t < n_items; t += n_clusters) {
+            const Item o = item_of(t);
+            const int n_seg = (o.n_k + S::kSegment - 1) / S::kSegment;
+            const int m = o.tile.mb * S::kTileM + int(rank) * BM + q * 32 + lane;
+            const int n0 = o.tile.nb * S::kTileN + col0;    // this thread's first column
             const bool live = m < m_rows;
             // what this row needs, requested before the wait for its sums
             int row = m;
@@ -484,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (CTAS == 1)
                         arrive_local(saddr(&acc_empty[ab]));
                     else
-                        arrive_cluster(mapa(saddr(&acc_empty[ab]), 0));
+                        arrive_remote(mapa(saddr(&acc_empty[ab]), 0));
                 }
             }
             if (!ok) break;
@@ -518,30 +565,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 32; ++j)
                         s[j & 3] += exp2_fast(fmaf(__uint_as_float(sums[c][j]), p.c1, -base));
                 if (live)
-                    p.part[int64_t(2 * o.nb + (col0 != 0)) * p.N + m] = make_float2(top, (s[0] + s[1]) + (s[2] + s[3]));
+                    p.part[int64_t(2 * o.tile.nb + (col0 != 0)) * p.N + m] = make_float2(top, (s[0] + s[1]) + (s[2] + s[3]));
             } else {
+                const int m_box = m - lane;
+                const bool floats = (MODE == kData || MODE == kWeight) && (o.part >= 0 || p.sums);
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
                     const uint32_t (&g)[32] = sums[c];
                     const int left = p.cols - (n0 + 32 * c);    // columns that exist
                     if (left <= 0) continue;
-                    const int m_box = m - lane;
-                    uint32_t packed[16];
-                    if constexpr (MODE == kGrad) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            float f[2];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const float v = coef * exp2_fast(fmaf(__uint_as_float(g[j + i]), p.c1, shift));
-                                f[i] = coef == 0.0f || j + i >= left ? 0.0f : v;
-                                if (tgt == 32 * c + j + i) f[i] = at_target;
-                            }
-                            packed[j / 2] = Cd::put(f);
-                        }
-                    } else if (p.partial) {
-                        // fp32 sums of this part of K: rows of 128 bytes, chunk c at c ^ (lane % 8)
-                        if (lane == 0 && n_boxes >= 1) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    if (floats) {
+                        // fp32 sums: rows of 128 bytes, 16-byte chunk v at v ^ (lane % 8)
+                        if (lane == 0 && boxed) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        boxed = true;
                         __syncwarp();
                         const uint32_t at = boxes + uint32_t(lane) * 128u, sw = uint32_t(lane) & 7u;
 #pragma unroll
@@ -550,39 +586,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
                         if (lane == 0) {
-                            if (p.partial == 1)
-                                tma_store(&tm_out, boxes, n0 + 32 * c, o.split * p.split_rows + m_box);
+                            const CUtensorMap *map = o.part < 0 ? &tm_out : &tm_tail;
+                            const int x = o.part < 0 ? n0 + 32 * c : col0 + 32 * c;
+                            const int y = o.part < 0 ? m_box : o.part * S::kTileM + (m_box - o.tile.mb * S::kTileM);
+                            if (p.sums == 2)
+                                tma_add(map, boxes, x, y);
                             else
-                                tma_add(&tm_out, boxes, n0 + 32 * c, o.split * p.split_rows + m_box);
+                                tma_store(map, boxes, x, y);
                         }
-                        ++n_boxes;
                         continue;
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const float f[2] = {__uint_as_float(g[j]) * unscale, __uint_as_float(g[j + 1]) * unscale};
-                            packed[j / 2] = Cd::put(f);
-                        }
                     }
-                    if (MODE == kGrad || (p.tma_store && (MODE == kWeight || all))) {
-                        const uint32_t buf = stage16(packed);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) tma_store(&tm_out, buf, n0 + 32 * c, m_box);
-                        ++n_boxes;
-                        continue;
+                    uint32_t packed[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        float f[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float z = __uint_as_float(g[j + i]);
+                            if constexpr (MODE == kGrad) {
+                                const float v = coef * exp2_fast(fmaf(z, p.c1, shift));
+                                f[i] = coef == 0.0f || j + i >= left ? 0.0f : v;
+                                if (tgt == 32 * c + j + i) f[i] = at_target;
+                            } else {
+                                f[i] = z * unscale;
+                            }
+                        }
+                        packed[j / 2] = Cd::put(f);
                     }
                     char *dst = p.out + int64_t(row) * p.out_stride + int64_t(n0 + 32 * c) * 2;
-                    if (p.vec_store && left >= 32) {
-                        if (!live) continue;
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const uint32_t w4[4] = {packed[4 * v], packed[4 * v + 1], packed[4 * v + 2], packed[4 * v + 3]};
-                            Access<16>::store(dst + 16 * v, w4);
+                    if constexpr (MODE == kGrad) {
+                        // whole chunks: a row of g has room for them; rows past the listed ones are 0
+                        if (m < p.N) {
+                            dst = p.out + int64_t(m) * p.out_stride + int64_t(n0 + 32 * c) * 2;
+                            store_row(dst, packed);
                         }
                         continue;
                     }
-                    // rows at any place: through shared memory, a row of 32 values to one access of the warp
+                    if (p.vec_store) {
+                        if (!live) continue;
+                        if (left >= 32 && p.vec_store == 32) {
+                            store_row(dst, packed);
+                            continue;
+                        }
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const uint32_t w4[4] = {packed[4 * v], packed[4 * v + 1], packed[4 * v + 2],
+                                                    packed[4 * v + 3]};
+                            if (8 * v + 8 <= left) {
+                                Access<16>::store(dst + 16 * v, w4);
+                            } else {
+#pragma unroll
+                                for (int j = 8 * v; j < 8 * v + 8; ++j)
+                                    if (j < left) Cd::store1(dst + j * 2, Cd::get(packed[j / 2], j % 2));
+                            }
+                        }
+                        continue;
+                    }
+                    // rows at any place: through shared memory, 32 values of a row to one access
+                    // of the warp (tiles that leave through boxes come after these, if at all)
                     const uint32_t at = boxes + uint32_t(lane) * 68u;
                     __syncwarp();
 #pragma unroll
@@ -600,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // every box this warp stored has left shared memory and reached global memory
-        if (lane == 0 && n_boxes > 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (lane == 0 && boxed) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (rank == 1 && warp == 4 && !wait_parity(saddr(done), 0) && lane == 0) atomicAdd(&g_loss_timeouts, 1u);
         __syncwarp();
     }
@@ -640,6 +701,9 @@ struct ListParams {
     float *scale;               // backward: what g is scaled by (and its inverse)
     int f16;
     float inv_t;
+    Cut *cut;                   // backward: of dx's product, dw's, and dw's for the last piece
+    int data_blocks, data_tile_m, data_k_tiles, data_slots;
+    int weight_tiles, last_tiles, weight_slots;
 };
 
 __device__ __forceinline__ bool takes_part(const ListParams &p, int i)
@@ -719,6 +783,18 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const ListParams p)
             p.scale[1] = 1.0f / s;
         }
     }
+    if (blockIdx.x == 0 && warp == 1 && p.cut) {
+        const Cut data = cut_of(max(1, (total + p.data_tile_m - 1) / p.data_tile_m) * p.data_blocks, p.data_k_tiles,
+                                p.data_slots, lane);
+        const int k_tiles = max(1, (total + BK - 1) / BK);
+        const Cut weight = cut_of(p.weight_tiles, k_tiles, p.weight_slots, lane);
+        const Cut last = cut_of(p.last_tiles, k_tiles, p.weight_slots, lane);
+        if (lane == 0) {
+            p.cut[0] = data;
+            p.cut[1] = weight;
+            p.cut[2] = last;
+        }
+    }
     if (total == p.N) return;
     __syncthreads();
     for (int i = first + warp; i < last; i += kListThreads / 32) {
@@ -743,7 +819,9 @@ constexpr int kJoinThreads = 1024;
 struct JoinParams {
     const float2 *part;
     int n_parts, N;
-    const int *count, *rows;
+    const int *count, *rows;    // NULL: nothing was listed, every row is here
+    const int64_t *target;
+    int64_t V;
     const float *named;
     const float *share;         // distillation: [N][top] teacher's probabilities, in the order of the sorted tokens
     const int *order;           //               and where each stands in the caller's order
@@ -763,7 +841,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int count = *p.count;
+    const int count = p.count ? *p.count : p.N;
     const int m0 = blockIdx.x * kJoinRows, m = m0 + lane;
     if (m0 >= count) return;
     float top = -INFINITY, sum = 0.0f;
@@ -789,8 +867,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p)
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
     const int row = count == p.N ? m0 + r : p.rows[m0 + r];
+    if (p.target ? uint64_t(p.target[row]) >= uint64_t(p.V) : p.entries[row] == 0) {    // takes no part
+        if (lane == 0) p.loss[row] = p.lse[row] = 0.0f;
+        return;
+    }
     const float l2 = log2f(s);
-    if (!p.share) {
+    if (p.target) {
         if (lane == 0) {
             p.loss[row] = kLn2 * (l2 - fmaf(p.named[m0 + r], p.c1, -base));
             p.lse[row] = kLn2 * (base + l2);
@@ -964,45 +1046,64 @@ __global__ void __launch_bounds__(128) named_grad_kernel(const NamedParams p)
 }
 
 struct SumParams {
-    const float *part;
+    const float *tail;          // parts of tile_m x tile_n sums
+    const float *sums;          // several pieces: the sums of the tiles that were not cut
     int64_t ld;                 // floats
-    int split_rows, splits;
-    const int *count, *rows;    // NULL: every row, where it stands
-    int N, cols, m_rows;
+    const int *count, *rows;
+    int weight;                 // the rows are tokens, K the listed rows (else the other way round)
+    int N, cols, m_rows, n_blocks, group_m, tile_m, tile_n;
+    const Cut *cut;
     const float *scale;
     char *out;
     int64_t out_stride;         // bytes
 };
 
-// Partial results added in the order of the parts and rounded once.
+// The tiles kept as fp32 sums, rounded once: their parts added in order.
 template <class T>
 __global__ void __launch_bounds__(256) sum_kernel(const SumParams p)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int count = p.rows ? *p.count : p.m_rows;
+    const int count = *p.count;
+    const int m_rows = p.weight ? p.m_rows : count;
+    const int m_blocks = max(1, (m_rows + p.tile_m - 1) / p.tile_m);
+    const int n_tiles = m_blocks * p.n_blocks;
+    const Cut cut = *p.cut;
+    const int tail = n_tiles - cut.whole;
     const float unscale = p.scale[1];
-    const int quads = (p.cols + 3) / 4;
     const bool vec = (uintptr_t(p.out) % 8) == 0 && p.out_stride % 8 == 0;
-    const int64_t n = int64_t(count) * quads;
+    const int quads = p.tile_n / 4, per_tile = p.tile_m * quads;
+    const int first = p.sums ? 0 : cut.whole;
+    const int64_t n = int64_t(n_tiles - first) * per_tile;
     for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
-        const int m = int(i / quads), c = int(i % quads) * 4;
-        const float *src = p.part + int64_t(m) * p.ld + c;
-        float4 a = *reinterpret_cast<const float4 *>(src);
-        for (int s = 1; s < p.splits; ++s) {
-            const float4 b = *reinterpret_cast<const float4 *>(src + int64_t(s) * p.split_rows * p.ld);
-            a.x += b.x;
-            a.y += b.y;
-            a.z += b.z;
-            a.w += b.w;
+        const int t = first + int(i / per_tile), j = int(i % per_tile);
+        const Tile o = tile_of(p.group_m, p.n_blocks, t, m_blocks);
+        const int r = j / quads, x = j % quads * 4;
+        const int m = o.mb * p.tile_m + r, c = o.nb * p.tile_n + x;
+        if (m >= m_rows || c >= p.cols) continue;
+        float4 a;
+        if (t < cut.whole) {
+            a = *reinterpret_cast<const float4 *>(p.sums + int64_t(m) * p.ld + c);
+        } else {
+            const float *src = p.tail + (int64_t(t - cut.whole) * p.tile_m + r) * p.tile_n + x;
+            const int64_t step = int64_t(tail) * p.tile_m * p.tile_n;
+            a = *reinterpret_cast<const float4 *>(src);
+#pragma unroll 4
+            for (int s = 1; s < cut.parts; ++s) {
+                const float4 b = *reinterpret_cast<const float4 *>(src + s * step);
+                a.x += b.x;
+                a.y += b.y;
+                a.z += b.z;
+                a.w += b.w;
+            }
         }
-        const int row = p.rows && count != p.N ? p.rows[m] : m;
+        const int row = !p.weight && count != p.N ? p.rows[m] : m;
         char *dst = p.out + int64_t(row) * p.out_stride + int64_t(c) * 2;
         const float f[4] = {a.x * unscale, a.y * unscale, a.z * unscale, a.w * unscale};
         if (vec && c + 4 <= p.cols) {
             *reinterpret_cast<uint2 *>(dst) = make_uint2(Codec<T>::put(f), Codec<T>::put(f + 2));
         } else {
-            for (int j = 0; j < 4 && c + j < p.cols; ++j) Codec<T>::store1(dst + 2 * j, f[j]);
+            for (int e = 0; e < 4 && c + e < p.cols; ++e) Codec<T>::store1(dst + 2 * e, f[e]);
         }
     }
 }
@@ -1049,7 +1150,7 @@ bool make_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, int64_
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-using GemmFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Params);
+using GemmFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Params);
 
 struct Variant {
     GemmFn fn;
@@ -1188,10 +1289,10 @@ struct Plan {
     int64_t piece;              // backward: tokens of a piece
     int pieces;
     int ctas, bn;               // of the logits' product: blocks a tile, half its columns
-    int data_splits, weight_splits;
-    int64_t data_rows, weight_rows, ld;         // of a partial result; ld in floats
+    int64_t tail_rows;          // rows of the parts of tiles that are kept apart
+    int64_t ld;                 // of the sums over pieces, in floats
     int64_t g_stride, listed_stride;            // bytes
-    uint64_t rows, listed, part, named, sorted, order, entries, share, entropy, g, data, weight, bytes;
+    uint64_t rows, listed, part, named, sorted, order, entries, share, entropy, g, tail, sums, bytes;
 };
 
 // Column-tile width of the logits' product: the fewest rows of x and w moved,
@@ -1211,22 +1312,8 @@ int pick_bn(int64_t m_blocks, int64_t V, int64_t slots, int64_t a_rows)
     return best;
 }
 
-// Parts of K for a product with few tiles: the fewest rounds, a part counted with
-// the 8 slices that it costs to start and to store; 8 slices a part at least.
-int pick_splits(int64_t tiles, int64_t k_tiles, int64_t slots)
-{
-    int best = 1;
-    int64_t best_cost = -1;
-    for (int s = 1; s <= 32 && (s == 1 || k_tiles / s >= 8); ++s) {
-        const int64_t cost = (tiles * s + slots - 1) / slots * ((k_tiles + s - 1) / s + 8);
-        if (best_cost < 0 || cost < best_cost) {
-            best = s;
-            best_cost = cost;
-        }
-    }
-    return best;
-}
-
+// Half the columns of a gradient product's tile.
+int grad_bn(int64_t H) { return H <= 128 ? 64 : 128; }
 
 Plan make_plan(const Call &c, int64_t piece)
 {
@@ -1239,7 +1326,7 @@ Plan make_plan(const Call &c, int64_t piece)
     };
     const uint64_t N = uint64_t(c.N), top = uint64_t(c.top);
     p.listed_stride = round_up(c.H, 8) * 2;
-    p.rows = take(4 * N + 64);          // the count, the scale and its inverse, then the list (from byte 64)
+    p.rows = take(4 * N + 64);          // the count, the scale and its inverse, the cuts, then the list (from byte 64)
     p.listed = take(N * uint64_t(p.listed_stride));
     if (c.distill) {
         p.sorted = take(4 * N * top);
@@ -1261,17 +1348,20 @@ Plan make_plan(const Call &c, int64_t piece)
         p.pieces = int((c.V + piece - 1) / piece);
         p.g_stride = round_up(piece, 64) * 2;
         p.g = take(N * uint64_t(p.g_stride));
+        // The parts of the tiles that are cut: of both gradients, one after the other
+        // on the stream, whatever number of rows takes part.
+        const int64_t tile_n = grad_bn(c.H) * 2, n_blocks = (c.H + tile_n - 1) / tile_n;
+        const auto room = [&](int64_t tiles, int64_t k_tiles, int64_t slots) {
+            const int64_t most = tiles * kMaxParts < kTailRounds * slots ? tiles * kMaxParts : kTailRounds * slots;
+            return k_tiles < 8 ? int64_t(0) : most;
+        };
+        const int64_t data = c.dx ? room(m_blocks * n_blocks, (piece + BK - 1) / BK, kSms / p.ctas) * tile_m : 0;
+        const int64_t weight =
+            c.dw ? room((piece + 255) / 256 * n_blocks, (c.N + BK - 1) / BK, kSms / 2) * 256 : 0;
+        p.tail_rows = data > weight ? data : weight;
+        p.tail = take(4 * uint64_t(p.tail_rows) * uint64_t(tile_n));
         p.ld = round_up(c.H, 4);
-        const int64_t n_blocks = (c.H + 255) / 256;
-        p.data_splits = pick_splits(m_blocks * n_blocks, (piece + BK - 1) / BK, kSms / p.ctas);
-        p.data_rows = m_blocks * tile_m;
-        if (c.dx && (p.data_splits > 1 || p.pieces > 1))
-            p.data = take(4 * uint64_t(p.data_splits) * uint64_t(p.data_rows) * uint64_t(p.ld));
-        const int64_t w_blocks = (piece + 255) / 256;
-        p.weight_splits = pick_splits(w_blocks * n_blocks, (c.N + BK - 1) / BK, kSms / 2);
-        p.weight_rows = w_blocks * 256;
-        if (c.dw && p.weight_splits > 1)
-            p.weight = take(4 * uint64_t(p.weight_splits) * uint64_t(p.weight_rows) * uint64_t(p.ld));
+        if (c.dx && p.pieces > 1) p.sums = take(4 * N * uint64_t(p.ld));
     }
     p.bytes = at;
     return p;
@@ -1393,6 +1483,7 @@ struct Run {
 
     int *count() const { return reinterpret_cast<int *>(ws + plan.rows); }
     float *scale() const { return reinterpret_cast<float *>(ws + plan.rows + 8); }
+    Cut *cuts() const { return reinterpret_cast<Cut *>(ws + plan.rows + 16); }
     int *rows() const { return reinterpret_cast<int *>(ws + plan.rows + 64); }
     template <class P>
     P *at(uint64_t offset) const { return reinterpret_cast<P *>(ws + offset); }
@@ -1448,6 +1539,15 @@ struct Run {
             l.dloss = c.dloss;
             l.scale = scale();
             l.f16 = !bf16;
+            const int64_t n_blocks = (c.H + 2 * grad_bn(c.H) - 1) / (2 * grad_bn(c.H));
+            l.cut = cuts();
+            l.data_blocks = int(n_blocks);
+            l.data_tile_m = BM * plan.ctas;
+            l.data_k_tiles = int((plan.piece + BK - 1) / BK);
+            l.data_slots = kSms / plan.ctas;
+            l.weight_tiles = int((plan.piece + 255) / 256 * n_blocks);
+            l.last_tiles = int((c.V - (plan.pieces - 1) * plan.piece + 255) / 256 * n_blocks);
+            l.weight_slots = kSms / 2;
         } else {
             l.loss = c.loss;
             l.lse = c.lse;
@@ -1463,29 +1563,33 @@ struct Run {
         return make_map(m, type16, base, r, cols, stride_bytes, box_cols, box_rows, sw);
     }
 
-    // One product.  `tiles_rows` sizes the grid for all rows.
-    int product(const Variant &v, CUtensorMap &a, CUtensorMap &b, CUtensorMap &listed, CUtensorMap &out, Params &p,
-                int64_t all_rows, int64_t row_bytes, glu_launch_info_t *info) const
+    // A forward pass over one block of rows lists nothing: rows without a token cost it nothing.
+    bool lists() const { return c.backward || plan.ctas == 2; }
+
+    // One product, its grid sized for all rows.
+    int product(const Variant &v, CUtensorMap &a, CUtensorMap &b, CUtensorMap &listed, CUtensorMap &out,
+                CUtensorMap &tail, Params &p, int64_t all_rows, int64_t row_bytes, glu_launch_info_t *info) const
     {
         int n_slots = 0;
         if (int st = slots_of(v, bf16, dev, sms, &n_slots)) return st;
         const int64_t tile_m = int64_t(BM) * v.ctas;
         const int64_t m_blocks = (all_rows + tile_m - 1) / tile_m;
-        p.count = count();
+        p.count = lists() ? count() : nullptr;
         p.rows = rows();
         p.N = int(c.N);
         p.n_blocks = int((p.cols + 2 * v.bn - 1) / (2 * v.bn));
-        if (p.splits < 1) p.splits = 1;
         // row blocks per group: their rows of A (about 48 MiB) stay in L2 while B
         // streams past once; where one block row is more than that, tiles that run
         // side by side form a square
         int64_t group = (int64_t(48) << 20) / (tile_m * row_bytes);
         if (group < 8) group = 8;
         p.group_m = int(group > m_blocks ? m_blocks : group);
-        const int64_t tiles = m_blocks * p.n_blocks * p.splits;
-        if (tiles * v.ctas > INT32_MAX) return GLU_ERR_SHAPE;
-        const int64_t clusters = tiles < n_slots ? tiles : n_slots;
-        void *args[] = {&a, &b, &listed, &out, &p};
+        const int64_t tiles = m_blocks * p.n_blocks;
+        if (tiles + kTailRounds * kSms > INT32_MAX / 2) return GLU_ERR_SHAPE;
+        // the gradients' tiles may be cut into up to kMaxParts parts
+        const int64_t items = v.id < 12 ? tiles : tiles * kMaxParts;
+        const int64_t clusters = items < n_slots ? items : n_slots;
+        void *args[] = {&a, &b, &listed, &out, &tail, &p};
         if (int st = launch(reinterpret_cast<const void *>(v.fn), unsigned(clusters * v.ctas), kThreads,
                             size_t(v.smem), unsigned(v.ctas), args, s))
             return st;
@@ -1519,7 +1623,7 @@ struct Run {
         // one block holding every row copies only the rows that exist (rounded up to a
         // swizzle atom): the MMA's other rows are never stored
         const int box_a = ctas == 1 ? int(round_up(c.N, 8)) : BM, box_b = ctas == 1 ? 2 * bn : bn;
-        CUtensorMap ta, tl, tb, to;
+        CUtensorMap ta, tl, tb;
         const char *w = static_cast<const char *>(c.w) + first * c.w_stride * 2;
         if (!map16(&ta, c.x, c.N, c.H, c.x_stride * 2, BK, box_a, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !map16(&tl, at<char>(plan.listed), c.N, c.H, plan.listed_stride, BK, box_a, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -1533,22 +1637,20 @@ struct Run {
         p.first = first;
         p.c1 = c1();
         if (grad) {
-            if (!map16(&to, at<char>(plan.g), c.N, round_up(cols, 8), plan.g_stride, kBox, kBox,
-                       CU_TENSOR_MAP_SWIZZLE_64B))
-                return glu::cuda_fail(cudaErrorInvalidValue);
+            p.out = at<char>(plan.g);
+            p.out_stride = plan.g_stride;
             p.lse = c.lse;
             p.loss = c.loss;
             p.dloss = c.dloss;
             p.inv_t = inv_t();
             p.scale = scale();
         } else {
-            to = ta;
             p.part = at<float2>(plan.part);
             p.named = at<float>(plan.named);
             p.index = c.distill ? at<int>(plan.sorted) : nullptr;
             p.top = int(c.top);
         }
-        return product(v, ta, tb, tl, to, p, c.N, c.H * 2, info);
+        return product(v, ta, tb, tl, ta, ta, p, c.N, c.H * 2, info);
     }
 
     int named(int64_t first, int64_t cols) const
@@ -1578,58 +1680,61 @@ struct Run {
         return launch(fn, unsigned(c.N), 128, 0, 1, args, s);
     }
 
-    // Where a gradient product's result goes: a 16-bit matrix or fp32 partial results.
-    int output(Params &p, CUtensorMap *to, const CUtensorMap &unused, void *out, int64_t out_stride, int64_t r,
-               bool partial, uint64_t buffer, int64_t split_rows, bool add) const
+    // Where a gradient product's result goes: a 16-bit matrix, or fp32 sums over the pieces; and the
+    // parts of the tiles that are cut.
+    int output(Params &p, CUtensorMap *to, CUtensorMap *tail, const CUtensorMap &unused, void *out, int64_t out_stride,
+               int64_t r, int bn, int sums) const
     {
-        if (partial) {
-            p.partial = add ? 2 : 1;
-            p.split_rows = int(split_rows);
-            if (!make_map(to, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, at<char>(buffer), split_rows * p.splits, plan.ld,
-                          plan.ld * 4, kBox, kBox, CU_TENSOR_MAP_SWIZZLE_128B))
+        const auto f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+        *to = *tail = unused;
+        if (plan.tail_rows > 0 && !make_map(tail, f32, at<char>(plan.tail), plan.tail_rows, 2 * bn, 8 * bn, 32, 32,
+                                            CU_TENSOR_MAP_SWIZZLE_128B))
+            return glu::cuda_fail(cudaErrorInvalidValue);
+        p.sums = sums;
+        if (sums) {
+            if (!make_map(to, f32, at<char>(plan.sums), r, plan.ld, plan.ld * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
                 return glu::cuda_fail(cudaErrorInvalidValue);
             return GLU_OK;
         }
         p.out = static_cast<char *>(out);
         p.out_stride = out_stride * 2;
-        p.vec_store = uintptr_t(out) % 16 == 0 && out_stride % 8 == 0;
-        // the copy engine clips a box at the last column in 16-byte units
-        p.tma_store = p.vec_store && c.H % 8 == 0 &&
-                      map16(to, out, r, c.H, out_stride * 2, kBox, kBox, CU_TENSOR_MAP_SWIZZLE_64B);
-        if (!p.tma_store) *to = unused;
+        p.vec_store = uintptr_t(out) % 32 == 0 && out_stride % 16 == 0  ? 32
+                      : uintptr_t(out) % 16 == 0 && out_stride % 8 == 0 ? 16
+                                                                        : 0;
         return GLU_OK;
     }
 
     // dx (+)= g w over the piece.
     int data(int64_t first, int64_t cols, bool add, glu_launch_info_t *info) const
     {
-        const int ctas = plan.ctas;
-        const int bn = c.H <= 128 ? 64 : 128;
+        const int ctas = plan.ctas, bn = grad_bn(c.H);
         const Variant v = ctas == 1 ? (bn == 64 ? variant<kData, 64, 1>(bf16, 12) : variant<kData, 128, 1>(bf16, 13))
                                     : (bn == 64 ? variant<kData, 64, 2>(bf16, 14) : variant<kData, 128, 2>(bf16, 15));
         const int box_a = ctas == 1 ? int(round_up(c.N, 8)) : BM;
-        CUtensorMap ta, tb, to;
+        CUtensorMap ta, tb, to, tt;
         const char *w = static_cast<const char *>(c.w) + first * c.w_stride * 2;
         if (!map16(&ta, at<char>(plan.g), c.N, cols, plan.g_stride, BK, box_a, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !map16(&tb, w, cols, c.H, c.w_stride * 2, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B))
             return glu::cuda_fail(cudaErrorInvalidValue);
         Params p{};
         p.cols = int(c.H);
-        p.depth = int(cols);
-        p.splits = plan.data_splits;
+        // every piece is cut alike, so that their sums meet: a last, shorter one reads zeros past its end
+        p.depth = int(plan.piece);
         p.a_bytes = uint32_t(box_a) * BK * 2;
         p.scale = scale();
-        if (int st = output(p, &to, ta, c.dx, c.dx_stride, c.N, plan.data_splits > 1 || plan.pieces > 1, plan.data,
-                            plan.data_rows, add))
-            return st;
-        return product(v, ta, tb, ta, to, p, c.N, plan.g_stride, info);
+        p.cut = cuts();
+        if (int st = output(p, &to, &tt, ta, c.dx, c.dx_stride, c.N, bn, plan.pieces == 1 ? 0 : add ? 2 : 1)) return st;
+        if (int st = product(v, ta, tb, ta, to, tt, p, c.N, plan.g_stride, info)) return st;
+        if (first + cols < c.V) return GLU_OK;
+        return sum(p, v, false, c.dx, c.dx_stride);
     }
 
     // dw = g^T x for the piece.
     int weight(int64_t first, int64_t cols, glu_launch_info_t *info) const
     {
-        const Variant v = c.H <= 128 ? variant<kWeight, 64, 2>(bf16, 16) : variant<kWeight, 128, 2>(bf16, 17);
-        CUtensorMap ta, tb, tl, to;
+        const int bn = grad_bn(c.H);
+        const Variant v = bn == 64 ? variant<kWeight, 64, 2>(bf16, 16) : variant<kWeight, 128, 2>(bf16, 17);
+        CUtensorMap ta, tb, tl, to, tt;
         if (!map16(&ta, at<char>(plan.g), c.N, cols, plan.g_stride, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !map16(&tb, c.x, c.N, c.H, c.x_stride * 2, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !map16(&tl, at<char>(plan.listed), c.N, c.H, plan.listed_stride, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -1637,36 +1742,48 @@ struct Run {
         Params p{};
         p.cols = int(c.H);
         p.m_rows = int(cols);
-        p.splits = plan.weight_splits;
-        p.a_bytes = uint32_t(Shape<kWeight, 128, 2>::kTileA);
+        p.a_bytes = uint32_t(BM * BK * 2);
         p.scale = scale();
+        p.cut = cuts() + (first + cols < c.V ? 1 : 2);
         char *out = static_cast<char *>(c.dw) + first * c.dw_stride * 2;
-        if (int st = output(p, &to, ta, out, c.dw_stride, cols, plan.weight_splits > 1, plan.weight, plan.weight_rows,
-                            false))
-            return st;
-        if (int st = product(v, ta, tb, tl, to, p, cols, c.N * 2, info)) return st;
-        if (plan.weight_splits == 1) return GLU_OK;
-        return sum(plan.weight, plan.weight_rows, plan.weight_splits, false, cols, out, c.dw_stride);
+        if (int st = output(p, &to, &tt, ta, out, c.dw_stride, cols, bn, 0)) return st;
+        if (int st = product(v, ta, tb, tl, to, tt, p, cols, c.N * 2, info)) return st;
+        return sum(p, v, true, out, c.dw_stride);
     }
 
-    int sum(uint64_t buffer, int64_t split_rows, int splits, bool listed, int64_t m_rows, void *out,
-            int64_t out_stride) const
+    // What the product `p` left as sums, where it can have left any.
+    int sum(const Params &p, const Variant &v, bool weight, void *out, int64_t out_stride) const
     {
+        const int tile_m = BM * v.ctas;
+        const int64_t m_blocks = ((weight ? int64_t(p.m_rows) : c.N) + tile_m - 1) / tile_m;
+        const int64_t tiles = m_blocks * p.n_blocks;
+        // A cut saves less than a round: none from 26 rounds on.  How many rows take
+        // part, which counts the tiles of dx and the slices of dw, only the GPU knows.
+        const int64_t k_tiles = ((weight ? c.N : int64_t(p.depth)) + BK - 1) / BK;
+        const int slots = kSms / v.ctas;
+        const bool cut = k_tiles >= 8 && (!weight || (tiles % slots != 0 && tiles < 26 * slots));
+        if (!p.sums && !cut) return GLU_OK;
         SumParams q{};
-        q.part = at<float>(buffer);
+        q.tail = at<float>(plan.tail);
+        q.sums = p.sums ? at<float>(plan.sums) : nullptr;
         q.ld = plan.ld;
-        q.split_rows = int(split_rows);
-        q.splits = splits;
         q.count = count();
-        q.rows = listed ? rows() : nullptr;
+        q.rows = rows();
+        q.weight = weight;
         q.N = int(c.N);
-        q.cols = int(c.H);
-        q.m_rows = int(m_rows);
+        q.cols = p.cols;
+        q.m_rows = p.m_rows;
+        q.n_blocks = p.n_blocks;
+        q.group_m = p.group_m;
+        q.cut = p.cut;
+        q.tile_m = tile_m;
+        q.tile_n = 2 * v.bn;
         q.scale = scale();
         q.out = static_cast<char *>(out);
         q.out_stride = out_stride * 2;
         void *args[] = {&q};
-        const int64_t blocks = (m_rows * ((c.H + 3) / 4) + 255) / 256;
+        const int64_t most = p.sums ? tiles : (tiles < 2 * slots ? tiles : 2 * slots);
+        const int64_t blocks = most * tile_m * v.bn / 2 / 256;
         const void *fn = bf16 ? reinterpret_cast<const void *>(&sum_kernel<__nv_bfloat16>)
                               : reinterpret_cast<const void *>(&sum_kernel<__half>);
         return launch(fn, unsigned(blocks < 16 * sms ? blocks : 16 * sms), 256, 0, 1, args, s);
@@ -1676,14 +1793,17 @@ struct Run {
     {
         if (c.distill)
             if (int st = teacher()) return st;
-        if (int st = list()) return st;
+        if (lists())
+            if (int st = list()) return st;
         if (int st = logits(false, 0, c.V, info)) return st;
         JoinParams j{};
         j.part = at<float2>(plan.part);
         j.n_parts = 2 * int((c.V + 2 * plan.bn - 1) / (2 * plan.bn));
         j.N = int(c.N);
-        j.count = count();
+        j.count = lists() ? count() : nullptr;
         j.rows = rows();
+        j.target = c.distill ? nullptr : c.target;
+        j.V = c.V;
         j.named = at<float>(plan.named);
         j.c1 = c1();
         j.loss = c.loss;
@@ -1716,8 +1836,6 @@ struct Run {
             if (c.dx)
                 if (int st = data(first, cols, i > 0, info)) return st;
         }
-        if (c.dx && (plan.data_splits > 1 || plan.pieces > 1))
-            return sum(plan.data, plan.data_rows, plan.data_splits, true, c.N, c.dx, c.dx_stride);
         return GLU_OK;
     }
 };

@@ -140,4 +140,4 @@ def test_python_refusals():
     with pytest.raises(ValueError):
         glu._gradient(torch.zeros(4, 8), x, "dx")
     with pytest.raises(ValueError):
-        glu._loss_workspace(torch.zeros(4), 4, x)
+        glu._loss_workspace(torch.zeros(4), x, 4, 8, 9, 0, 0)
