@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import torch
 from torch import nn
+from torch.autograd.function import once_differentiable
 
 from . import add_rmsnorm as _add_rmsnorm
 from . import add_rmsnorm_bwd as _add_rmsnorm_bwd
@@ -19,6 +20,11 @@ from . import add_rmsnorm_q as _add_rmsnorm_q
 from . import bwd as _bwd
 from . import fwd as _fwd
 from . import gemm_fwd as _gemm_fwd
+from . import gemm_nt as _gemm_nt
+from . import linear_ce as _linear_ce
+from . import linear_ce_bwd as _linear_ce_bwd
+from . import linear_distill as _linear_distill
+from . import linear_distill_bwd as _linear_distill_bwd
 from . import mlp_q_fwd as _mlp_q_fwd
 from . import quantize as _quantize
 
@@ -292,3 +298,115 @@ class FusedAddRMSNorm(nn.Module):
 
     def extra_repr(self):
         return f"{self.weight.shape[0]}, eps={self.eps}"
+
+
+def _wanted(ctx, i):
+    """None (allocate the gradient) where input i wants one, else False (leave it out)."""
+    return None if ctx.needs_input_grad[i] else False
+
+
+class LinearCrossEntropyFunction(torch.autograd.Function):
+    """loss (float32, one a row) of the rows x under the output projection: softmax
+    cross entropy over the vocabulary without keeping the logits.  The forward saves
+    its inputs and two floats a row; the backward forms the logits again."""
+
+    @staticmethod
+    def forward(ctx, x, weight, target):
+        loss, lse = _linear_ce(x, weight, target)
+        ctx.save_for_backward(x, weight, target, loss, lse)
+        return loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss):
+        x, weight, target, loss, lse = ctx.saved_tensors
+        dx, dw = _linear_ce_bwd(dloss.contiguous(), x, weight, target, loss, lse, dx=_wanted(ctx, 0),
+                                dw=_wanted(ctx, 1))
+        return dx, dw, None
+
+
+class LinearDistillationFunction(torch.autograd.Function):
+    """loss (float32, one a row): the divergence of the rows' softmax over the
+    vocabulary from a teacher's over its top tokens, without keeping the logits.
+    The teacher gets no gradient."""
+
+    @staticmethod
+    def forward(ctx, x, weight, index, logit, temperature: float = 1.0):
+        loss, lse, top_logits = _linear_distill(x, weight, index, logit, temperature)
+        ctx.save_for_backward(x, weight, index, logit, lse, top_logits)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss):
+        x, weight, index, logit, lse, top_logits = ctx.saved_tensors
+        dx, dw = _linear_distill_bwd(dloss.contiguous(), x, weight, index, logit, lse, top_logits, ctx.temperature,
+                                     dx=_wanted(ctx, 0), dw=_wanted(ctx, 1))
+        return dx, dw, None, None, None
+
+
+REDUCTIONS = ("mean", "sum", "none")
+
+
+def _reduced(loss, takes_part, reduction):
+    if reduction == "none":
+        return loss
+    if reduction == "sum":
+        return loss.sum()
+    if reduction == "mean":         # over the rows that take part; 0 where none does
+        return loss.sum() / takes_part.sum().clamp_min(1)
+    raise ValueError(f"unknown reduction {reduction!r}; expected one of {REDUCTIONS}")
+
+
+def linear_cross_entropy(x, weight, target, reduction: str = "mean"):
+    """Cross entropy of x (..., H) under the output projection weight (V, H) against
+    target (...): rows whose target is outside 0 .. V - 1 take no part."""
+    loss = LinearCrossEntropyFunction.apply(x, weight, target)
+    return _reduced(loss, (target >= 0) & (target < weight.shape[0]), reduction)
+
+
+def linear_distillation(x, weight, index, logit, temperature: float = 1.0, reduction: str = "mean"):
+    """Distillation of x (..., H) under weight (V, H) from a teacher's top logits:
+    logit (..., K) of the tokens index (..., K).  Entries outside 0 .. V - 1 or of
+    logit -inf are none; rows without entries take no part.  No factor
+    temperature^2 is applied."""
+    loss = LinearDistillationFunction.apply(x, weight, index, logit, temperature)
+    has = (index >= 0) & (index < weight.shape[0]) & (logit != -float("inf"))
+    return _reduced(loss, has.any(-1), reduction)
+
+
+class VocabLoss(nn.Module):
+    """A model's output projection with the losses over its vocabulary: the logits
+    of a batch, the largest matrix of a training step, are never stored.
+    forward(x, target) is the cross entropy, distill(x, index, logit) the
+    distillation loss, logits(x) the plain projection (for generation, one row a
+    sequence).  ``from_linear`` shares an existing projection's weight."""
+
+    def __init__(self, hidden: int, vocab: int, device=None, dtype=None):
+        super().__init__()
+        if hidden % 8:
+            raise ValueError("hidden must be a multiple of 8 (rows on 16-byte boundaries)")
+        self.weight = nn.Parameter(torch.empty(vocab, hidden, device=device, dtype=dtype))
+        nn.init.normal_(self.weight, std=hidden ** -0.5)
+
+    @classmethod
+    def from_linear(cls, linear: nn.Linear):
+        if linear.bias is not None:
+            raise ValueError("the projection must have no bias")
+        self = cls(linear.in_features, 0, linear.weight.device, linear.weight.dtype)
+        self.weight = linear.weight
+        return self
+
+    def forward(self, x, target, reduction: str = "mean"):
+        return linear_cross_entropy(x, self.weight, target, reduction)
+
+    def distill(self, x, index, logit, temperature: float = 1.0, reduction: str = "mean"):
+        return linear_distillation(x, self.weight, index, logit, temperature, reduction)
+
+    @torch.no_grad()
+    def logits(self, x):
+        return _gemm_nt(x, self.weight)
+
+    def extra_repr(self):
+        return f"{self.weight.shape[1]}, vocab={self.weight.shape[0]}"

@@ -19,12 +19,15 @@
 // One kernel template runs the four products (stats, grad, data, weight) on the
 // structure of glu_gemm.cu: a persistent grid; warp 0 fills a ring of 64-deep K
 // slices with the tensor-memory accelerator (128-byte swizzle), one thread of
-// warp 1 issues tcgen05.mma, two warpgroups
-// add the segments of K into registers, from the other of two accumulators.  The
-// operands lie as the user has them: g w wants w's vocabulary as its K, g^T x
-// wants rows as K, so those operands come as MN-major tiles (64 columns x 64 K
-// to a swizzled box), which the MMA reads directly; nothing is transposed in
-// memory.
+// warp 1 issues tcgen05.mma into one of two accumulators, and two warpgroups add
+// the other one, a segment of K, to the sums in their registers.  The operands lie
+// as the user has them: g w wants w's vocabulary as its K, g^T x wants rows as K,
+// so those come as MN-major tiles (64 columns x 64 K to a swizzled box), which the
+// MMA reads directly.  Only x is transposed in memory, where dw is large.
+//
+// Bound: the tensor cores (large calls run at the power limit, 1.6 - 1.75 PFLOP/s,
+// where the library's plain bf16 product settles at 1.7), w's bytes (few rows, 5.3
+// - 5.8 TB/s) or launches (a small forward call is two of 5 us).
 //
 // Rows without a target take no part in any product: a first kernel lists the
 // rows that have one and, only where some have none, copies them side by side.
@@ -70,12 +73,15 @@ enum Mode {
     kStats,     // z = x w^T -> per tile and row: maximum, sum of exponentials, named logits
     kGrad,      // z = x w^T -> g
     kData,      // g w     (K = the piece's vocabulary)
-    kWeight     // g^T x   (K = rows)
+    kWeight,    // g^T x   (K = rows)
+    kWeightT    // the same with x transposed before (K-major)
 };
+__host__ __device__ constexpr bool is_weight(int mode) { return mode == kWeight || mode == kWeightT; }
+__host__ __device__ constexpr bool is_gradient(int mode) { return mode == kData || is_weight(mode); }
 
 template <int MODE, int BN, int CTAS>
 struct Shape {
-    static constexpr bool kTransA = MODE == kWeight;
+    static constexpr bool kTransA = is_weight(MODE);
     static constexpr bool kTransB = MODE == kData || MODE == kWeight;
     static constexpr int kTileN = 2 * BN;                               // columns of a tile
     static constexpr int kBRows = CTAS == 1 ? 2 * BN : BN;              // of them, loaded by one block
@@ -84,14 +90,14 @@ struct Shape {
     static constexpr int kStageBytes = kTileA + kTileB;
     static constexpr int kStages = kRingBytes / kStageBytes > 8 ? 8 : kRingBytes / kStageBytes;
     static constexpr int kTileM = BM * CTAS;
-    static constexpr int kTmemCols = 2 * kTileN <= 256 ? 256 : 512;     // two accumulators
+    static constexpr int kTmemCols = 2 * kTileN <= 256 ? 256 : 512;     // two accumulators, a power of two
     static constexpr int kBars = 2 * kStages + 2 + 2 + 1;               // full, empty, acc_full, acc_empty, done
-    static constexpr int kStageOut = MODE == kData || MODE == kWeight ? kEpiWarps * kBoxBytes : 0;
+    static constexpr int kStageOut = is_gradient(MODE) ? kEpiWarps * kBoxBytes : 0;
     static constexpr int kCols = kTileN / 2;                            // columns of one epilogue thread
     // K slices summed in tensor memory before their sum goes to registers
     static constexpr int kSegment = MODE == kStats || MODE == kGrad ? 16 : 64;
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStageOut + kBars * 8 + 16;
-    static_assert(BN % 32 == 0 && kTileN <= 256, "one MMA covers the tile's columns");
+    static_assert(BN % 32 == 0 && BN >= 32 && kTileN <= 256, "one MMA covers the tile's columns");
     static_assert(!kTransB || kBRows % 64 == 0, "MN-major operands come in chunks of 64 columns");
     static_assert(kTileA % 1024 == 0 && kTileB % 1024 == 0, "swizzle atoms stay 1024-byte aligned");
     static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
@@ -176,8 +182,9 @@ __device__ __forceinline__ float exp2_fast(float v)
 }
 
 // 32 values of 16 bits to 64 bytes of a row, 32-byte aligned.  A thread writes its
-// own row: whole 32-byte sectors, no staging and no fence before a copy engine
-// (64 rows of x, 32768 x 4096 of dw: XXX us through staged boxes, YYY like this).
+// own row: whole 32-byte sectors, no staging and no fence before a copy engine (64
+// rows of x, 32768 x 4096 of dw: 75 us through staged boxes, 73 like this; 55 once
+// accumulators are handed back without a release to the cluster, arrive_remote).
 __device__ __forceinline__ void store_row(char *dst, const uint32_t (&w)[16])
 {
 #pragma unroll
@@ -315,11 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // block of rows (or one slice of K): it reads zeros and gives zeros.
     const int count = p.count ? *reinterpret_cast<const volatile int *>(p.count) : p.N;
     const bool all = count == p.N;
-    const int m_rows = MODE == kWeight ? p.m_rows : count;
+    const int m_rows = is_weight(MODE) ? p.m_rows : count;
     const int m_blocks = max(1, (m_rows + S::kTileM - 1) / S::kTileM);
-    const int k_tiles = max(1, ((MODE == kWeight ? count : p.depth) + BK - 1) / BK);
+    const int k_tiles = max(1, ((is_weight(MODE) ? count : p.depth) + BK - 1) / BK);
     const int n_tiles = m_blocks * p.n_blocks;
-    const Cut cut = MODE == kData || MODE == kWeight ? *p.cut : Cut{n_tiles, 1};
+    const Cut cut = is_gradient(MODE) ? *p.cut : Cut{n_tiles, 1};
     const int tail = n_tiles - cut.whole, per_part = (k_tiles + cut.parts - 1) / cut.parts;
     const int n_items = cut.whole + tail * cut.parts;
     const auto item_of = [&](int t) {
@@ -448,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool boxed = false;             // a box of this warp is with the copy engine
         float unscale = 1.0f, gscale = 1.0f;
         if constexpr (MODE == kGrad) gscale = p.scale[0] * p.inv_t;
-        if constexpr (MODE == kData || MODE == kWeight) unscale = p.scale[1];
+        if constexpr (is_gradient(MODE)) unscale = p.scale[1];
         int use = 0;
         bool ok = true;
         for (int t = cluster; t < n_items; t += n_clusters) {
@@ -568,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p.part[int64_t(2 * o.tile.nb + (col0 != 0)) * p.N + m] = make_float2(top, (s[0] + s[1]) + (s[2] + s[3]));
             } else {
                 const int m_box = m - lane;
-                const bool floats = (MODE == kData || MODE == kWeight) && (o.part >= 0 || p.sums);
+                const bool floats = is_gradient(MODE) && (o.part >= 0 || p.sums);
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
                     const uint32_t (&g)[32] = sums[c];
@@ -712,13 +719,20 @@ __device__ __forceinline__ bool takes_part(const ListParams &p, int i)
 }
 
 // Copies or clears a row of 16-bit values by one warp; 16 bytes at a time where
-// both sides allow.
+// both sides allow, four in flight.
 __device__ __forceinline__ void warp_row(char *dst, const char *src, int H, int lane)
 {
     const bool vec = (uintptr_t(dst) % 16) == 0 && (!src || uintptr_t(src) % 16 == 0);
     const int n = vec ? H / 8 : 0;
-    for (int i = lane; i < n; i += 32)
-        reinterpret_cast<uint4 *>(dst)[i] = src ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < n; i += 128) {
+        uint4 v[4] = {};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (src && i + 32 * j < n) v[j] = reinterpret_cast<const uint4 *>(src)[i + 32 * j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + 32 * j < n) reinterpret_cast<uint4 *>(dst)[i + 32 * j] = v[j];
+    }
     for (int i = n * 8 + lane; i < H; i += 32)
         reinterpret_cast<uint16_t *>(dst)[i] = src ? reinterpret_cast<const uint16_t *>(src)[i] : uint16_t(0);
 }
@@ -811,6 +825,55 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const ListParams p)
     const int end = min(p.N, max(BK, (total + BK - 1) / BK * BK));
     for (int i = total + blockIdx.x * (kListThreads / 32) + warp; i < end; i += gridDim.x * (kListThreads / 32))
         warp_row(p.listed + int64_t(i) * p.listed_stride, nullptr, p.H, lane);
+}
+
+struct TransposeParams {
+    const char *x, *listed;
+    int64_t x_stride, listed_stride;    // bytes
+    const int *count;
+    int N, H;
+    char *out;
+    int64_t out_stride;                 // bytes
+};
+
+constexpr int kTransTile = 64;
+
+// x of the rows that take part, transposed: H rows of them, zeros up to a whole
+// slice of K behind the last.  Tiles of 64 x 64 through shared memory, two rows
+// of x to a 32-bit word of the result.
+__global__ void __launch_bounds__(256) transpose_kernel(const TransposeParams p)
+{
+    __shared__ uint32_t s_tile[kTransTile][kTransTile / 2 + 1];     // [column][pair of rows]
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int count = *p.count, n0 = blockIdx.x * kTransTile;
+    if (n0 >= max(1, count)) return;
+    const char *src = count == p.N ? p.x : p.listed;
+    const int64_t stride = count == p.N ? p.x_stride : p.listed_stride;
+    const int pair = threadIdx.x >> 3, h = (threadIdx.x & 7) * 8;   // 32 pairs of rows, 8 columns each
+    const int lane = threadIdx.x & 31;
+    for (int h0 = blockIdx.y * kTransTile; h0 < p.H; h0 += gridDim.y * kTransTile) {
+        uint16_t v[2][8];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int n = n0 + 2 * pair + r;
+            const uint16_t *row = reinterpret_cast<const uint16_t *>(src + int64_t(n) * stride) + h0 + h;
+            if (n < count && h0 + h + 8 <= p.H) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(row);
+                memcpy(v[r], &w, 16);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[r][j] = n < count && h0 + h + j < p.H ? row[j] : uint16_t(0);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s_tile[h + j][pair] = uint32_t(v[0][j]) | uint32_t(v[1][j]) << 16;
+        __syncthreads();
+        // rows of the result have room for whole slices of 64
+        for (int c = threadIdx.x >> 5; c < kTransTile && h0 + c < p.H; c += 8)
+            reinterpret_cast<uint32_t *>(p.out + int64_t(h0 + c) * p.out_stride + int64_t(n0) * 2)[lane] = s_tile[c][lane];
+    }
 }
 
 constexpr int kJoinRows = 32;
@@ -1155,15 +1218,16 @@ using GemmFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUte
 struct Variant {
     GemmFn fn;
     int smem, bn, ctas, id;
+    bool gradient;
 };
 
-constexpr int kVariants = 18;
+constexpr int kVariants = 22;
 
 template <int MODE, int BN, int CTAS>
 Variant variant(bool bf16, int id)
 {
     return {bf16 ? loss_gemm_kernel<MODE, __nv_bfloat16, BN, CTAS> : loss_gemm_kernel<MODE, __half, BN, CTAS>,
-            Shape<MODE, BN, CTAS>::kSmemBytes, BN, CTAS, id};
+            Shape<MODE, BN, CTAS>::kSmemBytes, BN, CTAS, id, is_gradient(MODE)};
 }
 
 // Blocks (or pairs) of a variant that fit on the device at once, and the
@@ -1215,7 +1279,7 @@ int slots_of(const Variant &v, bool bf16, int dev, int sms, int *out)
 
 // A launch that may overlap the tail of the one before it in the stream (every
 // kernel here waits for that grid before it touches memory).
-int launch(const void *fn, unsigned grid, unsigned threads, size_t smem, unsigned cluster, void **args, cudaStream_t s)
+int launch(const void *fn, dim3 grid, unsigned threads, size_t smem, unsigned cluster, void **args, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[2];
@@ -1225,7 +1289,7 @@ int launch(const void *fn, unsigned grid, unsigned threads, size_t smem, unsigne
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -1291,17 +1355,19 @@ struct Plan {
     int ctas, bn;               // of the logits' product: blocks a tile, half its columns
     int64_t tail_rows;          // rows of the parts of tiles that are kept apart
     int64_t ld;                 // of the sums over pieces, in floats
-    int64_t g_stride, listed_stride;            // bytes
-    uint64_t rows, listed, part, named, sorted, order, entries, share, entropy, g, tail, sums, bytes;
+    bool transpose;             // x transposed for dw
+    int64_t g_stride, listed_stride, xt_stride;     // bytes
+    uint64_t rows, listed, part, named, sorted, order, entries, share, entropy, g, xt, tail, sums, bytes;
 };
 
 // Column-tile width of the logits' product: the fewest rows of x and w moved,
 // counted in rounds of tiles over the GPU (the widest on a tie).
-int pick_bn(int64_t m_blocks, int64_t V, int64_t slots, int64_t a_rows)
+int pick_bn(int64_t m_blocks, int64_t V, int64_t slots, int64_t a_rows, bool one_block)
 {
     int best = 128;
     int64_t best_cost = -1;
-    for (int bn : {128, 96, 64}) {
+    for (int bn : {128, 96, 64, 32}) {
+        if (bn == 32 && !one_block) break;
         const int64_t tiles = m_blocks * ((V + 2 * bn - 1) / (2 * bn));
         const int64_t cost = (tiles + slots - 1) / slots * (a_rows + 2 * bn);
         if (best_cost < 0 || cost < best_cost) {
@@ -1311,6 +1377,14 @@ int pick_bn(int64_t m_blocks, int64_t V, int64_t slots, int64_t a_rows)
     }
     return best;
 }
+
+// dw's product reads g as an MN-major operand, and x too unless it is transposed
+// first.  With x K-major the tensor cores wait less for shared memory (busy 72 % of
+// the cycles with both operands MN-major, 81 % with one); transposing moves x
+// twice.  Measured, g and dw together: 4096 x 4096 rows, 131072 tokens 5828 -> 5630
+// us, 2048 x 2048, 65536 766 -> 753; 1024 x 4096, 32768 384.9 -> 384.5, 777 x 1030,
+// 30001 129 -> 131, 300 x 1024, 16384 36.5 -> 38.
+bool transposes(int64_t N, int64_t V) { return N >= 2048 && V >= 32768; }
 
 // Half the columns of a gradient product's tile.
 int grad_bn(int64_t H) { return H <= 128 ? 64 : 128; }
@@ -1338,7 +1412,8 @@ Plan make_plan(const Call &c, int64_t piece)
     // sized for the whole GPU whatever the device, so that the bytes asked for hold
     p.ctas = c.N > BM ? 2 : 1;
     const int64_t tile_m = BM * p.ctas, m_blocks = (c.N + tile_m - 1) / tile_m;
-    p.bn = pick_bn(m_blocks, c.backward ? piece : c.V, kSms / p.ctas, p.ctas == 1 ? round_up(c.N, 8) : tile_m);
+    p.bn = pick_bn(m_blocks, c.backward ? piece : c.V, kSms / p.ctas, p.ctas == 1 ? round_up(c.N, 8) : tile_m,
+                   p.ctas == 1);
     if (!c.backward) {
         // two halves of a tile, each joined by itself
         p.part = take(16 * N * uint64_t((c.V + 2 * p.bn - 1) / (2 * p.bn)));
@@ -1348,6 +1423,9 @@ Plan make_plan(const Call &c, int64_t piece)
         p.pieces = int((c.V + piece - 1) / piece);
         p.g_stride = round_up(piece, 64) * 2;
         p.g = take(N * uint64_t(p.g_stride));
+        p.transpose = c.dw && transposes(c.N, c.V);
+        p.xt_stride = round_up(c.N, 64) * 2;
+        if (p.transpose) p.xt = take(uint64_t(c.H) * uint64_t(p.xt_stride));
         // The parts of the tiles that are cut: of both gradients, one after the other
         // on the stream, whatever number of rows takes part.
         const int64_t tile_n = grad_bn(c.H) * 2, n_blocks = (c.H + tile_n - 1) / tile_n;
@@ -1587,7 +1665,7 @@ struct Run {
         const int64_t tiles = m_blocks * p.n_blocks;
         if (tiles + kTailRounds * kSms > INT32_MAX / 2) return GLU_ERR_SHAPE;
         // the gradients' tiles may be cut into up to kMaxParts parts
-        const int64_t items = v.id < 12 ? tiles : tiles * kMaxParts;
+        const int64_t items = v.gradient ? tiles * kMaxParts : tiles;
         const int64_t clusters = items < n_slots ? items : n_slots;
         void *args[] = {&a, &b, &listed, &out, &tail, &p};
         if (int st = launch(reinterpret_cast<const void *>(v.fn), unsigned(clusters * v.ctas), kThreads,
@@ -1607,14 +1685,16 @@ struct Run {
         const int ctas = plan.ctas, bn = plan.bn;
         Variant v{};
         if (!grad)
-            v = ctas == 1 ? (bn == 64   ? variant<kStats, 64, 1>(bf16, 0)
+            v = ctas == 1 ? (bn == 32   ? variant<kStats, 32, 1>(bf16, 18)
+                             : bn == 64 ? variant<kStats, 64, 1>(bf16, 0)
                              : bn == 96 ? variant<kStats, 96, 1>(bf16, 1)
                                         : variant<kStats, 128, 1>(bf16, 2))
                           : (bn == 64   ? variant<kStats, 64, 2>(bf16, 3)
                              : bn == 96 ? variant<kStats, 96, 2>(bf16, 4)
                                         : variant<kStats, 128, 2>(bf16, 5));
         else
-            v = ctas == 1 ? (bn == 64   ? variant<kGrad, 64, 1>(bf16, 6)
+            v = ctas == 1 ? (bn == 32   ? variant<kGrad, 32, 1>(bf16, 19)
+                             : bn == 64 ? variant<kGrad, 64, 1>(bf16, 6)
                              : bn == 96 ? variant<kGrad, 96, 1>(bf16, 7)
                                         : variant<kGrad, 128, 1>(bf16, 8))
                           : (bn == 64   ? variant<kGrad, 64, 2>(bf16, 9)
@@ -1704,6 +1784,25 @@ struct Run {
         return GLU_OK;
     }
 
+    // x transposed, of the rows that take part.
+    int transpose() const
+    {
+        TransposeParams t{};
+        t.x = static_cast<const char *>(c.x);
+        t.listed = at<char>(plan.listed);
+        t.x_stride = c.x_stride * 2;
+        t.listed_stride = plan.listed_stride;
+        t.count = count();
+        t.N = int(c.N);
+        t.H = int(c.H);
+        t.out = at<char>(plan.xt);
+        t.out_stride = plan.xt_stride;
+        void *args[] = {&t};
+        const int64_t h_tiles = (c.H + kTransTile - 1) / kTransTile;
+        const dim3 grid(unsigned((c.N + kTransTile - 1) / kTransTile), unsigned(h_tiles < 65535 ? h_tiles : 65535));
+        return launch(reinterpret_cast<const void *>(&transpose_kernel), grid, 256, 0, 1, args, s);
+    }
+
     // dx (+)= g w over the piece.
     int data(int64_t first, int64_t cols, bool add, glu_launch_info_t *info) const
     {
@@ -1733,10 +1832,15 @@ struct Run {
     int weight(int64_t first, int64_t cols, glu_launch_info_t *info) const
     {
         const int bn = grad_bn(c.H);
-        const Variant v = bn == 64 ? variant<kWeight, 64, 2>(bf16, 16) : variant<kWeight, 128, 2>(bf16, 17);
+        const Variant v = plan.transpose
+                              ? (bn == 64 ? variant<kWeightT, 64, 2>(bf16, 20) : variant<kWeightT, 128, 2>(bf16, 21))
+                              : (bn == 64 ? variant<kWeight, 64, 2>(bf16, 16) : variant<kWeight, 128, 2>(bf16, 17));
         CUtensorMap ta, tb, tl, to, tt;
         if (!map16(&ta, at<char>(plan.g), c.N, cols, plan.g_stride, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !map16(&tb, c.x, c.N, c.H, c.x_stride * 2, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !(plan.transpose
+                  ? map16(&tb, at<char>(plan.xt), c.H, round_up(c.N, 64), plan.xt_stride, BK, bn,
+                          CU_TENSOR_MAP_SWIZZLE_128B)
+                  : map16(&tb, c.x, c.N, c.H, c.x_stride * 2, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B)) ||
             !map16(&tl, at<char>(plan.listed), c.N, c.H, plan.listed_stride, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B))
             return glu::cuda_fail(cudaErrorInvalidValue);
         Params p{};
@@ -1826,6 +1930,8 @@ struct Run {
         if (c.distill)
             if (int st = teacher()) return st;
         if (int st = list()) return st;
+        if (plan.transpose)
+            if (int st = transpose()) return st;
         for (int i = 0; i < plan.pieces; ++i) {
             const int64_t first = i * plan.piece, cols = c.V - first < plan.piece ? c.V - first : plan.piece;
             if (int st = logits(true, first, cols, info)) return st;
