@@ -115,6 +115,7 @@ struct Params {
     const int *count;           // rows that take part; rows[] lists them
     const int *rows;
     int N;                      // rows of x
+    int copied;                 // the listed rows are copied even if they are all
     int cols;                   // columns of the output: the piece's vocabulary (stats, grad), H (data, weight)
     int depth;                  // K: H (stats, grad), the piece's vocabulary (data); weight: the count
     int m_rows;                 // rows of the output for weight: the piece's vocabulary
@@ -164,6 +165,13 @@ __device__ __forceinline__ void tma_add(const CUtensorMap *map, uint32_t src, in
                  "r"(x), "r"(y), "r"(src)
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
 }
 
 // An arrival on the other block's barrier that hands back tensor memory.  What it
@@ -309,6 +317,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<CTAS>(saddr(const_cast<uint32_t *>(tmem_slot)), S::kTmemCols);
+    // few rows: the first tile's rows of w are asked of L2 before the wait for the
+    // kernel before (which may still write them: L2 then holds what it wrote)
+    if constexpr (CTAS == 1 && (MODE == kStats || MODE == kGrad)) {
+        if (warp == 0 && lane == 0 && cluster < p.n_blocks)
+            for (int kt = 0; kt < min(ST, (p.depth + BK - 1) / BK); ++kt)
+                tma_prefetch(&tm_b, kt * BK, cluster * S::kTileN);
+    }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     if constexpr (CTAS == 2)
         cluster_sync();
@@ -321,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // What depends on how many rows take part.  With none there is still one
     // block of rows (or one slice of K): it reads zeros and gives zeros.
     const int count = p.count ? *reinterpret_cast<const volatile int *>(p.count) : p.N;
-    const bool all = count == p.N;
+    const bool all = count == p.N, listed = !all || p.copied;
     const int m_rows = is_weight(MODE) ? p.m_rows : count;
     const int m_blocks = max(1, (m_rows + S::kTileM - 1) / S::kTileM);
     const int k_tiles = max(1, ((is_weight(MODE) ? count : p.depth) + BK - 1) / BK);
@@ -343,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
         if (warp == 0) {
             if (lane == 0) {
-                const CUtensorMap *ma = (MODE == kStats || MODE == kGrad) && !all ? &tm_listed : &tm_a;
-                const CUtensorMap *mbp = MODE == kWeight && !all ? &tm_listed : &tm_b;
+                const CUtensorMap *ma = (MODE == kStats || MODE == kGrad) && listed ? &tm_listed : &tm_a;
+                const CUtensorMap *mbp = MODE == kWeight && listed ? &tm_listed : &tm_b;
                 const uint32_t bytes = p.a_bytes + uint32_t(S::kTileB);
                 uint32_t it = 0;
                 for (int t = cluster; t < n_items && !*abort_flag; t += n_clusters) {
@@ -707,6 +722,7 @@ struct ListParams {
     const float *dloss;         // backward
     float *scale;               // backward: what g is scaled by (and its inverse)
     int f16;
+    int copy;                   // copy the rows even if all take part
     float inv_t;
     Cut *cut;                   // backward: of dx's product, dw's, and dw's for the last piece
     int data_blocks, data_tile_m, data_k_tiles, data_slots;
@@ -809,7 +825,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const ListParams p)
             p.cut[2] = last;
         }
     }
-    if (total == p.N) return;
+    if (total == p.N && !p.copy) return;
     __syncthreads();
     for (int i = first + warp; i < last; i += kListThreads / 32) {
         const int at = s_pos[i - first];
@@ -876,7 +892,6 @@ __global__ void __launch_bounds__(256) transpose_kernel(const TransposeParams p)
     }
 }
 
-constexpr int kJoinRows = 32;
 constexpr int kJoinThreads = 1024;
 
 struct JoinParams {
@@ -898,30 +913,33 @@ struct JoinParams {
 // The tiles' maxima and sums of one row joined, and the loss formed from them:
 // with s = sum_v 2^(c1 z_v - m) it is ln 2 (log2 s - (c1 z - m)), which keeps its
 // bits where the target's logit is the largest by far.
+template <int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p)
 {
-    __shared__ float2 s_part[kJoinThreads / 32][kJoinRows];
+    constexpr int kSlices = kJoinThreads / ROWS;        // of a row's parts, one a thread
+    __shared__ float2 s_part[kSlices][ROWS];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int count = p.count ? *p.count : p.N;
-    const int m0 = blockIdx.x * kJoinRows, m = m0 + lane;
+    const int m0 = blockIdx.x * ROWS, m = m0 + threadIdx.x % ROWS;
     if (m0 >= count) return;
-    float top = -INFINITY, sum = 0.0f;
-    if (m < count) {
-        for (int b = warp; b < p.n_parts; b += kJoinThreads / 32) {
-            const float2 v = p.part[int64_t(b) * p.N + m];
-            const float hi = fmaxf(top, v.x), base = hi == -INFINITY ? 0.0f : hi;
-            sum = sum * exp2f(top - base) + v.y * exp2f(v.x - base);
-            top = hi;
-        }
-    }
-    s_part[warp][lane] = make_float2(top, sum);
+    const auto join = [](float2 a, float2 b) {
+        const float hi = fmaxf(a.x, b.x), base = hi == -INFINITY ? 0.0f : hi;
+        return make_float2(hi, a.y * exp2f(a.x - base) + b.y * exp2f(b.x - base));
+    };
+    float2 mine = make_float2(-INFINITY, 0.0f);
+    if (m < count)
+#pragma unroll 4
+        for (int b = threadIdx.x / ROWS; b < p.n_parts; b += kSlices) mine = join(mine, p.part[int64_t(b) * p.N + m]);
+    s_part[threadIdx.x / ROWS][threadIdx.x % ROWS] = mine;
     __syncthreads();
     // warp w joins row w
     const int r = warp;
-    if (m0 + r >= count) return;
-    const float2 v = s_part[lane][r];
+    if (r >= ROWS || m0 + r >= count) return;
+    float2 v = s_part[lane][r];
+#pragma unroll
+    for (int i = 32; i < kSlices; i += 32) v = join(v, s_part[lane + i][r]);
     float hi = v.x;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, d));
@@ -1356,6 +1374,7 @@ struct Plan {
     int64_t tail_rows;          // rows of the parts of tiles that are kept apart
     int64_t ld;                 // of the sums over pieces, in floats
     bool transpose;             // x transposed for dw
+    bool copy;                  // x's rows copied whether or not all take part
     int64_t g_stride, listed_stride, xt_stride;     // bytes
     uint64_t rows, listed, part, named, sorted, order, entries, share, entropy, g, xt, tail, sums, bytes;
 };
@@ -1399,7 +1418,12 @@ Plan make_plan(const Call &c, int64_t piece)
         return here;
     };
     const uint64_t N = uint64_t(c.N), top = uint64_t(c.top);
-    p.listed_stride = round_up(c.H, 8) * 2;
+    // where x's rows are off 32 bytes the copy engine reads a sector more for every
+    // 128 bytes: such x is copied as if rows were missing (rows of 2064 bytes, 777 x
+    // 1030, 30001 tokens: backward 190 -> 185 us; of 4000 bytes, 333 x 1999, 50001,
+    // it would take 290 for 286)
+    p.copy = c.N > BM && c.x_stride % 16 != 0;
+    p.listed_stride = round_up(c.H, 64) * 2;
     p.rows = take(4 * N + 64);          // the count, the scale and its inverse, the cuts, then the list (from byte 64)
     p.listed = take(N * uint64_t(p.listed_stride));
     if (c.distill) {
@@ -1611,6 +1635,7 @@ struct Run {
         l.rows = rows();
         l.count = count();
         l.inv_t = inv_t();
+        l.copy = plan.copy;
         if (c.backward) {
             l.dx = static_cast<char *>(c.dx);
             l.dx_stride = c.dx_stride * 2;
@@ -1655,6 +1680,7 @@ struct Run {
         p.count = lists() ? count() : nullptr;
         p.rows = rows();
         p.N = int(c.N);
+        p.copied = plan.copy && lists();
         p.n_blocks = int((p.cols + 2 * v.bn - 1) / (2 * v.bn));
         // row blocks per group: their rows of A (about 48 MiB) stay in L2 while B
         // streams past once; where one block row is more than that, tiles that run
@@ -1921,8 +1947,12 @@ struct Run {
             j.top_logits = c.top_logits;
         }
         void *args[] = {&j};
-        return launch(reinterpret_cast<const void *>(&join_kernel), unsigned((c.N + kJoinRows - 1) / kJoinRows),
-                      kJoinThreads, 0, 1, args, s);
+        // 32 rows a block read whole lines; 8 rows while that is what it takes to fill the GPU
+        // (forward of 64 x 4096, 32768 tokens: 51.2 -> 49.1 us, with w's prefetch)
+        const bool wide = c.N > 8 * kSms * 2;
+        return launch(wide ? reinterpret_cast<const void *>(&join_kernel<32>)
+                           : reinterpret_cast<const void *>(&join_kernel<8>),
+                      unsigned((c.N + (wide ? 31 : 7)) / (wide ? 32 : 8)), kJoinThreads, 0, 1, args, s);
     }
 
     int backward(glu_launch_info_t *info) const
