@@ -771,14 +771,22 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const ListParams p)
     __syncthreads();
     int before = 0, total = 0;
     float amax = 0.0f;
-    for (int i = tid; i < p.N; i += kListThreads) {
-        const bool a = takes_part(p, i);
-        total += a;
-        before += a && i < first;
-        // a gradient that is not finite takes no part in the scale
-        if (p.f16 && a) {
-            const float d = fabsf(p.dloss[i] * p.inv_t);
-            if (d < INFINITY) amax = fmaxf(amax, d);
+    for (int i0 = tid; i0 < p.N; i0 += 8 * kListThreads) {       // eight loads in flight
+        bool a[8];
+        float d[8] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kListThreads;
+            a[j] = i < p.N && takes_part(p, i);
+            if (p.f16 && i < p.N) d[j] = p.dloss[i];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            total += a[j];
+            before += a[j] && i0 + j * kListThreads < first;
+            // a gradient that is not finite takes no part in the scale
+            const float v = fabsf(d[j] * p.inv_t);
+            if (a[j] && v < INFINITY) amax = fmaxf(amax, v);
         }
     }
     before = __reduce_add_sync(0xFFFFFFFFu, before);
