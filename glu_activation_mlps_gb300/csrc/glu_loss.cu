@@ -203,6 +203,11 @@ __device__ __forceinline__ void store_row(char *dst, const uint32_t (&w)[16])
     }
 }
 
+__device__ __forceinline__ f2 pair(const uint32_t (&g)[32], int j)
+{
+    return make_float2(__uint_as_float(g[j]), __uint_as_float(g[j + 1]));
+}
+
 // Element j of a row's 32 registers, j known at run time only.
 __device__ __forceinline__ float pick(const uint32_t (&g)[32], int j)
 {
@@ -542,8 +547,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld32(acc + uint32_t(32 * c), g);
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            sums[c][j] = __float_as_uint(__uint_as_float(sums[c][j]) + __uint_as_float(g[j]));
+                        for (int j = 0; j < 32; j += 2) {
+                            const f2 v = add2(pair(sums[c], j), pair(g, j));
+                            sums[c][j] = __float_as_uint(v.x);
+                            sums[c][j + 1] = __float_as_uint(v.y);
+                        }
                     }
                 }
                 // all of it read: hand the accumulator back
@@ -559,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if constexpr (MODE == kStats) {
                 const int width = p.cols - n0;              // columns that exist
-                float top = -INFINITY;
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
                     uint32_t (&g)[32] = sums[c];
@@ -575,19 +583,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < 32; ++j) g[j] = 32 * c + j < width ? g[j] : 0xFF800000u;    // -inf
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(g[j]));
+                    for (int j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(g[j]));
                 }
                 // maximum and sum of exponentials, in units of log2
-                top *= p.c1;
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c1;
                 const float base = top == -INFINITY ? 0.0f : top;
-                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const f2 c1 = splat(p.c1), shift2 = splat(-base);
+                f2 s[2] = {splat(0.0f), splat(0.0f)};
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        s[j & 3] += exp2_fast(fmaf(__uint_as_float(sums[c][j]), p.c1, -base));
+                    for (int j = 0; j < 32; j += 2) {
+                        const f2 v = fma2(pair(sums[c], j), c1, shift2);
+                        s[j / 2 & 1] = add2(s[j / 2 & 1], make_float2(exp2_fast(v.x), exp2_fast(v.y)));
+                    }
+                s[0] = add2(s[0], s[1]);
                 if (live)
-                    p.part[int64_t(2 * o.tile.nb + (col0 != 0)) * p.N + m] = make_float2(top, (s[0] + s[1]) + (s[2] + s[3]));
+                    p.part[int64_t(2 * o.tile.nb + (col0 != 0)) * p.N + m] = make_float2(top, s[0].x + s[0].y);
             } else {
                 const int m_box = m - lane;
                 const bool floats = is_gradient(MODE) && (o.part >= 0 || p.sums);
@@ -622,22 +634,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         float f[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float z = __uint_as_float(g[j + i]);
-                            if constexpr (MODE == kGrad) {
-                                const float v = coef * exp2_fast(fmaf(z, p.c1, shift));
-                                f[i] = coef == 0.0f || j + i >= left ? 0.0f : v;
-                                if (tgt == 32 * c + j + i) f[i] = at_target;
-                            } else {
-                                f[i] = z * unscale;
-                            }
+                        if constexpr (MODE == kGrad) {
+                            const f2 v = fma2(pair(g, j), splat(p.c1), splat(shift));
+                            const f2 e = mul2(splat(coef), make_float2(exp2_fast(v.x), exp2_fast(v.y)));
+                            f[0] = e.x;
+                            f[1] = e.y;
+                        } else {
+                            const f2 v = mul2(pair(g, j), splat(unscale));
+                            f[0] = v.x;
+                            f[1] = v.y;
                         }
                         packed[j / 2] = Cd::put(f);
                     }
                     char *dst = p.out + int64_t(row) * p.out_stride + int64_t(n0 + 32 * c) * 2;
                     if constexpr (MODE == kGrad) {
-                        // whole chunks: a row of g has room for them; rows past the listed ones are 0
+                        if (tgt >= 32 * c && tgt < 32 * c + 32) {
+                            const int at = int(tgt) - 32 * c;
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                const float f[2] = {at == j ? at_target : Cd::get(packed[j / 2], 0),
+                                                    at == j + 1 ? at_target : Cd::get(packed[j / 2], 1)};
+                                packed[j / 2] = Cd::put(f);
+                            }
+                        }
+                        // 0 past the piece, and in rows without a gradient, whatever their logits are
+                        const uint32_t mask = coef == 0.0f ? 0u : 0xFFFFFFFFu;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2)
+                            packed[j / 2] &= left >= 32 ? mask : j >= left ? 0u : j + 1 >= left ? mask & 0xFFFFu : mask;
+                        // whole chunks: a row of g has room for them
                         if (m < p.N) {
                             dst = p.out + int64_t(m) * p.out_stride + int64_t(n0 + 32 * c) * 2;
                             store_row(dst, packed);
