@@ -243,7 +243,9 @@ __device__ __forceinline__ Cut cut_of(int tiles, int k_tiles, int slots, int lan
     const uint32_t none = uint32_t((tiles + slots - 1) / slots) * uint32_t(k_tiles + 8);
     uint32_t cost = UINT32_MAX;
     int whole = tiles;
-    if (rem != 0 && lane >= 2 && lane <= kMaxParts && k_tiles >= 4 * lane && tiles < 26 * slots) {
+    // no part without a slice: so many parts that the last would start behind K are left out
+    const bool full = lane >= 2 && (lane - 1) * ((k_tiles + lane - 1) / lane) < k_tiles;
+    if (rem != 0 && full && lane <= kMaxParts && k_tiles >= 4 * lane && tiles < 26 * slots) {
         for (int tail = rem; tail <= tiles && tail <= rem + slots && tail * lane <= kTailRounds * slots; tail += slots) {
             const uint32_t v = uint32_t((tiles - tail) / slots) * uint32_t(k_tiles + 8) +
                                uint32_t((tail * lane + slots - 1) / slots) * uint32_t((k_tiles + lane - 1) / lane + 8);
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if constexpr (MODE == kStats) {
                 const int width = p.cols - n0;              // columns that exist
-                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float top = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
                     uint32_t (&g)[32] = sums[c];
@@ -583,10 +585,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < 32; ++j) g[j] = 32 * c + j < width ? g[j] : 0xFF800000u;    // -inf
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(g[j]));
+                    for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(g[j]));
                 }
                 // maximum and sum of exponentials, in units of log2
-                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c1;
+                top *= p.c1;
                 const float base = top == -INFINITY ? 0.0f : top;
                 const f2 c1 = splat(p.c1), shift2 = splat(-base);
                 f2 s[2] = {splat(0.0f), splat(0.0f)};

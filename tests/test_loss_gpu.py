@@ -26,7 +26,11 @@ pytestmark = pytest.mark.gpu
 
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
 SIZES = [(1, 1, 1), (1, 8, 1), (3, 9, 2), (1, 64, 1000), (7, 40, 130), (128, 64, 256), (129, 100, 257), (300, 72, 1000),
-         (64, 512, 5000), (257, 1030, 3001), (1000, 130, 129), (5, 2048, 20000), (520, 256, 40), (2000, 192, 700)]
+         (64, 512, 5000), (257, 1030, 3001), (1000, 130, 129), (5, 2048, 20000), (520, 256, 40), (2000, 192, 700),
+         # K of dx and dw in parts of uneven numbers of slices
+         (128, 256, 4160), (129, 520, 8200), (4160, 64, 300), (600, 1100, 9000),
+         # x transposed before dw
+         (2048, 136, 32768)]
 
 
 def matrix(rows, cols, dtype, g, scale=1.0, pad=True, grid=False):
@@ -137,7 +141,8 @@ def test_ce(N, H, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("N,H,V", [(1, 64, 300), (100, 64, 1000), (300, 72, 1000), (700, 136, 515), (2000, 64, 200)])
+@pytest.mark.parametrize("N,H,V", [(1, 64, 300), (100, 64, 1000), (300, 72, 1000), (700, 136, 515), (2000, 64, 200),
+                                   (2500, 72, 33000), (70000, 64, 300)])
 @pytest.mark.parametrize("masked", ["some", "all", "last"])
 def test_ce_rows_without_target(N, H, V, masked, dtype):
     g = gen(N + V)
@@ -244,6 +249,66 @@ def test_distill(N, H, V, K, kind, T, dtype):
     close(dx, ref["dx"], ref["dx_tol"], "dx")
     close(dw, ref["dw"], ref["dw_tol"], "dw")
     assert glu.glu_wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("T", [2.0 ** -6, 100.0])
+def test_distill_far_temperatures(T):
+    N, H, V, K = 40, 64, 500, 9
+    g = gen(17)
+    x, w = matrix(N, H, torch.bfloat16, g, grid=True), matrix(V, H, torch.bfloat16, g, grid=True)
+    index, logit = teacher(N, V, K, g, torch.float32, "plain")
+    dloss = torch.rand(N, generator=g, device="cuda")
+    has, valid, shares, ent = shares_of(index, logit, V, T)
+    ref = reference(x, w, shares, valid, ent, T, dloss, exact=True)
+    loss, lse, top = glu.linear_distill(x, w, index, logit, T)
+    # logits over T of some hundreds: c1 z is one rounding of that size (in ref's bound), p's of d / T another
+    slack = 2.0 ** -23 * (ref["z"].abs().amax(1) + 32.0) / T
+    close(loss, ref["loss"], ref["tol"] + slack, "loss")
+    close(lse, ref["lse"], ref["tol"] + slack, "lse")
+    dx, dw = glu.linear_distill_bwd(dloss, x, w, index, logit, lse, top, T)
+    more = 2 * slack.max() * dloss.max().double() / T * 2
+    close(dx, ref["dx"], ref["dx_tol"] + more * w.double().abs().sum(0).max(), "dx")
+    close(dw, ref["dw"], ref["dw_tol"] + more * x.double().abs().sum(0).max(), "dw")
+
+
+def test_two_calls_at_once():
+    """Two streams, each call with its own workspace and its own results."""
+    N, H, V = 700, 512, 9000
+    g = gen(31)
+    w = matrix(V, H, torch.bfloat16, g, 0.1)
+    xs = [matrix(N, H, torch.bfloat16, g) for _ in range(2)]
+    ts = [targets(N, V, g, "some") for _ in range(2)]
+    d = torch.rand(N, generator=g, device="cuda")
+
+    def step(x, t):
+        loss, lse = glu.linear_ce(x, w, t)
+        return (loss, lse, *glu.linear_ce_bwd(d, x, w, t, loss, lse))
+
+    want = [step(x, t) for x, t in zip(xs, ts)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = step(xs[i], ts[i])
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)
+    assert glu.glu_wait_timeouts() == 0
+
+
+def test_rows_of_a_wider_matrix():
+    """x and w as columns of wider matrices, dx and dw into columns of others."""
+    N, H, V = 260, 80, 600
+    g = gen(41)
+    x = torch.randn(N, 3 * H, generator=g, device="cuda").half()[:, H:2 * H]
+    w = (torch.randn(V, 2 * H, generator=g, device="cuda") * 0.2).half()[:, H:]
+    t = targets(N, V, g, "some")
+    dx = torch.zeros(N, 2 * H, device="cuda").half()[:, :H]
+    dw = torch.zeros(V, 3 * H, device="cuda").half()[:, H:2 * H]
+    check_ce(x, w, t, torch.rand(N, generator=g, device="cuda"), dx=dx, dw=dw)
 
 
 def test_distill_strided_entries_and_pieces():
