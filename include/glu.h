@@ -101,7 +101,8 @@ typedef enum {
     GLU_ERR_ALIAS = -4,   /* outputs overlap inputs other than exactly, or each other */
     GLU_ERR_ENUM = -5,    /* unknown act, layout or dtype */
     GLU_ERR_CUDA = -6,    /* the CUDA runtime refused a launch or copy; see glu_last_cuda_error() */
-    GLU_ERR_WORKSPACE = -7, /* host-memory entry points, glu_mlp_fwd: workspace NULL or too small for one row */
+    GLU_ERR_WORKSPACE = -7, /* host-memory entry points, glu_mlp_fwd: workspace NULL or too small for one row;
+                               glu_linear_*: too small */
     GLU_ERR_VALUE = -8      /* an argument out of range: glu_add_rmsnorm_fwd's eps, or an
                                operand of a tensor-core entry point or glu_add_rmsnorm_bwd's
                                dgamma that is not in device memory */
@@ -304,7 +305,7 @@ int glu_set_tuning(const glu_tuning_t *t);   /* GLU_ERR_ENUM for unsupported val
 int glu_get_tuning(glu_tuning_t *out);
 
 /* Kernels that wait on the bulk-copy engine or the tensor cores (the bulk-copy
- * path, glu_gemm_fwd and glu_add_rmsnorm_bwd's staged kernel) bound every wait
+ * path, glu_gemm_fwd, glu_gemm_q_*, glu_linear_* and glu_add_rmsnorm_bwd's staged kernel) bound every wait
  * (about a second) and count the waits that ran out on the current device
  * instead of hanging.
  * Copies that count into *count (synchronising with the device) and, if
