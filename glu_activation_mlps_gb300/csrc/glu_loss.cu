@@ -1405,12 +1405,12 @@ struct Plan {
     int64_t piece;              // backward: tokens of a piece
     int pieces;
     int ctas, bn;               // of the logits' product: blocks a tile, half its columns
-    int64_t tail_rows;          // rows of the parts of tiles that are kept apart
+    int64_t tail_rows[2];       // rows of the parts of tiles that are kept apart: of dx, of dw
     int64_t ld;                 // of the sums over pieces, in floats
     bool transpose;             // x transposed for dw
     bool copy;                  // x's rows copied whether or not all take part
     int64_t g_stride, listed_stride, xt_stride;     // bytes
-    uint64_t rows, listed, part, named, sorted, order, entries, share, entropy, g, xt, tail, sums, bytes;
+    uint64_t rows, listed, part, named, sorted, order, entries, share, entropy, g, xt, tail[2], sums, bytes;
 };
 
 // Column-tile width of the logits' product: the fewest rows of x and w moved,
@@ -1484,18 +1484,16 @@ Plan make_plan(const Call &c, int64_t piece)
         p.transpose = c.dw && transposes(c.N, c.V);
         p.xt_stride = round_up(c.N, 64) * 2;
         if (p.transpose) p.xt = take(uint64_t(c.H) * uint64_t(p.xt_stride));
-        // The parts of the tiles that are cut: of both gradients, one after the other
-        // on the stream, whatever number of rows takes part.
+        // The parts of the tiles that are cut, whatever number of rows takes part.  Those of
+        // dx add up over the pieces, with dw's in between: each has its own.
         const int64_t tile_n = grad_bn(c.H) * 2, n_blocks = (c.H + tile_n - 1) / tile_n;
         const auto room = [&](int64_t tiles, int64_t k_tiles, int64_t slots) {
             const int64_t most = tiles * kMaxParts < kTailRounds * slots ? tiles * kMaxParts : kTailRounds * slots;
             return k_tiles < 8 ? int64_t(0) : most;
         };
-        const int64_t data = c.dx ? room(m_blocks * n_blocks, (piece + BK - 1) / BK, kSms / p.ctas) * tile_m : 0;
-        const int64_t weight =
-            c.dw ? room((piece + 255) / 256 * n_blocks, (c.N + BK - 1) / BK, kSms / 2) * 256 : 0;
-        p.tail_rows = data > weight ? data : weight;
-        p.tail = take(4 * uint64_t(p.tail_rows) * uint64_t(tile_n));
+        p.tail_rows[0] = c.dx ? room(m_blocks * n_blocks, (piece + BK - 1) / BK, kSms / p.ctas) * tile_m : 0;
+        p.tail_rows[1] = c.dw ? room((piece + 255) / 256 * n_blocks, (c.N + BK - 1) / BK, kSms / 2) * 256 : 0;
+        for (int i = 0; i < 2; ++i) p.tail[i] = take(4 * uint64_t(p.tail_rows[i]) * uint64_t(tile_n));
         p.ld = round_up(c.H, 4);
         if (c.dx && p.pieces > 1) p.sums = take(4 * N * uint64_t(p.ld));
     }
@@ -1827,12 +1825,12 @@ struct Run {
     // Where a gradient product's result goes: a 16-bit matrix, or fp32 sums over the pieces; and the
     // parts of the tiles that are cut.
     int output(Params &p, CUtensorMap *to, CUtensorMap *tail, const CUtensorMap &unused, void *out, int64_t out_stride,
-               int64_t r, int bn, int sums) const
+               int64_t r, int bn, int sums, int which) const
     {
         const auto f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
         *to = *tail = unused;
-        if (plan.tail_rows > 0 && !make_map(tail, f32, at<char>(plan.tail), plan.tail_rows, 2 * bn, 8 * bn, 32, 32,
-                                            CU_TENSOR_MAP_SWIZZLE_128B))
+        if (plan.tail_rows[which] > 0 && !make_map(tail, f32, at<char>(plan.tail[which]), plan.tail_rows[which], 2 * bn,
+                                                   8 * bn, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
             return glu::cuda_fail(cudaErrorInvalidValue);
         p.sums = sums;
         if (sums) {
@@ -1886,7 +1884,8 @@ struct Run {
         p.a_bytes = uint32_t(box_a) * BK * 2;
         p.scale = scale();
         p.cut = cuts();
-        if (int st = output(p, &to, &tt, ta, c.dx, c.dx_stride, c.N, bn, plan.pieces == 1 ? 0 : add ? 2 : 1)) return st;
+        if (int st = output(p, &to, &tt, ta, c.dx, c.dx_stride, c.N, bn, plan.pieces == 1 ? 0 : add ? 2 : 1, 0))
+            return st;
         if (int st = product(v, ta, tb, ta, to, tt, p, c.N, plan.g_stride, info)) return st;
         if (first + cols < c.V) return GLU_OK;
         return sum(p, v, false, c.dx, c.dx_stride);
@@ -1914,7 +1913,7 @@ struct Run {
         p.scale = scale();
         p.cut = cuts() + (first + cols < c.V ? 1 : 2);
         char *out = static_cast<char *>(c.dw) + first * c.dw_stride * 2;
-        if (int st = output(p, &to, &tt, ta, out, c.dw_stride, cols, bn, 0)) return st;
+        if (int st = output(p, &to, &tt, ta, out, c.dw_stride, cols, bn, 0, 1)) return st;
         if (int st = product(v, ta, tb, tl, to, tt, p, cols, c.N * 2, info)) return st;
         return sum(p, v, true, out, c.dw_stride);
     }
@@ -1932,7 +1931,7 @@ struct Run {
         const bool cut = k_tiles >= 8 && (!weight || (tiles % slots != 0 && tiles < 26 * slots));
         if (!p.sums && !cut) return GLU_OK;
         SumParams q{};
-        q.tail = at<float>(plan.tail);
+        q.tail = at<float>(plan.tail[weight]);
         q.sums = p.sums ? at<float>(plan.sums) : nullptr;
         q.ld = plan.ld;
         q.count = count();
