@@ -64,7 +64,7 @@ constexpr int kEpiWarps = 8;            // 32 rows each, in two halves of the co
 constexpr int kRegsLaunch = 168, kRegsFew = 72, kRegsMany = 216;
 static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads * kRegsLaunch, "the split fits the launch");
 constexpr int kRingBytes = 192 * 1024;
-constexpr int kBoxBytes = 4096;         // fp32 sums leave through boxes of 32 rows x 32 columns
+constexpr int kBoxBytes = 4096;         // results leave through boxes of 32 rows x 128 bytes, one a warp
 constexpr int kChunkBytes = 64 * BK * 2;    // an MN-major box: 64 columns x 64 K
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -139,6 +139,7 @@ struct Params {
     char *out;
     int64_t out_stride;         // bytes
     int vec_store;              // rows are 32- or 16-byte aligned; 0: at any place
+    int tma_store;              // results may leave through boxes
     int sums;                   // fp32 sums of this piece instead of results: 1 stored, 2 added to the last piece's
 };
 
@@ -189,10 +190,7 @@ __device__ __forceinline__ float exp2_fast(float v)
     return r;
 }
 
-// 32 values of 16 bits to 64 bytes of a row, 32-byte aligned.  A thread writes its
-// own row: whole 32-byte sectors, no staging and no fence before a copy engine (64
-// rows of x, 32768 x 4096 of dw: 75 us through staged boxes, 73 like this; 55 once
-// accumulators are handed back without a release to the cluster, arrive_remote).
+// 32 values of 16 bits to 64 bytes of a row, 32-byte aligned.
 __device__ __forceinline__ void store_row(char *dst, const uint32_t (&w)[16])
 {
 #pragma unroll
@@ -605,34 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 const int m_box = m - lane;
                 const bool floats = is_gradient(MODE) && (o.part >= 0 || p.sums);
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
+                // 32 columns of a row, rounded
+                const auto round16 = [&](int c, uint32_t (&packed)[16]) {
                     const uint32_t (&g)[32] = sums[c];
-                    const int left = p.cols - (n0 + 32 * c);    // columns that exist
-                    if (left <= 0) continue;
-                    if (floats) {
-                        // fp32 sums: rows of 128 bytes, 16-byte chunk v at v ^ (lane % 8)
-                        if (lane == 0 && boxed) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        boxed = true;
-                        __syncwarp();
-                        const uint32_t at = boxes + uint32_t(lane) * 128u, sw = uint32_t(lane) & 7u;
-#pragma unroll
-                        for (uint32_t v = 0; v < 8; ++v)
-                            st_shared16(at + ((v ^ sw) << 4), g[4 * v], g[4 * v + 1], g[4 * v + 2], g[4 * v + 3]);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) {
-                            const CUtensorMap *map = o.part < 0 ? &tm_out : &tm_tail;
-                            const int x = o.part < 0 ? n0 + 32 * c : col0 + 32 * c;
-                            const int y = o.part < 0 ? m_box : o.part * S::kTileM + (m_box - o.tile.mb * S::kTileM);
-                            if (p.sums == 2)
-                                tma_add(map, boxes, x, y);
-                            else
-                                tma_store(map, boxes, x, y);
-                        }
-                        continue;
-                    }
-                    uint32_t packed[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         float f[2];
@@ -648,7 +621,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         packed[j / 2] = Cd::put(f);
                     }
-                    char *dst = p.out + int64_t(row) * p.out_stride + int64_t(n0 + 32 * c) * 2;
                     if constexpr (MODE == kGrad) {
                         if (tgt >= 32 * c && tgt < 32 * c + 32) {
                             const int at = int(tgt) - 32 * c;
@@ -660,15 +632,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         // 0 past the piece, and in rows without a gradient, whatever their logits are
+                        const int left = p.cols - (n0 + 32 * c);
                         const uint32_t mask = coef == 0.0f ? 0u : 0xFFFFFFFFu;
 #pragma unroll
                         for (int j = 0; j < 32; j += 2)
                             packed[j / 2] &= left >= 32 ? mask : j >= left ? 0u : j + 1 >= left ? mask & 0xFFFFu : mask;
-                        // whole chunks: a row of g has room for them
-                        if (m < p.N) {
-                            dst = p.out + int64_t(m) * p.out_stride + int64_t(n0 + 32 * c) * 2;
-                            store_row(dst, packed);
+                    }
+                };
+                // A box: row `lane` is 128 bytes, its 16-byte chunk v at v ^ (lane % 8).  The
+                // copy engine has read what was there before; then it gets this one.
+                const auto box_free = [&]() {
+                    if (lane == 0 && boxed) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    boxed = true;
+                    __syncwarp();
+                };
+                const auto to_box = [&](uint32_t v, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+                    st_shared16(boxes + uint32_t(lane) * 128u + ((v ^ (uint32_t(lane) & 7u)) << 4), w0, w1, w2, w3);
+                };
+                const auto box_full = [&]() {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                };
+                if (floats) {               // fp32 sums, 32 columns to a box
+                    const CUtensorMap *map = o.part < 0 ? &tm_out : &tm_tail;
+                    const int y = o.part < 0 ? m_box : o.part * S::kTileM + (m_box - o.tile.mb * S::kTileM);
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        const uint32_t (&g)[32] = sums[c];
+                        if (n0 + 32 * c >= p.cols) continue;
+                        box_free();
+#pragma unroll
+                        for (uint32_t v = 0; v < 8; ++v) to_box(v, g[4 * v], g[4 * v + 1], g[4 * v + 2], g[4 * v + 3]);
+                        box_full();
+                        if (lane == 0) {
+                            const int x = o.part < 0 ? n0 + 32 * c : col0 + 32 * c;
+                            if (p.sums == 2)
+                                tma_add(map, boxes, x, y);
+                            else
+                                tma_store(map, boxes, x, y);
                         }
+                    }
+                    continue;
+                }
+                // 16 bits, 64 columns to a box: whole lines, and the fence a box costs is cheaper
+                // than the lines that a warp's own stores to 32 rows touch (g and dw of 64 rows,
+                // 32768 x 4096: 116 -> 111 us; of 100 rows, 50001 x 1000, rows of 2000 bytes: 80 ->
+                // 59).  g itself, whose rows start on lines, is 3 % faster without (300 x 1024,
+                // 16384 tokens).
+                if (is_gradient(MODE) && kChunks % 2 == 0 && p.tma_store && (MODE != kData || all)) {
+#pragma unroll
+                    for (int c = 0; c + 1 < kChunks; c += 2) {
+                        if (n0 + 32 * c >= p.cols) continue;
+                        uint32_t lo[16], hi[16];
+                        round16(c, lo);
+                        round16(c + 1, hi);
+                        box_free();
+#pragma unroll
+                        for (uint32_t v = 0; v < 4; ++v) {
+                            to_box(v, lo[4 * v], lo[4 * v + 1], lo[4 * v + 2], lo[4 * v + 3]);
+                            to_box(v + 4, hi[4 * v], hi[4 * v + 1], hi[4 * v + 2], hi[4 * v + 3]);
+                        }
+                        box_full();
+                        if (lane == 0) tma_store(&tm_out, boxes, n0 + 32 * c, m_box);
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const int left = p.cols - (n0 + 32 * c);    // columns that exist
+                    if (left <= 0) continue;
+                    uint32_t packed[16];
+                    round16(c, packed);
+                    char *dst = p.out + int64_t(MODE == kGrad ? m : row) * p.out_stride + int64_t(n0 + 32 * c) * 2;
+                    if constexpr (MODE == kGrad) {
+                        if (m < p.N) store_row(dst, packed);    // whole chunks: a row of g has room for them
                         continue;
                     }
                     if (p.vec_store) {
@@ -1843,6 +1880,8 @@ struct Run {
         p.vec_store = uintptr_t(out) % 32 == 0 && out_stride % 16 == 0  ? 32
                       : uintptr_t(out) % 16 == 0 && out_stride % 8 == 0 ? 16
                                                                         : 0;
+        p.tma_store = p.vec_store && c.H % 8 == 0 &&
+                      map16(to, out, r, c.H, out_stride * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
         return GLU_OK;
     }
 
