@@ -1002,13 +1002,19 @@ def _teacher(index, logit, lead):
 
 
 def _gradient(t, like, name):
-    """(tensor or None, its row stride) of a gradient: None allocates it, False leaves it out."""
+    """(tensor or None, its row stride) of a gradient: None allocates it, rows on
+    16-byte boundaries as those of x and w, False leaves it out."""
     import torch
     if t is False:
         return None, 0
     if t is None:
-        t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    elif t.shape != like.shape or t.dtype != like.dtype:
+        shape = like.shape
+        H = shape[-1]
+        wide = H + -H % 8
+        if wide == H:
+            return torch.empty(shape, dtype=like.dtype, device=like.device), H
+        return torch.empty((*shape[:-1], wide), dtype=like.dtype, device=like.device)[..., :H], wide
+    if t.shape != like.shape or t.dtype != like.dtype:
         raise ValueError(f"{name} has the wrong shape or dtype")
     return t, _mat(t, name)[1]
 
@@ -1051,7 +1057,7 @@ def linear_ce_bwd(dloss, x, w, target, loss, lse, *, dx=None, dw=None, workspace
     """(dx, dw): gradients of linear_ce's loss, given what it returned for the
     same x, w and target.  ``dloss`` (float32, one a row) is the gradient arriving
     at the loss.  ``dx`` and ``dw`` may be given, or False: not wanted (None is
-    returned in its place).  The workspace (uint8, glu_linear_ce_workspace_bytes(N,
+    returned in its place); what is allocated has rows on 16-byte boundaries.  The workspace (uint8, glu_linear_ce_workspace_bytes(N,
     H, V, 1) bytes, or less: smaller pieces of the vocabulary) is allocated here
     when not given."""
     if stream is not None:
