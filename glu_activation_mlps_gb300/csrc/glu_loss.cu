@@ -94,8 +94,9 @@ struct Shape {
     static constexpr int kBars = 2 * kStages + 2 + 2 + 1;               // full, empty, acc_full, acc_empty, done
     static constexpr int kStageOut = is_gradient(MODE) ? kEpiWarps * kBoxBytes : 0;
     static constexpr int kCols = kTileN / 2;                            // columns of one epilogue thread
-    // K slices summed in tensor memory before their sum goes to registers
-    static constexpr int kSegment = MODE == kStats || MODE == kGrad ? 16 : 64;
+    // K slices summed in tensor memory before their sum goes to registers: fewer where
+    // that costs nothing, because w's bytes bound the few rows of one block
+    static constexpr int kSegment = is_gradient(MODE) ? 64 : CTAS == 1 ? 4 : 16;
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStageOut + kBars * 8 + 16;
     static_assert(BN % 32 == 0 && BN >= 32 && kTileN <= 256, "one MMA covers the tile's columns");
     static_assert(!kTransB || kBRows % 64 == 0, "MN-major operands come in chunks of 64 columns");

@@ -166,6 +166,20 @@ def test_ce_on_exact_sums(N, H, V, dtype):
     check_ce(x, w, targets(N, V, g, "some"), torch.randint(1, 5, (N,), generator=g, device="cuda").float(), exact=True)
 
 
+@pytest.mark.parametrize("N,steps", [(64, 16), (300, 64)])
+def test_logits_are_summed_in_segments(N, steps):
+    """The logits of 4096 products: `steps` steps of 16 products in one accumulator, each of
+    which may drop two units of 2^-23 of what is in it, and one rounded addition a segment."""
+    H, V, K = 4096, 1000, 16
+    g = gen(N)
+    x, w = matrix(N, H, torch.bfloat16, g), matrix(V, H, torch.bfloat16, g, 0.1)
+    index = torch.randint(0, V, (N, K), generator=g, device="cuda")
+    _, _, top = glu.linear_distill(x, w, index, torch.zeros(N, K, device="cuda"))
+    z, A = x.double() @ w.double().T, x.double().abs() @ w.double().abs().T
+    segments = H // (16 * steps)
+    close(top, z.gather(1, index), ((2 * steps + segments) * 2.0 ** -23 * A).gather(1, index), "top_logits")
+
+
 def test_ce_confident_rows():
     """Where the target has nearly all the probability the loss and the target's
     gradient are small differences: to 2^-10 relative of what 64 bits give, on exact sums."""
