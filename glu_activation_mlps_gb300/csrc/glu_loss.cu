@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (CTAS == 1 && (MODE == kStats || MODE == kGrad)) {
         if (warp == 0 && lane == 0 && cluster < p.n_blocks)
             for (int kt = 0; kt < min(ST, (p.depth + BK - 1) / BK); ++kt)
-                tma_prefetch(&tm_b, kt * BK, cluster * S::kTileN);
+                tma_prefetch(&tm_b, kt * BK, (MODE == kGrad ? p.n_blocks - 1 - cluster : cluster) * S::kTileN);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     if constexpr (CTAS == 2)
@@ -355,6 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         o.part = t < cut.whole ? -1 : t - cut.whole;
         const int q = o.part < 0 ? 0 : o.part / tail;
         o.tile = tile_of(p.group_m, p.n_blocks, t - q * tail, m_blocks);
+        // g walks the vocabulary backwards: the forward pass before left its end in L2
+        // (with dx before dw, step of 64 x 4096, 32768 tokens: 224 -> 218 us)
+        if constexpr (MODE == kGrad) o.tile.nb = p.n_blocks - 1 - o.tile.nb;
         o.k0 = q * per_part;
         o.n_k = o.part < 0 ? k_tiles : min(per_part, k_tiles - o.k0);
         return o;
@@ -2044,10 +2047,11 @@ struct Run {
             if (int st = logits(true, first, cols, info)) return st;
             if (c.distill)
                 if (int st = named(first, cols)) return st;
-            if (c.dw)
-                if (int st = weight(first, cols, info)) return st;
+            // dx first: it finds what g's product read last of w in L2
             if (c.dx)
                 if (int st = data(first, cols, i > 0, info)) return st;
+            if (c.dw)
+                if (int st = weight(first, cols, info)) return st;
         }
         return GLU_OK;
     }
