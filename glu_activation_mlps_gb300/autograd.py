@@ -381,7 +381,12 @@ class VocabLoss(nn.Module):
     of a batch, the largest matrix of a training step, are never stored.
     forward(x, target) is the cross entropy, distill(x, index, logit) the
     distillation loss, logits(x) the plain projection (for generation, one row a
-    sequence).  ``from_linear`` shares an existing projection's weight."""
+    sequence).  ``from_linear`` shares an existing projection's weight.
+
+    A training step may be captured into a CUDA graph.  As with every module, no
+    eager autograd graph of the same parameters may be alive then (PyTorch ties
+    their gradients' accumulation to the stream of that graph): capture after the
+    eager losses are gone, or with torch.autograd.grad, as the tests do."""
 
     def __init__(self, hidden: int, vocab: int, device=None, dtype=None):
         super().__init__()
