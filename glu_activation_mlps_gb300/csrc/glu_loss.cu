@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (live) {
                     coef = p.dloss[row] * gscale;
                     shift = -p.lse[row] * kLog2e;
-                    // p - 1 at the target, without the cancellation
+                    // p - 1 at the target, without the cancellation (the loss is good to its own size)
                     if (p.target && coef != 0.0f) at_target = coef * expm1f(-p.loss[row]);
                 }
             }
@@ -588,8 +588,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(g[j]));
+                    // the sum leaves the target's own term out: beside it the other terms
+                    // of a confident row would lose the bits that are its loss
+                    if (tgt >= 32 * c && tgt < 32 * c + 32) {
+                        const int at = int(tgt) - 32 * c;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) g[j] = at == j ? 0xFF800000u : g[j];
+                    }
                 }
-                // maximum and sum of exponentials, in units of log2
+                // maximum (the target's logit included) and sum of exponentials, in units of log2
                 top *= p.c1;
                 const float base = top == -INFINITY ? 0.0f : top;
                 const f2 c1 = splat(p.c1), shift2 = splat(-base);
@@ -986,9 +993,19 @@ struct JoinParams {
     float *loss, *lse, *top_logits;
 };
 
-// The tiles' maxima and sums of one row joined, and the loss formed from them:
-// with s = sum_v 2^(c1 z_v - m) it is ln 2 (log2 s - (c1 z - m)), which keeps its
-// bits where the target's logit is the largest by far.
+// The tiles' maxima and sums of one row joined, and the loss formed from them.
+//
+// Cross entropy: s = sum over v != target of 2^(c1 z_v - m), r = c1 z_target - m and
+// q = s 2^-r, what the other tokens have beside the target's 1.  The loss is
+// log(1 + q): log1p of q where the target has more than half (it is then the
+// maximum, r is 0 but for m's rounding, and the loss is never negative and as good
+// as q, relatively), else ln 2 (log2(s + 2^r) - r), at least ln 2.  Relative to the
+// loss that is what the terms are off by: a few roundings of 2^-24 of their
+// distance from the maximum in log2 units, 2^-22 of each exponential, and the sum's.
+//
+// Distillation: sum_k p_k log p_k + ln 2 (log2 s - sum_k p_k (c1 z_k - m)), s over every
+// token: off by some 2^-23 of the sizes of its terms whatever their sum is, so a
+// student that is its teacher may see a loss of -1e-7.
 template <int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p)
 {
@@ -1028,14 +1045,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p)
         if (lane == 0) p.loss[row] = p.lse[row] = 0.0f;
         return;
     }
-    const float l2 = log2f(s);
     if (p.target) {
         if (lane == 0) {
-            p.loss[row] = kLn2 * (l2 - fmaf(p.named[m0 + r], p.c1, -base));
+            const float at = fmaf(p.named[m0 + r], p.c1, -base);
+            const float q = s * exp2f(-at), l2 = log2f(s + exp2f(at));
+            p.loss[row] = q < 1.0f ? log1pf(q) : kLn2 * (l2 - at);
             p.lse[row] = kLn2 * (base + l2);
         }
         return;
     }
+    const float l2 = log2f(s);
     const int n = p.entries[row];
     const int64_t at = int64_t(row) * p.top;
     float mean = 0.0f;          // sum of p_k (c1 z_k - m)

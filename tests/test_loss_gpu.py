@@ -521,3 +521,38 @@ def test_offsets_past_32_bits():
     val = p @ w[last:].double()
     # the tokens before hold zeros and add nothing
     close(dx, val, err @ w[last:].double().abs() * 1.01 + 2.0 ** -8 * val.abs() + 1e-6, "dx")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N", [1, 64, 300])
+def test_ce_confident_rows_relative_to_the_loss(N, dtype):
+    """Rows whose target has nearly all the probability, on exact sums: the loss, the other
+    tokens' share, is good relative to itself, down to 1e-17, and so is the target's gradient.
+
+    A term 2^-d of the target's is off by four roundings of d 2^-24 (the product with
+    log2 e, its constant, the differences in a tile and between tiles) and 2^-22 for each
+    of two exponentials; their sum by 300 roundings; log1p and expm1 by 2^-22."""
+    H, V = 128, 2000
+    g = gen(N)
+    w = matrix(V, H, dtype, g, grid=True)
+    t = torch.randint(0, V, (N,), generator=g, device="cuda")
+    x = torch.round(w[t].float() * (torch.arange(1, N + 1, device="cuda")[:, None] % 4 + 1) / 4 * 8).div(8).to(dtype)
+    loss, lse = glu.linear_ce(x, w, t)
+    s = x.double() @ w.double().T
+    d = s - s.gather(1, t[:, None])
+    want = torch.log1p(torch.exp(d).scatter_(1, t[:, None], 0.0).sum(1))
+    assert N == 1 or (want.min() < 1e-13 and want.max() > 1e-4)
+    rel = (4 * d.abs().amax(1) * math.log2(math.e) + 300) * 2.0 ** -24 + 4 * 2.0 ** -22
+    assert torch.all(loss >= 0)
+    close(loss, want, rel * want, "loss")
+    # one row's gradient alone: dw of its target is g x, three roundings (g, the product's sum is exact, dw)
+    for i in sorted({0, N // 3, N // 2, N - 1}):
+        dloss = torch.zeros(N, device="cuda")
+        dloss[i] = 2.0 ** 12
+        dw = glu.linear_ce_bwd(dloss, x, w, t, loss, lse, dx=False)[1]
+        val = 2.0 ** 12 * torch.expm1(-want[i]) * x[i].double()
+        u = U[dtype]
+        tol = (2.1 * u + rel[i]) * val.abs()
+        if dtype == torch.float16:      # steps of f16: dw's, and g's under its scale (2^12 goes to 2^13)
+            tol = tol + 2.0 ** -25 + 2.0 ** -26 * x[i].double().abs()
+        close(dw[t[i]], val, tol, "dw")
