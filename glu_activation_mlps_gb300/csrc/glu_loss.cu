@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t boxes = saddr(ostage) + uint32_t(warp - 4) * kBoxBytes;
         bool boxed = false;             // a box of this warp is with the copy engine
         float unscale = 1.0f, gscale = 1.0f;
-        if constexpr (MODE == kGrad) gscale = p.scale[0] * p.inv_t;
+        if constexpr (MODE == kGrad) gscale = p.scale[0];
         if constexpr (is_gradient(MODE)) unscale = p.scale[1];
         int use = 0;
         bool ok = true;
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if constexpr (MODE == kGrad) {
                 if (live) {
-                    coef = p.dloss[row] * gscale;
+                    coef = p.dloss[row] * p.inv_t * gscale;    // in this order: scale / T may overflow
                     shift = -p.lse[row] * kLog2e;
                     // p - 1 at the target, without the cancellation (the loss is good to its own size)
                     if (p.target && coef != 0.0f) at_target = coef * expm1f(-p.loss[row]);
@@ -1207,7 +1207,7 @@ __global__ void __launch_bounds__(128) named_grad_kernel(const NamedParams p)
     const int row = count == p.N ? m : p.rows[m];
     const int n = p.entries[row];
     const int64_t at = int64_t(row) * p.top;
-    const float coef = p.dloss[row] * (p.scale[0] * p.inv_t);
+    const float coef = p.dloss[row] * p.inv_t * p.scale[0];
     if (coef == 0.0f) return;
     const float shift = -p.lse[row] * kLog2e;
     for (int e = threadIdx.x; e < n; e += blockDim.x) {

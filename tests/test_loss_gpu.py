@@ -556,3 +556,16 @@ def test_ce_confident_rows_relative_to_the_loss(N, dtype):
         if dtype == torch.float16:      # steps of f16: dw's, and g's under its scale (2^12 goes to 2^13)
             tol = tol + 2.0 ** -25 + 2.0 ** -26 * x[i].double().abs()
         close(dw[t[i]], val, tol, "dw")
+
+
+def test_f16_scale_with_a_low_temperature():
+    """The power of two that g is scaled by times 1 / T may pass the largest float."""
+    N, H, V, K, T = 40, 64, 300, 5, 2.0 ** -10
+    g = gen(19)
+    x, w = matrix(N, H, torch.float16, g, 0.01), matrix(V, H, torch.float16, g, 0.1)
+    index, logit = teacher(N, V, K, g, torch.float32, "plain")
+    loss, lse, top = glu.linear_distill(x, w, index, logit, T)
+    for dloss in (2.0 ** -118, 2.0 ** -140):
+        dx, dw = glu.linear_distill_bwd(torch.full((N,), dloss, device="cuda"), x, w, index, logit, lse, top, T)
+        # below half of f16's smallest step
+        assert torch.all(dx == 0) and torch.all(dw == 0)
