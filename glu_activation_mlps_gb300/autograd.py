@@ -305,13 +305,32 @@ def _wanted(ctx, i):
     return None if ctx.needs_input_grad[i] else False
 
 
+def _as_rows(t, align: int = 1):
+    """t where the calls take it as it lies (a contiguous last dimension, one row stride,
+    rows on multiples of ``align`` elements), else a copy: x[:, :-1] of a batch of
+    sequences has no single row stride."""
+    n, align_bytes = t.shape[-1], align * t.element_size()
+    try:
+        rows = t.view(-1, n)
+        if t.stride(-1) == 1 and t.data_ptr() % align_bytes == 0 and (
+                rows.shape[0] <= 1 or (rows.stride(0) >= n and rows.stride(0) % align == 0)):
+            return t
+    except RuntimeError:        # not one row stride
+        pass
+    wide = t.new_empty((*t.shape[:-1], n + -n % align))[..., :n]
+    return wide.copy_(t)
+
+
 class LinearCrossEntropyFunction(torch.autograd.Function):
     """loss (float32, one a row) of the rows x under the output projection: softmax
     cross entropy over the vocabulary without keeping the logits.  The forward saves
-    its inputs and two floats a row; the backward forms the logits again."""
+    its inputs and two floats a row; the backward forms the logits again.  x and
+    target may be slices such as x[:, :-1] and tokens[:, 1:]: what the kernels do not
+    take as it lies is copied."""
 
     @staticmethod
     def forward(ctx, x, weight, target):
+        x, target = _as_rows(x, 8), target.contiguous()
         loss, lse = _linear_ce(x, weight, target)
         ctx.save_for_backward(x, weight, target, loss, lse)
         return loss
@@ -328,10 +347,12 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
 class LinearDistillationFunction(torch.autograd.Function):
     """loss (float32, one a row): the divergence of the rows' softmax over the
     vocabulary from a teacher's over its top tokens, without keeping the logits.
-    The teacher gets no gradient."""
+    The teacher gets no gradient.  x, index and logit may be slices, as in
+    LinearCrossEntropyFunction."""
 
     @staticmethod
     def forward(ctx, x, weight, index, logit, temperature: float = 1.0):
+        x, index, logit = _as_rows(x, 8), _as_rows(index), _as_rows(logit)
         loss, lse, top_logits = _linear_distill(x, weight, index, logit, temperature)
         ctx.save_for_backward(x, weight, index, logit, lse, top_logits)
         ctx.temperature = temperature

@@ -163,3 +163,51 @@ def test_training_step_in_a_graph():
     for a, b in zip(got, step()):
         assert torch.equal(a, b)
     assert math.isfinite(got[0].item())
+
+
+@pytest.mark.parametrize("hidden,dtype", [(64, torch.bfloat16), (75, torch.float16)])
+def test_shifted_targets(hidden, dtype):
+    """A batch of sequences, each row's target the next token: slices that have no single
+    row stride give what their copies give, values and gradients."""
+    B, S, V_, K = 3, 21, 500, 6
+    torch.manual_seed(1)
+    wide = hidden + -hidden % 8
+    w = (torch.randn(V_, wide, device="cuda") * 0.2).to(dtype)[:, :hidden].requires_grad_()
+    x = torch.randn(B, S, wide, device="cuda").to(dtype)[..., :hidden].requires_grad_()
+    tokens = torch.randint(0, V_, (B, S), device="cuda")
+    index, logit = torch.randint(0, V_, (B, S, K), device="cuda"), torch.randn(B, S, K, device="cuda")
+    d = torch.rand(B, S - 1, device="cuda")
+
+    def padded(t):
+        return torch.nn.functional.pad(t, (0, wide - hidden))[..., :hidden]
+
+    for f, slices in ((ag.linear_cross_entropy, (tokens[:, 1:],)),
+                      (ag.linear_distillation, (index[:, 1:], logit[:, 1:]))):
+        loss = f(x[:, :-1], w, *slices, reduction="none")
+        got = torch.autograd.grad(loss, (x, w), d)
+        flat = padded(x.detach()[:, :-1].reshape(-1, hidden)).requires_grad_()
+        want_loss = f(flat, w, *(v.reshape(B * (S - 1), *v.shape[2:]) for v in slices), reduction="none")
+        dx, dw = torch.autograd.grad(want_loss, (flat, w), d.flatten())
+        assert loss.shape == (B, S - 1) and torch.equal(loss.flatten(), want_loss)
+        assert torch.equal(got[0][:, :-1].reshape(-1, hidden), dx) and torch.equal(got[1], dw)
+        assert torch.all(got[0][:, -1] == 0)
+        assert torch.isfinite(f(x[:, :-1], w, *slices))
+
+
+def test_rows_that_do_not_lie_side_by_side():
+    """Transposed, broadcast and unaligned hidden rows, transposed and broadcast entries."""
+    torch.manual_seed(2)
+    w = (torch.randn(300, 64, device="cuda") * 0.2).bfloat16()
+    target = torch.randint(0, 300, (10,), device="cuda")
+    base = torch.randn(64 * 10 + 1, device="cuda").bfloat16()
+    views = (base[:-1].view(64, 10).t(), base[:64].expand(10, 64), base[1:].view(10, 64))
+    index = torch.randint(0, 300, (4, 10), device="cuda").t()
+    logit = torch.randn(4, device="cuda").expand(10, 4)
+    for x in views:
+        x = x.detach().requires_grad_()
+        y = x.detach().contiguous().clone().requires_grad_()
+        for f, a, b in ((ag.linear_cross_entropy, (target,), (target,)),
+                        (ag.linear_distillation, (index, logit), (index.contiguous(), logit.contiguous()))):
+            got, want = f(x, w, *a), f(y, w, *b)
+            assert torch.equal(got, want)
+            assert torch.equal(torch.autograd.grad(got, x)[0], torch.autograd.grad(want, y)[0])
