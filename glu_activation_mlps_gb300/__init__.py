@@ -405,11 +405,16 @@ def _rows(t, name):
     if t.dim() == 1:
         return 1, t.shape[0]
     lead = t.shape[:-1]
-    # leading dims must collapse to one row index with a single stride
+    # leading dims must collapse to one row index with a single stride: that of the
+    # innermost of them that has more than one entry (x[:, -1:] is one row a sequence)
     stride = t.stride(-2)
-    expect = stride
+    expect = None
     for d in range(t.dim() - 2, -1, -1):
-        if t.shape[d] != 1 and t.stride(d) != expect:
+        if t.shape[d] == 1:
+            continue
+        if expect is None:
+            stride = expect = t.stride(d)
+        elif t.stride(d) != expect:
             raise ValueError(f"{name}: leading dimensions do not collapse to one row stride")
         expect *= t.shape[d]
     n = 1

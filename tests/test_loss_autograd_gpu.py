@@ -211,3 +211,20 @@ def test_rows_that_do_not_lie_side_by_side():
             got, want = f(x, w, *a), f(y, w, *b)
             assert torch.equal(got, want)
             assert torch.equal(torch.autograd.grad(got, x)[0], torch.autograd.grad(want, y)[0])
+
+
+def test_last_row_of_each_sequence():
+    """x[:, -1:], whose innermost leading dimension has one entry: its stride says nothing."""
+    torch.manual_seed(3)
+    head = model()[3]
+    x = torch.randn(5, 9, H, device="cuda").bfloat16()
+    last, flat = x[:, -1:], x[:, -1].contiguous()
+    assert torch.equal(head.logits(last)[:, 0], head.logits(flat))
+    target = torch.randint(0, V, (5,), device="cuda")
+    loss, lse = glu.linear_ce(last, head.weight, target[:, None])
+    want = glu.linear_ce(flat, head.weight, target)
+    assert torch.equal(loss[:, 0], want[0]) and torch.equal(lse[:, 0], want[1])
+    assert torch.equal(head(last, target[:, None]), head(flat, target))
+    assert torch.equal(glu.fwd(last, last)[:, 0], glu.fwd(flat, flat))
+    q, s = glu.quantize(last)
+    assert torch.equal(q[:, 0].float(), glu.quantize(flat)[0].float())
