@@ -398,11 +398,19 @@ def linear_distillation(x, weight, index, logit, temperature: float = 1.0, reduc
 
 
 class VocabLoss(nn.Module):
-    """A model's output projection with the losses over its vocabulary: the logits
-    of a batch, the largest matrix of a training step, are never stored.
+    """A model's output projection with the losses over its vocabulary.  Nothing of
+    the logits' size lives between the passes: the forward keeps two floats a row
+    (distillation: and one an entry), the backward forms the logits again and, in
+    its workspace, the 16-bit matrix of their gradient, a piece of the vocabulary at
+    a time (1 GiB, or 256 tokens where those are more; linear_ce_bwd takes a smaller
+    workspace).
     forward(x, target) is the cross entropy, distill(x, index, logit) the
     distillation loss, logits(x) the plain projection (for generation, one row a
     sequence).  ``from_linear`` shares an existing projection's weight.
+
+    The rows x and the weight are of one type, float16 or bfloat16.  Without
+    ``dtype`` the weight gets PyTorch's default type where that is one of the two,
+    else bfloat16.
 
     A training step may be captured into a CUDA graph.  As with every module, no
     eager autograd graph of the same parameters may be alive then (PyTorch ties
@@ -413,6 +421,10 @@ class VocabLoss(nn.Module):
         super().__init__()
         if hidden % 8:
             raise ValueError("hidden must be a multiple of 8 (rows on 16-byte boundaries)")
+        if dtype is None:
+            dtype = torch.get_default_dtype()
+            if dtype not in (torch.float16, torch.bfloat16):
+                dtype = torch.bfloat16
         self.weight = nn.Parameter(torch.empty(vocab, hidden, device=device, dtype=dtype))
         nn.init.normal_(self.weight, std=hidden ** -0.5)
 

@@ -141,3 +141,19 @@ def test_python_refusals():
         glu._gradient(torch.zeros(4, 8), x, "dx")
     with pytest.raises(ValueError):
         glu._loss_workspace(torch.zeros(4), x, 4, 8, 9, 0, 0)
+
+
+def test_module_without_a_type():
+    """VocabLoss(hidden, vocab) has a type that its calls take."""
+    import torch
+    from glu_activation_mlps_gb300.autograd import VocabLoss
+    assert VocabLoss(16, 9).weight.dtype == torch.bfloat16
+    assert VocabLoss(16, 9, dtype=torch.float16).weight.dtype == torch.float16
+    before = torch.get_default_dtype()
+    try:
+        torch.set_default_dtype(torch.float16)
+        assert VocabLoss(16, 9).weight.dtype == torch.float16
+    finally:
+        torch.set_default_dtype(before)
+    lin = torch.nn.Linear(16, 9, bias=False)
+    assert VocabLoss.from_linear(lin).weight is lin.weight

@@ -228,3 +228,11 @@ def test_last_row_of_each_sequence():
     assert torch.equal(glu.fwd(last, last)[:, 0], glu.fwd(flat, flat))
     q, s = glu.quantize(last)
     assert torch.equal(q[:, 0].float(), glu.quantize(flat)[0].float())
+
+
+def test_module_as_the_readme_has_it():
+    torch.manual_seed(4)
+    x = torch.randn(20, 64, device="cuda").bfloat16().requires_grad_()
+    head = ag.VocabLoss(64, 100, device="cuda")
+    head(x, torch.randint(0, 100, (20,), device="cuda")).backward()
+    assert x.grad.dtype == head.weight.grad.dtype == torch.bfloat16
