@@ -778,7 +778,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- the small kernels
 
 constexpr int kListThreads = 256;
-constexpr int kListRows = 4096;         // rows of one block of the listing kernel at most
+constexpr int kListRows = 4096;         // rows that a block of the listing kernel places at a time
+constexpr int kListBlocks = 512;        // of the listing kernel at most
 
 struct ListParams {
     const int64_t *target;      // cross entropy: a row takes part if its target is in 0 .. V - 1
@@ -830,7 +831,9 @@ __device__ __forceinline__ void warp_row(char *dst, const char *src, int H, int 
 
 // Lists the rows that take part, in order.  Each block counts the rows before
 // its own by itself (a row is 8 bytes, from L2): one launch and no order among
-// blocks.  Where every row takes part, nothing is copied.
+// blocks, whose number is bounded so that the time grows with the rows and not with
+// their square (33.5 million rows of 8, 2 tokens: forward 300 -> 56 ms).  Where every
+// row takes part, nothing is copied.
 __global__ void __launch_bounds__(kListThreads) list_kernel(const ListParams p)
 {
     __shared__ int s_before, s_total, s_pos[kListRows];
@@ -838,7 +841,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const ListParams p)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int first = blockIdx.x * p.per_block, last = min(p.N, first + p.per_block);
+    const int first = blockIdx.x * p.per_block, last = first + min(p.per_block, p.N - first);
     if (tid == 0) {
         s_before = s_total = 0;
         s_amax = 0;
@@ -874,17 +877,6 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const ListParams p)
     }
     __syncthreads();
     total = s_total;
-    if (warp == 0) {
-        int pos = s_before;
-        for (int i = first; i < last; i += 32) {
-            const bool a = i + lane < last && takes_part(p, i + lane);
-            const unsigned int set = __ballot_sync(0xFFFFFFFFu, a);
-            const int at = pos + __popc(set & ((1u << lane) - 1));
-            if (a) p.rows[at] = i + lane;
-            if (i + lane < last) s_pos[i + lane - first] = a ? at : -1;
-            pos += __popc(set);
-        }
-    }
     if (blockIdx.x == 0 && tid == 0) {
         *p.count = total;
         if (p.scale) {
@@ -908,18 +900,35 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const ListParams p)
             p.cut[2] = last;
         }
     }
-    if (total == p.N && !p.copy) return;
-    __syncthreads();
-    for (int i = first + warp; i < last; i += kListThreads / 32) {
-        const int at = s_pos[i - first];
-        if (at >= 0) {
-            warp_row(p.listed + int64_t(at) * p.listed_stride, p.x + int64_t(i) * p.x_stride, p.H, lane);
-        } else {
-            if (p.dx) warp_row(p.dx + int64_t(i) * p.dx_stride, nullptr, p.H, lane);
-            if (lane == 0 && p.loss) p.loss[i] = 0.0f;
-            if (lane == 0 && p.lse) p.lse[i] = 0.0f;
+    const bool side_by_side = total != p.N || p.copy;
+    int pos = s_before;
+    for (int from = first; from < last; from += kListRows) {
+        const int to = min(last, from + kListRows);
+        if (warp == 0) {
+            for (int i = from; i < to; i += 32) {
+                const bool a = i + lane < to && takes_part(p, i + lane);
+                const unsigned int set = __ballot_sync(0xFFFFFFFFu, a);
+                const int at = pos + __popc(set & ((1u << lane) - 1));
+                if (a) p.rows[at] = i + lane;
+                if (i + lane < to) s_pos[i + lane - from] = a ? at : -1;
+                pos += __popc(set);
+            }
         }
+        if (!side_by_side) continue;
+        __syncthreads();
+        for (int i = from + warp; i < to; i += kListThreads / 32) {
+            const int at = s_pos[i - from];
+            if (at >= 0) {
+                warp_row(p.listed + int64_t(at) * p.listed_stride, p.x + int64_t(i) * p.x_stride, p.H, lane);
+            } else {
+                if (p.dx) warp_row(p.dx + int64_t(i) * p.dx_stride, nullptr, p.H, lane);
+                if (lane == 0 && p.loss) p.loss[i] = 0.0f;
+                if (lane == 0 && p.lse) p.lse[i] = 0.0f;
+            }
+        }
+        __syncthreads();            // the positions have been read
     }
+    if (!side_by_side) return;
     // the last slice of rows of g^T x reads whole multiples of 64 rows
     const int end = min(p.N, max(BK, (total + BK - 1) / BK * BK));
     for (int i = total + blockIdx.x * (kListThreads / 32) + warp; i < end; i += gridDim.x * (kListThreads / 32))
@@ -1719,9 +1728,8 @@ struct Run {
         l.entries = c.distill ? at<int>(plan.entries) : nullptr;
         l.V = c.V;
         l.N = int(c.N);
-        l.per_block = int((c.N + 511) / 512);
+        l.per_block = int((c.N + kListBlocks - 1) / kListBlocks);
         if (l.per_block < 16) l.per_block = 16;
-        if (l.per_block > kListRows) l.per_block = kListRows;
         l.x = static_cast<const char *>(c.x);
         l.x_stride = c.x_stride * 2;
         l.H = int(c.H);

@@ -569,3 +569,34 @@ def test_f16_scale_with_a_low_temperature():
         dx, dw = glu.linear_distill_bwd(torch.full((N,), dloss, device="cuda"), x, w, index, logit, lse, top, T)
         # below half of f16's smallest step
         assert torch.all(dx == 0) and torch.all(dw == 0)
+
+
+def test_very_many_rows():
+    """Rows that one block lists in more than one stretch."""
+    N, H, V = 512 * 4096 + 300001, 8, 3
+    g = gen(23)
+    x, w = matrix(N, H, torch.bfloat16, g), matrix(V, H, torch.bfloat16, g)
+    for masked in ("some", "last"):
+        check_ce(x, w, targets(N, V, g, masked), torch.rand(N, generator=g, device="cuda"))
+
+
+def test_time_of_very_many_rows():
+    """Eight times the rows take about eight times as long (not 64 times: the rows were
+    counted anew for every 4096 of them)."""
+    H, V = 8, 2
+    w = torch.randn(V, H, device="cuda").half()
+    took = []
+    for N in (1 << 21, 1 << 24):
+        x = torch.randn(N, H, device="cuda").half()
+        t = torch.randint(-1, V, (N,), device="cuda")
+        ws = torch.empty(glu.glu_linear_ce_workspace_bytes(N, H, V, 0), dtype=torch.uint8, device="cuda")
+        times = []
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            glu.linear_ce(x, w, t, workspace=ws)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        took.append(min(times))
+    assert took[1] <= 20 * took[0], took
