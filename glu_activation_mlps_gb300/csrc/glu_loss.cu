@@ -1610,6 +1610,7 @@ int validate(Call &c, bool *empty)
     }
     if (c.N == 0) {             // dw is 0, nothing else is left to do
         *empty = true;
+        if (c.V == 1) c.dw_stride = c.H;    // separates nothing
         if (c.backward && c.dw && c.dw_stride < c.H) return GLU_ERR_STRIDE;
         if (uintptr_t(c.dw) % 2) return GLU_ERR_STRIDE;
         return GLU_OK;

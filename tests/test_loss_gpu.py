@@ -600,3 +600,13 @@ def test_time_of_very_many_rows():
             times.append(a.elapsed_time(b))
         took.append(min(times))
     assert took[1] <= 20 * took[0], took
+
+
+def test_no_rows_and_one_token():
+    """The row stride of a matrix of one row says nothing, with no rows of x either."""
+    w = torch.ones(1, 64, dtype=torch.bfloat16, device="cuda")
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    t, f = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
+    dw = torch.full((64,), 3.0, dtype=torch.bfloat16, device="cuda").as_strided((1, 64), (1, 1))
+    glu.linear_ce_bwd(f, x, w, t, f, f, dw=dw)
+    assert torch.all(dw == 0)
