@@ -1476,6 +1476,7 @@ struct Plan {
     int ctas, bn;               // of the logits' product: blocks a tile, half its columns
     int64_t tail_rows[2];       // rows of the parts of tiles that are kept apart: of dx, of dw
     int64_t ld;                 // of the sums over pieces, in floats
+    bool lists;                 // the rows that take part are listed: not for a forward pass over one block of rows
     bool transpose;             // x transposed for dw
     bool copy;                  // x's rows copied whether or not all take part
     int64_t g_stride, listed_stride, xt_stride;     // bytes
@@ -1529,9 +1530,12 @@ Plan make_plan(const Call &c, int64_t piece)
     // 1030, 30001 tokens: backward 190 -> 185 us; of 4000 bytes, 333 x 1999, 50001,
     // it would take 290 for 286)
     p.copy = c.N > BM && c.x_stride % 16 != 0;
+    p.lists = c.backward || c.N > BM;   // where it is not, rows without a token cost nothing
     p.listed_stride = round_up(c.H, 64) * 2;
-    p.rows = take(4 * N + 64);          // the count, the scale and its inverse, the cuts, then the list (from byte 64)
-    p.listed = take(N * uint64_t(p.listed_stride));
+    if (p.lists) {
+        p.rows = take(4 * N + 64);      // the count, the scale and its inverse, the cuts, then the list (from byte 64)
+        p.listed = take(N * uint64_t(p.listed_stride));
+    }
     if (c.distill) {
         p.sorted = take(4 * N * top);
         p.order = take(4 * N * top);
@@ -1770,9 +1774,6 @@ struct Run {
         return make_map(m, type16, base, r, cols, stride_bytes, box_cols, box_rows, sw);
     }
 
-    // A forward pass over one block of rows lists nothing: rows without a token cost it nothing.
-    bool lists() const { return c.backward || plan.ctas == 2; }
-
     // One product, its grid sized for all rows.
     int product(const Variant &v, CUtensorMap &a, CUtensorMap &b, CUtensorMap &listed, CUtensorMap &out,
                 CUtensorMap &tail, Params &p, int64_t all_rows, int64_t row_bytes, glu_launch_info_t *info) const
@@ -1781,10 +1782,10 @@ struct Run {
         if (int st = slots_of(v, bf16, dev, sms, &n_slots)) return st;
         const int64_t tile_m = int64_t(BM) * v.ctas;
         const int64_t m_blocks = (all_rows + tile_m - 1) / tile_m;
-        p.count = lists() ? count() : nullptr;
+        p.count = plan.lists ? count() : nullptr;
         p.rows = rows();
         p.N = int(c.N);
-        p.copied = plan.copy && lists();
+        p.copied = plan.copy && plan.lists;
         p.n_blocks = int((p.cols + 2 * v.bn - 1) / (2 * v.bn));
         // row blocks per group: their rows of A (about 48 MiB) stay in L2 while B
         // streams past once; where one block row is more than that, tiles that run
@@ -1840,8 +1841,11 @@ struct Run {
         CUtensorMap ta, tl, tb;
         const char *w = static_cast<const char *>(c.w) + first * c.w_stride * 2;
         if (!map16(&ta, c.x, c.N, c.H, c.x_stride * 2, BK, box_a, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !map16(&tl, at<char>(plan.listed), c.N, c.H, plan.listed_stride, BK, box_a, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !map16(&tb, w, cols, c.H, c.w_stride * 2, BK, box_b, CU_TENSOR_MAP_SWIZZLE_128B))
+            return glu::cuda_fail(cudaErrorInvalidValue);
+        tl = ta;
+        if (plan.lists && !map16(&tl, at<char>(plan.listed), c.N, c.H, plan.listed_stride, BK, box_a,
+                                 CU_TENSOR_MAP_SWIZZLE_128B))
             return glu::cuda_fail(cudaErrorInvalidValue);
         Params p{};
         p.cols = int(cols);
@@ -2034,14 +2038,14 @@ struct Run {
     {
         if (c.distill)
             if (int st = teacher()) return st;
-        if (lists())
+        if (plan.lists)
             if (int st = list()) return st;
         if (int st = logits(false, 0, c.V, info)) return st;
         JoinParams j{};
         j.part = at<float2>(plan.part);
         j.n_parts = 2 * int((c.V + 2 * plan.bn - 1) / (2 * plan.bn));
         j.N = int(c.N);
-        j.count = lists() ? count() : nullptr;
+        j.count = plan.lists ? count() : nullptr;
         j.rows = rows();
         j.target = c.distill ? nullptr : c.target;
         j.V = c.V;

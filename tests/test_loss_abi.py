@@ -157,3 +157,11 @@ def test_module_without_a_type():
         torch.set_default_dtype(before)
     lin = torch.nn.Linear(16, 9, bias=False)
     assert VocabLoss.from_linear(lin).weight is lin.weight
+
+
+def test_forward_of_few_rows_has_no_room_for_x():
+    """Up to 128 rows nothing is listed, so no copy of x is made room for."""
+    for n in (1, 100, 128):
+        assert glu.glu_linear_ce_workspace_bytes(n, 65536, 1000, 0) < n * 65536
+        assert glu.glu_linear_distill_workspace_bytes(n, 65536, 1000, K, 0) < n * 65536 + 4096
+    assert glu.glu_linear_ce_workspace_bytes(129, 65536, 1000, 0) > 2 * 129 * 65536
