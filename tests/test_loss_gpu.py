@@ -610,3 +610,180 @@ def test_no_rows_and_one_token():
     dw = torch.full((64,), 3.0, dtype=torch.bfloat16, device="cuda").as_strided((1, 64), (1, 1))
     glu.linear_ce_bwd(f, x, w, t, f, f, dw=dw)
     assert torch.all(dw == 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N", [50, 300])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_gradients_that_are_not_finite_come_through(bad, N, dtype):
+    """What a gradient scaler must see: dloss of infinity or NaN in rows that take part."""
+    H, V, K = 72, 700, 5
+    g = gen(29)
+    x, w = matrix(N, H, dtype, g), matrix(V, H, dtype, g, 0.2)
+    x[x == 0] = 1.0
+    t = targets(N, V, g, "some")
+    t[3], t[N // 2 + 1] = 1, 2
+    index, logit = teacher(N, V, K, g, torch.float32, "plain")
+    dloss = torch.rand(N, generator=g, device="cuda") + 0.5
+    rows = torch.zeros(N, dtype=torch.bool, device="cuda")
+    rows[[3, N // 2 + 1]] = True
+    hurt, without = dloss.masked_fill(rows, bad), dloss.masked_fill(rows, 0.0)
+    loss, lse = glu.linear_ce(x, w, t)
+    kd, klse, top = glu.linear_distill(x, w, index, logit, 2.0)
+    for grads in (lambda d: glu.linear_ce_bwd(d, x, w, t, loss, lse),
+                  lambda d: glu.linear_distill_bwd(d, x, w, index, logit, klse, top, 2.0)):
+        (dx, dw), (dx0, dw0) = grads(hurt), grads(without)
+        assert not torch.isfinite(dx[rows]).any() and not torch.isfinite(dw).any()
+        assert torch.equal(dx[~rows], dx0[~rows]) and torch.isfinite(dx0).all() and torch.isfinite(dw0).all()
+
+
+def test_f16_gradients_far_apart():
+    """dloss over 2^24: a row all of whose g is at least 2^-27 of the largest |dloss| keeps
+    f16's relative rounding; smaller entries are rounded to multiples of 2^-37 of it at most."""
+    N, H, V = 200, 64, 300
+    g = gen(37)
+    x, w = matrix(N, H, torch.float16, g), matrix(V, H, torch.float16, g, 0.1)
+    t = targets(N, V, g, "none")
+    dloss = 2.0 ** (10 - torch.arange(N, device="cuda") % 25).float()
+    check_ce(x, w, t, dloss)            # with those steps, absolute
+    loss, lse = glu.linear_ce(x, w, t)
+    dx = glu.linear_ce_bwd(dloss, x, w, t, loss, lse, dw=False)[0]
+    x64, w64 = x.double(), w.double()
+    z = x64 @ w64.T
+    q = torch.softmax(z, 1)
+    q[torch.arange(N, device="cuda"), t] -= 1
+    gg = q * dloss.double()[:, None]
+    normal = gg.abs().amin(1) >= 2.0 ** -27 * dloss.max().double()
+    assert 50 < int(normal.sum()) < N - 50
+    dz = (H * 2.0 ** -23 * (x64.abs() @ w64.abs().T)).amax(1)[:, None]
+    # the exponential (lse's bound and the logit's), g's rounding, V products of fp32 sums, dx's rounding
+    rel = 4 * dz + 300 * 2.0 ** -24 + 2.0 ** -17 + 2.0 ** -11 * 1.01 + V * 2.0 ** -23
+    tol = (rel * gg.abs() + (gg < 0) * dloss[:, None].double() * (4 * dz + 2.0 ** -15)) @ w64.abs()
+    val = gg @ w64
+    close(dx[normal], val[normal], (tol * (1 + 2.0 ** -11) + 2.0 ** -11 * val.abs() + 2.0 ** -25)[normal], "dx")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N", [60, 300])
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_rows_that_are_not_finite(bad, N, dtype):
+    """Infinity or NaN in hidden rows that take part stays in those rows' losses and dx, and is in all of dw, as 64 bits have it."""
+    H, V, K = 72, 700, 5
+    g = gen(43)
+    x, w = matrix(N, H, dtype, g), matrix(V, H, dtype, g, 0.2)
+    w[w == 0] = 0.125
+    t = targets(N, V, g, "some")
+    t[5], t[N - 2] = 1, 699
+    index, logit = teacher(N, V, K, g, torch.float32, "plain")
+    d = torch.rand(N, generator=g, device="cuda") + 0.5
+    rows = torch.zeros(N, dtype=torch.bool, device="cuda")
+    rows[[5, N - 2]] = True
+    hurt = matrix(N, H, dtype, g)
+    hurt.copy_(x)
+    hurt[5, 7] = bad
+    hurt[N - 2, H - 1] = bad
+
+    def ce(x):
+        loss, lse = glu.linear_ce(x, w, t)
+        return (loss, lse, *glu.linear_ce_bwd(d, x, w, t, loss, lse))
+
+    def distill(x):
+        loss, lse, top = glu.linear_distill(x, w, index, logit, 2.0)
+        return (loss, lse, *glu.linear_distill_bwd(d, x, w, index, logit, lse, top, 2.0))
+
+    for f in (ce, distill):
+        got, want = f(hurt), f(x)
+        for a, b in zip(got[:3], want[:3]):
+            assert torch.equal(a[~rows], b[~rows]) and not torch.isfinite(a[rows]).any()
+        assert not torch.isfinite(got[3]).any()
+
+
+def test_tokens_that_are_not_finite():
+    """A projection row of NaN is in every row's softmax; one of infinities makes logits of
+    -inf, which have no share, or +inf, which leave nothing finite."""
+    N, H, V = 150, 64, 400
+    g = gen(47)
+    x, w = matrix(N, H, torch.bfloat16, g), matrix(V, H, torch.bfloat16, g, 0.2)
+    x[x == 0] = 1.0
+    t = targets(N, V, g, "none") % (V - 1)
+    d = torch.ones(N, device="cuda")
+    w[V - 1] = 0.0
+    w[V - 1, 3] = math.nan
+    loss, lse = glu.linear_ce(x, w, t)
+    dx, dw = glu.linear_ce_bwd(d, x, w, t, loss, lse)
+    for v in (loss, lse, dx, dw):
+        assert not torch.isfinite(v).any()
+    w[V - 1] = 0.0
+    x[:, 4] = torch.where(torch.arange(N, device="cuda") % 2 == 0, -1.0, 1.0)
+    w[V - 1, 4] = math.inf              # 0 elsewhere: logits of -inf and +inf in turn
+    loss, lse = glu.linear_ce(x, w, t)
+    low = x[:, 4] < 0
+    want = glu.linear_ce(x, w[:V - 1], t)
+    tol = 600 * 2.0 ** -24 + 2.0 ** -19 + 16 * 2.0 ** -24 * want[1].abs().double()
+    close(loss[low], want[0][low].double(), tol[low], "loss")
+    close(lse[low], want[1][low].double(), tol[low], "lse")
+    assert not torch.isfinite(loss[~low]).any()
+
+
+def test_distill_on_another_stream_and_one_gradient_only():
+    N, H, V, K, T = 200, 128, 900, 9, 1.5
+    g = gen(53)
+    x, w = matrix(N, H, torch.float16, g), matrix(V, H, torch.float16, g, 0.3)
+    index, logit = teacher(N, V, K, g, torch.float32, "ragged")
+    d = torch.rand(N, generator=g, device="cuda")
+    loss, lse, top = glu.linear_distill(x, w, index, logit, T)
+    dx, dw = glu.linear_distill_bwd(d, x, w, index, logit, lse, top, T)
+    for kw in ({"dx": False}, {"dw": False}, {"dx": False, "dw": False}):
+        a, b = glu.linear_distill_bwd(d, x, w, index, logit, lse, top, T, **kw)
+        assert a is None if "dx" in kw else torch.equal(a, dx)
+        assert b is None if "dw" in kw else torch.equal(b, dw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    loss2, lse2, top2 = glu.linear_distill(x, w, index, logit, T, stream=side)
+    got = glu.linear_distill_bwd(d, x, w, index, logit, lse2, top2, T, stream=side)
+    only = glu.linear_distill_bwd(d, x, w, index, logit, lse2, top2, T, dx=False, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip((loss, lse, top, dx, dw, dw), (loss2, lse2, top2, *got, only[1])):
+        assert torch.equal(a, b)
+    assert only[0] is None
+
+
+@pytest.mark.parametrize("H,wide", [(64, 64), (77, 80), (1, 8), (1030, 1032)])
+def test_gradients_have_rows_on_16_bytes(H, wide):
+    """dx and dw that are allocated here lie as x and w must: rows on 16-byte boundaries,
+    views of wider rows where H is no multiple of 8; the values are those of plain matrices."""
+    g = gen(59)
+    x, w = matrix(30, H, torch.float16, g).unflatten(0, (5, 6)), matrix(200, H, torch.float16, g, 0.2)
+    t = targets(30, 200, g, "none").view(5, 6)
+    loss, lse = glu.linear_ce(x, w, t)
+    d = torch.rand(5, 6, generator=g, device="cuda")
+    dx, dw = glu.linear_ce_bwd(d, x, w, t, loss, lse)
+    assert dx.shape == x.shape and dx.stride() == (6 * wide, wide, 1) and dx.data_ptr() % 16 == 0
+    assert dw.shape == w.shape and dw.stride() == (wide, 1) and dw.data_ptr() % 16 == 0
+    px, pw = torch.empty(5, 6, H, dtype=x.dtype, device="cuda"), torch.empty(200, H, dtype=x.dtype, device="cuda")
+    glu.linear_ce_bwd(d, x, w, t, loss, lse, dx=px, dw=pw)
+    assert torch.equal(px, dx) and torch.equal(pw, dw)
+
+
+@pytest.mark.parametrize("N", [64, 300])
+def test_dx_is_summed_in_segments(N):
+    """dx over a large vocabulary, logits on exact sums: 256 steps of 16 products in one
+    accumulator, each of which may drop two units of 2^-23 of what is in it, and one rounded
+    addition a segment or part (32 and 16 at most); beside it g's own rounding."""
+    H, V = 64, 131072
+    g = gen(61)
+    x = matrix(N, H, torch.float16, g, grid=True) * 0.125
+    w = matrix(V, H, torch.float16, g, grid=True)
+    t = targets(N, V, g, "none")
+    dloss = torch.full((N,), 1024.0, device="cuda")
+    loss, lse = glu.linear_ce(x, w, t)
+    dx = glu.linear_ce_bwd(dloss, x, w, t, loss, lse, dw=False)[0]
+    z = x.double() @ w.double().T
+    gg = torch.softmax(z, 1)
+    gg[torch.arange(N, device="cuda"), t] -= 1
+    gg *= 1024.0
+    # g: the exponential and its argument (2^-19), lse (V / 128 parts joined, a few hundred roundings), 2^-11
+    rel = 2.0 ** -11 + 2.0 ** -19 + 600 * 2.0 ** -24 + 8 * 2.0 ** -24 * lse.abs().max().double()
+    rel = rel * 1.01 + (2 * 256 + 48) * 2.0 ** -23
+    val = gg @ w.double()
+    close(dx, val, rel * (gg.abs() @ w.double().abs()) + 2.0 ** -11 * val.abs() * 1.01 + 2.0 ** -25, "dx")
