@@ -1505,11 +1505,14 @@ int pick_bn(int64_t m_blocks, int64_t V, int64_t slots, int64_t a_rows, bool one
 
 // dw's product reads g as an MN-major operand, and x too unless it is transposed
 // first.  With x K-major the tensor cores wait less for shared memory (busy 72 % of
-// the cycles with both operands MN-major, 81 % with one); transposing moves x
-// twice.  Measured, g and dw together: 4096 x 4096 rows, 131072 tokens 5828 -> 5630
-// us, 2048 x 2048, 65536 766 -> 753; 1024 x 4096, 32768 384.9 -> 384.5, 777 x 1030,
-// 30001 129 -> 131, 300 x 1024, 16384 36.5 -> 38.
-bool transposes(int64_t N, int64_t V) { return N >= 2048 && V >= 32768; }
+// the cycles with both operands MN-major, 81 % with one), which saves some 4 % of the
+// product, 4.5e-11 N H V us; transposing takes a launch, about 1.1 us behind the
+// others, and moves x twice, 4.2e-7 N H us.  So it pays where N H (V - 9400) is above
+// 2.5e10.  Measured, g and dw together, without -> with: 4096 x 4096, 65536 tokens
+// 2389 -> 2340 us, 16384 641 -> 634, 8192 336 -> 339; 2048 x 2048, 32000 343 -> 339,
+// 16384 182 -> 180, 8192 110 -> 111; 512 x 4096, 32000 209 -> 207, 16384 120 -> 121;
+// 512 x 1024, 65536 120.4 -> 119.8, 32000 74.6 -> 74.9.
+bool transposes(int64_t N, int64_t H, int64_t V) { return double(N) * double(H) * double(V - 9400) > 2.5e10; }
 
 // Half the columns of a gradient product's tile: 128 columns where a tile of 256 would
 // be half empty.
@@ -1557,7 +1560,7 @@ Plan make_plan(const Call &c, int64_t piece)
         p.pieces = int((c.V + piece - 1) / piece);
         p.g_stride = round_up(piece, 64) * 2;
         p.g = take(N * uint64_t(p.g_stride));
-        p.transpose = c.dw && transposes(c.N, c.V);
+        p.transpose = c.dw && transposes(c.N, c.H, c.V);
         p.xt_stride = round_up(c.N, 64) * 2;
         if (p.transpose) p.xt = take(uint64_t(c.H) * uint64_t(p.xt_stride));
         // The parts of the tiles that are cut, whatever number of rows takes part.  Those of

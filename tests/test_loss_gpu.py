@@ -787,3 +787,37 @@ def test_dx_is_summed_in_segments(N):
     rel = rel * 1.01 + (2 * 256 + 48) * 2.0 ** -23
     val = gg @ w.double()
     close(dx, val, rel * (gg.abs() @ w.double().abs()) + 2.0 ** -11 * val.abs() * 1.01 + 2.0 ** -25, "dx")
+
+
+@pytest.mark.parametrize("N,H,V", [(2048, 640, 32768), (1000, 1030, 40000), (16384, 264, 16000), (300, 2056, 51111)])
+@pytest.mark.parametrize("masked", ["none", "some", "last"])
+def test_x_transposed_before_dw(N, H, V, masked):
+    """N H (V - 9400) above 2.5e10: dw's product reads x transposed."""
+    assert N * H * (V - 9400) > 2.5e10
+    g = gen(N + H)
+    x, w = matrix(N, H, torch.bfloat16, g), matrix(V, H, torch.bfloat16, g, 1.0 / math.sqrt(H))
+    t = targets(N, V, g, masked)
+    dloss = torch.rand(N, generator=g, device="cuda")
+    none = (t < 0) | (t >= V)
+    x[none] = math.nan
+    dloss[none] = math.nan
+    loss, lse, dx, dw = check_ce(x, w, t, dloss)
+    # in pieces the transposed rows are read again
+    ws = torch.full((int(glu.glu_linear_ce_workspace_bytes(N, H, V, 1) * 0.8),), 255, dtype=torch.uint8, device="cuda")
+    check_ce(x, w, t, dloss, workspace=ws)
+
+
+def test_transposed_or_not_the_same_sums():
+    """Rows that take part give the same dw whichever way x is read: 700 rows of a batch that is
+    transposed, alone in one that is not."""
+    H, V, n = 1024, 32000, 700
+    g = gen(67)
+    x, w = matrix(1200, H, torch.bfloat16, g), matrix(V, H, torch.bfloat16, g, 0.05)
+    t = targets(1200, V, g, "none")
+    t[n:] = -1
+    assert n * H * (V - 9400) < 2.5e10 < 1200 * H * (V - 9400)
+    d = torch.rand(1200, generator=g, device="cuda")
+    loss, lse = glu.linear_ce(x, w, t)
+    a = glu.linear_ce_bwd(d, x, w, t, loss, lse, dx=False)[1]
+    b = glu.linear_ce_bwd(d[:n].contiguous(), x[:n], w, t[:n].contiguous(), loss[:n].contiguous(), lse[:n].contiguous(), dx=False)[1]
+    assert torch.equal(a, b)
