@@ -744,10 +744,11 @@ int glu_linear_ce_fwd(const void *x, int64_t x_stride, const void *w, int64_t w_
  *     g[n, v] = dloss[n] (exp(z[n, v] - lse[n]) - [v = target[n]])
  *     dx = round(g w),   dw = round(g^T x)
  *
- * z is formed again from x and w.  g is rounded to `dtype` (f16: after scaling by
- * the power of two that brings the largest |dloss| to 2^13 .. 2^14, undone in
- * fp32: rows whose dloss is below 2^-20 of the largest lose bits), the products
- * are summed in fp32.
+ * z is formed again from x and w.  g is formed over the largest |dloss| (put back
+ * in fp32) and rounded to `dtype`; the products are summed in fp32.  In f16, entries
+ * with |dloss| |p - [v = target]| below 2^-27 of the largest |dloss| are rounded to
+ * multiples of 2^-37 of it: the softmax part of rows far below the largest dloss
+ * loses bits first (at p = 1 / 131072, rows below 2^-10 of it).
  *   loss, lse     as glu_linear_ce_fwd gave them for the same x, w and target.
  *   dx, dw        either may be NULL: not wanted.
  */

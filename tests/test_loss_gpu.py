@@ -821,3 +821,25 @@ def test_transposed_or_not_the_same_sums():
     a = glu.linear_ce_bwd(d, x, w, t, loss, lse, dx=False)[1]
     b = glu.linear_ce_bwd(d[:n].contiguous(), x[:n], w, t[:n].contiguous(), loss[:n].contiguous(), lse[:n].contiguous(), dx=False)[1]
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N", [40, 300])
+def test_mean_over_any_number_of_rows(N, dtype):
+    """Every row's dloss is one number that 16 bits do not hold, the target's probability is
+    below half a step and only its token has a row in the projection that is not 0: g is
+    -dloss to 2^-12, so dx is its exact value rounded once, but for 2^-12 of it."""
+    H, V = 64, 20000
+    g = gen(71)
+    x = matrix(N, H, dtype, g, 0.1)
+    w = torch.zeros(V, H, dtype=dtype, device="cuda")
+    w[777] = matrix(1, H, dtype, g, 0.3)[0]
+    t = torch.full((N,), 777, device="cuda")
+    dloss = torch.full((N,), 1024 / 3000, device="cuda")
+    loss, lse = glu.linear_ce(x, w, t)
+    dx = glu.linear_ce_bwd(dloss, x, w, t, loss, lse, dw=False)[0]
+    share = torch.softmax(x.double() @ w.double().T, 1)[:, 777:778]
+    assert share.max() < 2.0 ** -12
+    val = (share - 1) * dloss.double()[:, None] * w[777].double()
+    half_step = torch.exp2(torch.floor(torch.log2(val.abs()))) * U[dtype]
+    close(dx, val, half_step + (2.0 ** -12 + 2.0 ** -16) * val.abs() + 2.0 ** -25, "dx")
