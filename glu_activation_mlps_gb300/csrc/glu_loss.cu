@@ -1512,8 +1512,12 @@ int pick_bn(int64_t m_blocks, int64_t V, int64_t slots, int64_t a_rows, bool one
 // 2.5e10.  Measured, g and dw together, without -> with: 4096 x 4096, 65536 tokens
 // 2389 -> 2340 us, 16384 641 -> 634, 8192 336 -> 339; 2048 x 2048, 32000 343 -> 339,
 // 16384 182 -> 180, 8192 110 -> 111; 512 x 4096, 32000 209 -> 207, 16384 120 -> 121;
-// 512 x 1024, 65536 120.4 -> 119.8, 32000 74.6 -> 74.9.
-bool transposes(int64_t N, int64_t H, int64_t V) { return double(N) * double(H) * double(V - 9400) > 2.5e10; }
+// 512 x 1024, 65536 120.4 -> 119.8, 32000 74.6 -> 74.9.  Up to 128 rows dw's bytes bound
+// the product: 256 x 4096, 65536 257 -> 250, 128 x 4096, 65536 200 -> 203.
+bool transposes(int64_t N, int64_t H, int64_t V)
+{
+    return N > BM && double(N) * double(H) * double(V - 9400) > 2.5e10;
+}
 
 // Half the columns of a gradient product's tile: 128 columns where a tile of 256 would
 // be half empty.
