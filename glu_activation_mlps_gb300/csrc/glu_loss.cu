@@ -12,7 +12,8 @@
 // the backward pass forms them again, a piece of the vocabulary at a time, and
 // its epilogue turns them into g in 16 bits, which the two gradient products
 // read: g rounds to the inputs' type because one tensor-core product takes one
-// type (half a step, relative 2^-8 or 2^-11 an entry).  g is formed over the largest
+// type (half a step, relative 2^-8 or 2^-11 an entry; up to 64 rows in two parts, see
+// g_parts).  g is formed over the largest
 // |dloss| / T, which is put back in fp32: the share at a target is then -(1 - p) to
 // the last bit for p below half a step, whatever number of rows a mean divides by
 // (8192 rows of which 3277 have a target, against 64 bits in the 2-norm: dx and dw off
@@ -89,6 +90,11 @@ struct Shape {
     static constexpr int kTileN = 2 * BN;                               // columns of a tile
     static constexpr int kBRows = CTAS == 1 ? 2 * BN : BN;              // of them, loaded by one block
     static constexpr int kTileA = BM * BK * 2;
+    // dx of up to 64 rows: a stage holds both parts of g for one slice of w, the second in
+    // the tile's upper half.  One MMA reads the tile from its start, a second from the middle
+    // on; what that makes of the accumulator's upper 64 rows is no row of dx.
+    static constexpr int kAParts = MODE == kData && CTAS == 1 ? 2 : 1;
+    static constexpr int kSecondA = kTileA / 2;
     static constexpr int kTileB = kBRows * BK * 2;
     static constexpr int kStageBytes = kTileA + kTileB;
     static constexpr int kStages = kRingBytes / kStageBytes > 8 ? 8 : kRingBytes / kStageBytes;
@@ -99,7 +105,7 @@ struct Shape {
     static constexpr int kCols = kTileN / 2;                            // columns of one epilogue thread
     // K slices summed in tensor memory before their sum goes to registers: fewer where
     // that costs nothing, because w's bytes bound the few rows of one block
-    static constexpr int kSegment = is_gradient(MODE) ? 64 : CTAS == 1 ? 4 : 16;
+    static constexpr int kSegment = is_gradient(MODE) ? 64 / kAParts : CTAS == 1 ? 4 : 16;
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStageOut + kBars * 8 + 16;
     static_assert(BN % 32 == 0 && BN >= 32 && kTileN <= 256, "one MMA covers the tile's columns");
     static_assert(!kTransB || kBRows % 64 == 0, "MN-major operands come in chunks of 64 columns");
@@ -126,7 +132,7 @@ struct Params {
     int n_blocks;
     const Cut *cut;             // data, weight
     int group_m;                // row blocks per group of the tile order
-    uint32_t a_bytes;           // bytes of the A box (stats, grad, data: rows that exist, up to 128)
+    uint32_t a_bytes;           // bytes of A in a stage (stats, grad, data: rows that exist, up to 128)
     // stats
     float2 *part;               // [2 n_blocks][N]: maximum (in log2 units) and sum of half a tile's columns
     float *named;               // cross entropy: the target's logit by listed row; distillation: [N][top] by row
@@ -139,6 +145,9 @@ struct Params {
     const float *lse, *loss, *dloss;
     float inv_t;
     const float *scale;         // [0] what g is scaled by, [1] its inverse
+    // grad, data, weight
+    int parts;                  // 16-bit parts of g
+    int part_cols;              // columns of g from the first to the second
     // data, weight
     char *out;
     int64_t out_stride;         // bytes
@@ -348,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool all = count == p.N, listed = !all || p.copied;
     const int m_rows = is_weight(MODE) ? p.m_rows : count;
     const int m_blocks = max(1, (m_rows + S::kTileM - 1) / S::kTileM);
-    const int k_tiles = max(1, ((is_weight(MODE) ? count : p.depth) + BK - 1) / BK);
+    const int parts = is_weight(MODE) ? p.parts : 1;        // slices of g with one slice of x, in turn along K
+    const int k_tiles = parts * max(1, ((is_weight(MODE) ? count : p.depth) + BK - 1) / BK);
     const int n_tiles = m_blocks * p.n_blocks;
     const Cut cut = is_gradient(MODE) ? *p.cut : Cut{n_tiles, 1};
     const int tail = n_tiles - cut.whole, per_part = (k_tiles + cut.parts - 1) / cut.parts;
@@ -386,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                         const uint32_t st = saddr(smem + s * S::kStageBytes);
-                        const int k = (o.k0 + kt) * BK;
+                        const bool second = parts == 2 && ((o.k0 + kt) & 1);
+                        const int k = (parts == 2 ? (o.k0 + kt) >> 1 : o.k0 + kt) * BK;
                         // both blocks' copies count on block 0's barrier
                         uint32_t bar = saddr(&full[s]);
                         if (rank == 0)
@@ -396,9 +407,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if constexpr (S::kTransA) {
 #pragma unroll
                             for (int c = 0; c < BM / 64; ++c)
-                                tma_load<CTAS>(st + c * kChunkBytes, ma, m0 + 64 * c, k, bar);
+                                tma_load<CTAS>(st + c * kChunkBytes, ma, m0 + (second ? p.part_cols : 0) + 64 * c, k,
+                                               bar);
                         } else {
                             tma_load<CTAS>(st, ma, k, m0, bar);
+                            if constexpr (S::kAParts == 2)
+                                if (p.parts == 2) tma_load<CTAS>(st + S::kSecondA, &tm_listed, k, m0, bar);
                         }
                         if constexpr (S::kTransB) {
 #pragma unroll
@@ -458,6 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const uint64_t sa = uint64_t(kk * (S::kTransA ? 2048 : 32) >> 4);
                                 const uint64_t sb = uint64_t(kk * (S::kTransB ? 2048 : 32) >> 4);
                                 mma<CTAS>(d, da + sa, db + sb, kIdesc, more || kk != 0);
+                                if constexpr (S::kAParts == 2)
+                                    if (p.parts == 2) mma<CTAS>(d, da + sa + (S::kSecondA >> 4), db + sb, kIdesc, 1);
                             }
                             mma_commit<CTAS>(saddr(&empty[s]));
                         }
@@ -622,35 +638,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t (&g)[32] = sums[c];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        float f[2];
-                        if constexpr (MODE == kGrad) {
-                            const f2 v = fma2(pair(g, j), splat(p.c1), splat(shift));
-                            const f2 e = mul2(splat(coef), make_float2(exp2_fast(v.x), exp2_fast(v.y)));
-                            f[0] = e.x;
-                            f[1] = e.y;
-                        } else {
+                        float f[2] = {__uint_as_float(g[j]), __uint_as_float(g[j + 1])};
+                        if constexpr (is_gradient(MODE)) {
                             const f2 v = mul2(pair(g, j), splat(unscale));
                             f[0] = v.x;
                             f[1] = v.y;
                         }
                         packed[j / 2] = Cd::put(f);
                     }
-                    if constexpr (MODE == kGrad) {
-                        if (tgt >= 32 * c && tgt < 32 * c + 32) {
-                            const int at = int(tgt) - 32 * c;
+                };
+                // grad: 32 columns of g in place of their logits
+                const auto to_g = [&](int c) {
+                    uint32_t (&g)[32] = sums[c];
 #pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                const float f[2] = {at == j ? at_target : Cd::get(packed[j / 2], 0),
-                                                    at == j + 1 ? at_target : Cd::get(packed[j / 2], 1)};
-                                packed[j / 2] = Cd::put(f);
-                            }
-                        }
-                        // 0 past the piece, and in rows without a gradient, whatever their logits are
-                        const int left = p.cols - (n0 + 32 * c);
-                        const uint32_t mask = coef == 0.0f ? 0u : 0xFFFFFFFFu;
+                    for (int j = 0; j < 32; j += 2) {
+                        const f2 v = fma2(pair(g, j), splat(p.c1), splat(shift));
+                        const f2 e = mul2(splat(coef), make_float2(exp2_fast(v.x), exp2_fast(v.y)));
+                        g[j] = __float_as_uint(e.x);
+                        g[j + 1] = __float_as_uint(e.y);
+                    }
+                    if (tgt >= 32 * c && tgt < 32 * c + 32) {
+                        const int at = int(tgt) - 32 * c;
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2)
-                            packed[j / 2] &= left >= 32 ? mask : j >= left ? 0u : j + 1 >= left ? mask & 0xFFFFu : mask;
+                        for (int j = 0; j < 32; ++j) g[j] = at == j ? __float_as_uint(at_target) : g[j];
+                    }
+                    // 0 past the piece, and in rows without a gradient, whatever their logits are
+                    const int exist = coef == 0.0f ? 0 : p.cols - (n0 + 32 * c);
+                    if (exist < 32) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) g[j] = j < exist ? g[j] : 0u;
                     }
                 };
                 // A box: row `lane` is 128 bytes, its 16-byte chunk v at v ^ (lane % 8).  The
@@ -716,10 +732,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int left = p.cols - (n0 + 32 * c);    // columns that exist
                     if (left <= 0) continue;
                     uint32_t packed[16];
+                    if constexpr (MODE == kGrad) to_g(c);
                     round16(c, packed);
                     char *dst = p.out + int64_t(MODE == kGrad ? m : row) * p.out_stride + int64_t(n0 + 32 * c) * 2;
                     if constexpr (MODE == kGrad) {
                         if (m < p.N) store_row(dst, packed);    // whole chunks: a row of g has room for them
+                        if constexpr (CTAS == 1) {              // what the rounding leaves, rounded
+                            if (p.parts == 2) {
+#pragma unroll
+                                for (int j = 0; j < 32; j += 2) {
+                                    const float f[2] = {__uint_as_float(sums[c][j]) - Cd::get(packed[j / 2], 0),
+                                                        __uint_as_float(sums[c][j + 1]) - Cd::get(packed[j / 2], 1)};
+                                    packed[j / 2] = Cd::put(f);
+                                }
+                                if (m < p.N) store_row(dst + int64_t(p.part_cols) * 2, packed);
+                            }
+                        }
                         continue;
                     }
                     if (p.vec_store) {
@@ -805,6 +833,7 @@ struct ListParams {
     Cut *cut;                   // backward: of dx's product, dw's, and dw's for the last piece
     int data_blocks, data_tile_m, data_k_tiles, data_slots;
     int weight_tiles, last_tiles, weight_slots;
+    int parts;                  // of g
 };
 
 __device__ __forceinline__ bool takes_part(const ListParams &p, int i)
@@ -892,7 +921,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const ListParams p)
     if (blockIdx.x == 0 && warp == 1 && p.cut) {
         const Cut data = cut_of(max(1, (total + p.data_tile_m - 1) / p.data_tile_m) * p.data_blocks, p.data_k_tiles,
                                 p.data_slots, lane);
-        const int k_tiles = max(1, (total + BK - 1) / BK);
+        const int k_tiles = p.parts * max(1, (total + BK - 1) / BK);
         const Cut weight = cut_of(p.weight_tiles, k_tiles, p.weight_slots, lane);
         const Cut last = cut_of(p.last_tiles, k_tiles, p.weight_slots, lane);
         if (lane == 0) {
@@ -1202,6 +1231,8 @@ struct NamedParams {
     float c1, inv_t;
     char *g;
     int64_t g_stride;           // bytes
+    int parts;                  // of g, the second part_cols columns behind the first
+    int64_t part_cols;
 };
 
 // Distillation: the entries of g that the teacher names, formed anew from the
@@ -1226,8 +1257,10 @@ __global__ void __launch_bounds__(128) named_grad_kernel(const NamedParams p)
         float share = p.share[at + e];
         for (int i = e + 1; i < n && p.sorted[at + i] == v; ++i) share += p.share[at + i];
         const float z = p.top_logits[at + p.order[at + e]];
-        Codec<T>::store1(p.g + int64_t(m) * p.g_stride + (v - p.first) * 2,
-                         coef * (exp2_fast(fmaf(z, p.c1, shift)) - share));
+        const float f = coef * (exp2_fast(fmaf(z, p.c1, shift)) - share);
+        char *dst = p.g + int64_t(m) * p.g_stride + (v - p.first) * 2;
+        Codec<T>::store1(dst, f);
+        if (p.parts == 2) Codec<T>::store1(dst + p.part_cols * 2, f - Codec<T>::load1(dst));
     }
 }
 
@@ -1480,6 +1513,8 @@ struct Plan {
     bool lists;                 // the rows that take part are listed: not for a forward pass over one block of rows
     bool transpose;             // x transposed for dw
     bool copy;                  // x's rows copied whether or not all take part
+    int parts;                  // 16-bit parts of g
+    int64_t part_cols;          // columns of one
     int64_t g_stride, listed_stride, xt_stride;     // bytes
     uint64_t rows, listed, part, named, sorted, order, entries, share, entropy, g, xt, tail[2], sums, bytes;
 };
@@ -1523,6 +1558,18 @@ bool transposes(int64_t N, int64_t H, int64_t V)
 // be half empty.
 int grad_bn(int64_t H) { return H <= 128 ? 64 : 128; }
 
+// 16-bit parts of g.  One rounds g to the inputs' type.  With a second for what the
+// first leaves, g has 16 bits (f16: 22) and dx and dw are off by no more than their own
+// rounding (16 x 1024, 8192 tokens, 8 teacher's entries, against 64 bits in the 2-norm:
+// 2.4e-3 -> 1.7e-3), at twice the tensor cores' work.  Up to 64 rows that hides behind
+// w's and dw's bytes: step of 64 x 4096, 32768 tokens 216 -> 225 us, 16 x 1024, 8192
+// 45.7 -> 47.7, 64 x 1000, 50001 117 -> 125.  With more rows it does not: 96 x 4096,
+// 32768 221 -> 247, 256 x 4096 260 -> 332, 1024 x 4096 670 -> 978, 4096 x 4096, 131072
+// 9250 -> 13970; there one part is the choice, as in training with 16-bit logits (4096 x
+// 4096, 131072: off 1.82e-3 of 64 bits, 1.66e-3 of it dx's own rounding; with 64
+// teacher's entries a row 2.3e-3).
+int g_parts(int64_t N) { return N <= BM / 2 ? 2 : 1; }
+
 Plan make_plan(const Call &c, int64_t piece)
 {
     Plan p{};
@@ -1563,7 +1610,9 @@ Plan make_plan(const Call &c, int64_t piece)
     } else {
         p.piece = piece;
         p.pieces = int((c.V + piece - 1) / piece);
-        p.g_stride = round_up(piece, 64) * 2;
+        p.parts = g_parts(c.N);
+        p.part_cols = round_up(piece, 64);
+        p.g_stride = p.parts * p.part_cols * 2;
         p.g = take(N * uint64_t(p.g_stride));
         p.transpose = c.dw && transposes(c.N, c.H, c.V);
         p.xt_stride = round_up(c.N, 64) * 2;
@@ -1572,11 +1621,13 @@ Plan make_plan(const Call &c, int64_t piece)
         // dx add up over the pieces, with dw's in between: each has its own.
         const int64_t tile_n = grad_bn(c.H) * 2, n_blocks = (c.H + tile_n - 1) / tile_n;
         const auto room = [&](int64_t tiles, int64_t k_tiles, int64_t slots) {
-            const int64_t most = tiles * kMaxParts < kTailRounds * slots ? tiles * kMaxParts : kTailRounds * slots;
-            return k_tiles < 8 ? int64_t(0) : most;
+            const int64_t cuts = k_tiles / 4 < kMaxParts ? k_tiles / 4 : kMaxParts;     // of one tile at most
+            const int64_t most = tiles * cuts < kTailRounds * slots ? tiles * cuts : kTailRounds * slots;
+            return cuts < 2 ? int64_t(0) : most;
         };
         p.tail_rows[0] = c.dx ? room(m_blocks * n_blocks, (piece + BK - 1) / BK, kSms / p.ctas) * tile_m : 0;
-        p.tail_rows[1] = c.dw ? room((piece + 255) / 256 * n_blocks, (c.N + BK - 1) / BK, kSms / 2) * 256 : 0;
+        p.tail_rows[1] =
+            c.dw ? room((piece + 255) / 256 * n_blocks, p.parts * ((c.N + BK - 1) / BK), kSms / 2) * 256 : 0;
         for (int i = 0; i < 2; ++i) p.tail[i] = take(4 * uint64_t(p.tail_rows[i]) * uint64_t(tile_n));
         p.ld = round_up(c.H, 4);
         if (c.dx && p.pieces > 1) p.sums = take(4 * N * uint64_t(p.ld));
@@ -1761,6 +1812,7 @@ struct Run {
             l.cut = cuts();
             l.data_blocks = int(n_blocks);
             l.data_tile_m = BM * plan.ctas;
+            l.parts = plan.parts;
             l.data_k_tiles = int((plan.piece + BK - 1) / BK);
             l.data_slots = kSms / plan.ctas;
             l.weight_tiles = int((plan.piece + 255) / 256 * n_blocks);
@@ -1864,6 +1916,8 @@ struct Run {
         if (grad) {
             p.out = at<char>(plan.g);
             p.out_stride = plan.g_stride;
+            p.parts = plan.parts;
+            p.part_cols = int(plan.part_cols);
             p.lse = c.lse;
             p.loss = c.loss;
             p.dloss = c.dloss;
@@ -1899,6 +1953,8 @@ struct Run {
         n.inv_t = inv_t();
         n.g = at<char>(plan.g);
         n.g_stride = plan.g_stride;
+        n.parts = plan.parts;
+        n.part_cols = plan.part_cols;
         void *args[] = {&n};
         const void *fn = bf16 ? reinterpret_cast<const void *>(&named_grad_kernel<__nv_bfloat16>)
                               : reinterpret_cast<const void *>(&named_grad_kernel<__half>);
@@ -1957,21 +2013,24 @@ struct Run {
         const Variant v = ctas == 1 ? (bn == 64 ? variant<kData, 64, 1>(bf16, 12) : variant<kData, 128, 1>(bf16, 13))
                                     : (bn == 64 ? variant<kData, 64, 2>(bf16, 14) : variant<kData, 128, 2>(bf16, 15));
         const int box_a = ctas == 1 ? int(round_up(c.N, 8)) : BM;
-        CUtensorMap ta, tb, to, tt;
+        CUtensorMap ta, t2, tb, to, tt;
         const char *w = static_cast<const char *>(c.w) + first * c.w_stride * 2;
+        const uint64_t second = plan.parts == 2 ? uint64_t(plan.part_cols) * 2 : 0;
         if (!map16(&ta, at<char>(plan.g), c.N, cols, plan.g_stride, BK, box_a, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !map16(&t2, at<char>(plan.g + second), c.N, cols, plan.g_stride, BK, box_a, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !map16(&tb, w, cols, c.H, c.w_stride * 2, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B))
             return glu::cuda_fail(cudaErrorInvalidValue);
         Params p{};
         p.cols = int(c.H);
         // every piece is cut alike, so that their sums meet: a last, shorter one reads zeros past its end
         p.depth = int(plan.piece);
-        p.a_bytes = uint32_t(box_a) * BK * 2;
+        p.a_bytes = uint32_t(box_a) * BK * 2 * uint32_t(plan.parts);
         p.scale = scale();
+        p.parts = plan.parts;
         p.cut = cuts();
         if (int st = output(p, &to, &tt, ta, c.dx, c.dx_stride, c.N, bn, plan.pieces == 1 ? 0 : add ? 2 : 1, 0))
             return st;
-        if (int st = product(v, ta, tb, ta, to, tt, p, c.N, plan.g_stride, info)) return st;
+        if (int st = product(v, ta, tb, t2, to, tt, p, c.N, plan.g_stride, info)) return st;
         if (first + cols < c.V) return GLU_OK;
         return sum(p, v, false, c.dx, c.dx_stride);
     }
@@ -1984,7 +2043,9 @@ struct Run {
                               ? (bn == 64 ? variant<kWeightT, 64, 2>(bf16, 20) : variant<kWeightT, 128, 2>(bf16, 21))
                               : (bn == 64 ? variant<kWeight, 64, 2>(bf16, 16) : variant<kWeight, 128, 2>(bf16, 17));
         CUtensorMap ta, tb, tl, to, tt;
-        if (!map16(&ta, at<char>(plan.g), c.N, cols, plan.g_stride, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        // columns behind the piece's are rows of dw that do not exist
+        if (!map16(&ta, at<char>(plan.g), c.N, (plan.parts - 1) * plan.part_cols + cols, plan.g_stride, 64, BK,
+                   CU_TENSOR_MAP_SWIZZLE_128B) ||
             !(plan.transpose
                   ? map16(&tb, at<char>(plan.xt), c.H, round_up(c.N, 64), plan.xt_stride, BK, bn,
                           CU_TENSOR_MAP_SWIZZLE_128B)
@@ -1996,6 +2057,8 @@ struct Run {
         p.m_rows = int(cols);
         p.a_bytes = uint32_t(BM * BK * 2);
         p.scale = scale();
+        p.parts = plan.parts;
+        p.part_cols = int(plan.part_cols);
         p.cut = cuts() + (first + cols < c.V ? 1 : 2);
         char *out = static_cast<char *>(c.dw) + first * c.dw_stride * 2;
         if (int st = output(p, &to, &tt, ta, out, c.dw_stride, cols, bn, 0, 1)) return st;
@@ -2011,7 +2074,7 @@ struct Run {
         const int64_t tiles = m_blocks * p.n_blocks;
         // A cut saves less than a round: none from 26 rounds on.  How many rows take
         // part, which counts the tiles of dx and the slices of dw, only the GPU knows.
-        const int64_t k_tiles = ((weight ? c.N : int64_t(p.depth)) + BK - 1) / BK;
+        const int64_t k_tiles = weight ? p.parts * ((c.N + BK - 1) / BK) : (p.depth + BK - 1) / BK;
         const int slots = kSms / v.ctas;
         const bool cut = k_tiles >= 8 && (!weight || (tiles % slots != 0 && tiles < 26 * slots));
         if (!p.sums && !cut) return GLU_OK;

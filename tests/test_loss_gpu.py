@@ -843,3 +843,48 @@ def test_mean_over_any_number_of_rows(N, dtype):
     val = (share - 1) * dloss.double()[:, None] * w[777].double()
     half_step = torch.exp2(torch.floor(torch.log2(val.abs()))) * U[dtype]
     close(dx, val, half_step + (2.0 ** -12 + 2.0 ** -16) * val.abs() + 2.0 ** -25, "dx")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N", [1, 16, 50, 64])
+@pytest.mark.parametrize("op", ["ce", "distill"])
+@pytest.mark.parametrize("pieces", [False, True])
+def test_few_rows_have_g_in_two_parts(pieces, op, N, dtype):
+    """Up to 64 rows dx and dw see g rounded to twice the type's bits (2^-16 or 2^-22, in f16
+    under the scale 2^-38 of the largest at least), on exact sums: beside their own rounding
+    remain the exponential and the loss (as in ``reference``) and the sums, at most 256 steps of
+    two units of 2^-23 and 64 rounded additions."""
+    H, V, K, T = 72, 3100, 8, 1.5 if op == "distill" else 1.0
+    g = gen(N + 73)
+    x = matrix(N, H, dtype, g, grid=True) * 0.25
+    w = matrix(V, H, dtype, g, grid=True)
+    dloss = torch.rand(N, generator=g, device="cuda") + 0.5
+    if op == "ce":
+        t = targets(N, V, g, "none")
+        valid = torch.ones(N, dtype=torch.bool, device="cuda")
+        shares = torch.zeros(N, V, dtype=torch.float64, device="cuda").scatter_(1, t[:, None], 1.0)
+        ent = torch.zeros(N, dtype=torch.float64, device="cuda")
+        loss, lse = glu.linear_ce(x, w, t)
+        full = glu.glu_linear_ce_workspace_bytes(N, H, V, 1)
+    else:
+        index, logit = teacher(N, V, K, g, torch.float32, "plain")
+        _, valid, shares, ent = shares_of(index, logit, V, T)
+        loss, lse, top = glu.linear_distill(x, w, index, logit, T)
+        full = glu.glu_linear_distill_workspace_bytes(N, H, V, K, 1)
+    ws = torch.full((int(full * 0.8) if pieces else full,), 255, dtype=torch.uint8, device="cuda")
+    if op == "ce":
+        dx, dw = glu.linear_ce_bwd(dloss, x, w, t, loss, lse, workspace=ws)
+    else:
+        dx, dw = glu.linear_distill_bwd(dloss, x, w, index, logit, lse, top, T, workspace=ws)
+    ref = reference(x, w, shares, valid, ent, T, exact=True)
+    x64, w64, c = x.double(), w.double(), dloss.double()[:, None] / T
+    p = torch.softmax(x64 @ w64.T / T, 1)
+    gg, tol = c * (p - shares), ref["tol"][:, None]
+    u = U[dtype]
+    eg = c * (p * (tol + 2.0 ** -19) + shares * (tol + 2.0 ** -20))
+    eg = eg + u * u * (gg.abs() + eg) + (2.0 ** -38 * c.max() if dtype == torch.float16 else 0.0)
+    sums = (2 * 256 + 64) * 2.0 ** -23
+    for got, val, err, size, what in ((dx, gg @ w64, eg @ w64.abs(), gg.abs() @ w64.abs(), "dx"),
+                                      (dw, gg.T @ x64, eg.T @ x64.abs(), gg.abs().T @ x64.abs(), "dw")):
+        err = 1.01 * err + sums * size
+        close(got, val, err + u * (val.abs() + err) + (2.0 ** -25 if dtype == torch.float16 else 2.0 ** -134), what)
