@@ -594,7 +594,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
                     uint32_t (&g)[32] = sums[c];
-                    if (tgt >= 32 * c && tgt < 32 * c + 32) p.named[m] = pick(g, int(tgt) - 32 * c);
+                    // the target's logit counts in the maximum, but its term is left out of the sum:
+                    // beside it the other terms of a confident row would lose the bits that are its loss
+                    if (tgt >= 32 * c && tgt < 32 * c + 32) {
+                        const int at = int(tgt) - 32 * c;
+                        const float z = pick(g, at);
+                        p.named[m] = z;
+                        top = fmaxf(top, z);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) g[j] = at == j ? 0xFF800000u : g[j];
+                    }
                     while (next < n0 + 32 * c + 32) {
                         p.named[int64_t(row) * p.top + e] = pick(g, next - n0 - 32 * c);
                         ++e;
@@ -607,13 +616,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(g[j]));
-                    // the sum leaves the target's own term out: beside it the other terms
-                    // of a confident row would lose the bits that are its loss
-                    if (tgt >= 32 * c && tgt < 32 * c + 32) {
-                        const int at = int(tgt) - 32 * c;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) g[j] = at == j ? 0xFF800000u : g[j];
-                    }
                 }
                 // maximum (the target's logit included) and sum of exponentials, in units of log2
                 top *= p.c1;
@@ -1060,15 +1062,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p)
         const float hi = fmaxf(a.x, b.x), base = hi == -INFINITY ? 0.0f : hi;
         return make_float2(hi, a.y * exp2f(a.x - base) + b.y * exp2f(b.x - base));
     };
+    // warp w joins row w; what its loss needs is on the way meanwhile
+    const int r = warp, row = r < ROWS && m0 + r < count ? (count == p.N ? m0 + r : p.rows[m0 + r]) : -1;
+    const int64_t target = p.target && row >= 0 ? p.target[row] : 0;
+    const float named = p.target && row >= 0 ? p.named[m0 + r] : 0.0f;
     float2 mine = make_float2(-INFINITY, 0.0f);
     if (m < count)
 #pragma unroll 4
         for (int b = threadIdx.x / ROWS; b < p.n_parts; b += kSlices) mine = join(mine, p.part[int64_t(b) * p.N + m]);
     s_part[threadIdx.x / ROWS][threadIdx.x % ROWS] = mine;
     __syncthreads();
-    // warp w joins row w
-    const int r = warp;
-    if (r >= ROWS || m0 + r >= count) return;
+    if (row < 0) return;
     float2 v = s_part[lane][r];
 #pragma unroll
     for (int i = 32; i < kSlices; i += 32) v = join(v, s_part[lane + i][r]);
@@ -1079,14 +1083,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p)
     float s = v.y * exp2f(v.x - base);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    const int row = count == p.N ? m0 + r : p.rows[m0 + r];
-    if (p.target ? uint64_t(p.target[row]) >= uint64_t(p.V) : p.entries[row] == 0) {    // takes no part
+    if (p.target ? uint64_t(target) >= uint64_t(p.V) : p.entries[row] == 0) {   // takes no part
         if (lane == 0) p.loss[row] = p.lse[row] = 0.0f;
         return;
     }
     if (p.target) {
         if (lane == 0) {
-            const float at = fmaf(p.named[m0 + r], p.c1, -base);
+            const float at = fmaf(named, p.c1, -base);
             const float q = s * exp2f(-at), l2 = log2f(s + exp2f(at));
             p.loss[row] = q < 1.0f ? log1pf(q) : kLn2 * (l2 - at);
             p.lse[row] = kLn2 * (base + l2);
