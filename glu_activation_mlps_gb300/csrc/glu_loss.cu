@@ -830,6 +830,7 @@ struct ListParams {
     int64_t dx_stride;
     const float *dloss;         // backward
     float *scale;               // backward: what g is scaled by (and its inverse)
+    float level;                // f16, which holds 2^-24 .. 2^16: 2^13; bf16: 1
     int copy;                   // copy the rows even if all take part
     float inv_t;
     Cut *cut;                   // backward: of dx's product, dw's, and dw's for the last piece
@@ -913,11 +914,11 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const ListParams p)
     if (blockIdx.x == 0 && tid == 0) {
         *p.count = total;
         if (p.scale) {
-            // g is formed with the largest |dloss| / T at 2^13 (f16 holds 2^-24 .. 2^16); one
-            // below 2^-107 stays as far below as 2^120 leaves it
-            const float a = __uint_as_float(s_amax);
-            p.scale[0] = a == 0.0f ? 1.0f : a >= 0x1p-107f ? 0x1p13f / a : 0x1p120f;
-            p.scale[1] = a == 0.0f ? 1.0f : a >= 0x1p-107f ? a * 0x1p-13f : 0x1p-120f;
+            // g is formed with the largest |dloss| / T at `level`; one below 2^-107 stays as far
+            // below as 2^107 leaves it
+            const float a = __uint_as_float(s_amax), low = fmaxf(a, 0x1p-107f);
+            p.scale[0] = a == 0.0f ? 1.0f : p.level / low;
+            p.scale[1] = a == 0.0f ? 1.0f : low / p.level;
         }
     }
     if (blockIdx.x == 0 && warp == 1 && p.cut) {
@@ -1811,6 +1812,7 @@ struct Run {
             l.dx_stride = c.dx_stride * 2;
             l.dloss = c.dloss;
             l.scale = scale();
+            l.level = bf16 ? 1.0f : 8192.0f;
             const int64_t n_blocks = (c.H + 2 * grad_bn(c.H) - 1) / (2 * grad_bn(c.H));
             l.cut = cuts();
             l.data_blocks = int(n_blocks);

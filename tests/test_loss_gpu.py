@@ -888,3 +888,23 @@ def test_few_rows_have_g_in_two_parts(pieces, op, N, dtype):
                                       (dw, gg.T @ x64, eg.T @ x64.abs(), gg.abs().T @ x64.abs(), "dw")):
         err = 1.01 * err + sums * size
         close(got, val, err + u * (val.abs() + err) + (2.0 ** -25 if dtype == torch.float16 else 2.0 ** -134), what)
+
+
+@pytest.mark.parametrize("N", [40, 70, 300])
+def test_very_large_projection_rows(N):
+    """bf16's range: a projection of 2^116 and hidden rows of 2^-116 have ordinary logits, and a
+    dx of 2^116 times the ordinary one."""
+    H, V = 64, 900
+    g = gen(79)
+    x, w = matrix(N, H, torch.bfloat16, g, grid=True), matrix(V, H, torch.bfloat16, g, grid=True)
+    t = targets(N, V, g, "none")
+    d = torch.rand(N, generator=g, device="cuda") + 0.5
+
+    def step(x, w):
+        loss, lse = glu.linear_ce(x, w, t)
+        return loss, lse, glu.linear_ce_bwd(d, x, w, t, loss, lse, dw=False)[0]
+
+    big = 2.0 ** 116
+    got, want = step(x / big, w * big), step(x, w)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.isfinite(got[2]).all() and torch.equal(got[2] / big, want[2])
