@@ -310,6 +310,8 @@ def _as_rows(t, align: int = 1):
     rows on multiples of ``align`` elements), else a copy: x[:, :-1] of a batch of
     sequences has no single row stride."""
     n, align_bytes = t.shape[-1], align * t.element_size()
+    if n % align == 0 and t.is_contiguous() and t.data_ptr() % align_bytes == 0:
+        return t
     try:
         rows = t.view(-1, n)
         if t.stride(-1) == 1 and t.data_ptr() % align_bytes == 0 and (
