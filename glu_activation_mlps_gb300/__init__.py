@@ -1062,8 +1062,10 @@ def linear_ce_bwd(dloss, x, w, target, loss, lse, *, dx=None, dw=None, workspace
     """(dx, dw): gradients of linear_ce's loss, given what it returned for the
     same x, w and target.  ``dloss`` (float32, one a row) is the gradient arriving
     at the loss.  ``dx`` and ``dw`` may be given, or False: not wanted (None is
-    returned in its place); what is allocated has rows on 16-byte boundaries.  The workspace (uint8, glu_linear_ce_workspace_bytes(N,
-    H, V, 1) bytes, or less: smaller pieces of the vocabulary) is allocated here
+    returned in its place); what is allocated has rows on 16-byte boundaries, so for
+    an H that is no multiple of 8 it is a view of wider rows.  The workspace (uint8,
+    glu_linear_ce_workspace_bytes(N, H, V, 1) bytes, or less: smaller pieces of the
+    vocabulary) holds the logits' gradient, in 16 bits a piece; it is allocated here
     when not given."""
     if stream is not None:
         return _on_stream(stream, linear_ce_bwd, dloss, x, w, target, loss, lse, dx=dx, dw=dw, workspace=workspace)

@@ -7,18 +7,19 @@
 //     gradient        g_v  = dloss / T (exp(s_v - lse) - [target share of v])
 //                     dx   = g w,   dw = g^T x
 //
-// The logits are not kept.  The forward product's epilogue reduces each tile of
-// them to a maximum and a sum per row and picks the few logits the loss names;
-// the backward pass forms them again, a piece of the vocabulary at a time, and
-// its epilogue turns them into g in 16 bits, which the two gradient products
-// read: g rounds to the inputs' type because one tensor-core product takes one
-// type (half a step, relative 2^-8 or 2^-11 an entry; up to 64 rows in two parts, see
-// g_parts).  g is formed over the largest
-// |dloss| / T, which is put back in fp32: the share at a target is then -(1 - p) to
-// the last bit for p below half a step, whatever number of rows a mean divides by
-// (8192 rows of which 3277 have a target, against 64 bits in the 2-norm: dx and dw off
-// by 2.2e-3 -> 1.85e-3, 1.7e-3 of it their own rounding), and shares of 1 / V are normal
-// f16 numbers.  Sums are fp32 throughout.
+// The logits are not kept between the passes.  The forward product's epilogue
+// reduces each tile of them to a maximum and a sum per row and picks the few logits
+// the loss names; the backward pass forms them again, a piece of the vocabulary at a
+// time, and its epilogue turns them into g in 16 bits, which the two gradient
+// products read.  Sums are fp32 throughout.
+//
+// g rounds to the inputs' type because one tensor-core product takes one type: half
+// a step, relative 2^-8 or 2^-11 an entry; up to 64 rows in two parts (g_parts, which
+// has the price of a second part and what one costs).  It is formed over the largest
+// |dloss| / T, which is put back in fp32: the share at a target is then within p of
+// -1 for p below half a step, whatever number of rows a mean divides by (8192 rows of
+// which 3277 have a target, against 64 bits in the 2-norm: dx and dw off by 2.2e-3 ->
+// 1.85e-3, 1.7e-3 of it their own rounding), and shares of 1 / V are normal f16 numbers.
 //
 // One kernel template runs the four products (stats, grad, data, weight) on the
 // structure of glu_gemm.cu: a persistent grid; warp 0 fills a ring of 64-deep K
@@ -64,7 +65,9 @@ constexpr int kThreads = 384;           // warp 0 loads, warp 1 issues MMAs, war
 constexpr int kEpiWarps = 8;            // 32 rows each, in two halves of the columns
 // Registers of a thread: launched with 168 (65536 over 384 threads); warps 0-3
 // give theirs up to 72, the others take 216 for a row's 128 sums and what forms
-// the results: 128 x 72 + 256 x 216 = 384 x 168.
+// the results: 128 x 72 + 256 x 216 = 384 x 168.  Tiles of 256 columns spill all the
+// same (44 - 136 bytes stored and 120 - 228 loaded a thread), narrower ones 16 bytes or
+// nothing.
 constexpr int kRegsLaunch = 168, kRegsFew = 72, kRegsMany = 216;
 static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads * kRegsLaunch, "the split fits the launch");
 constexpr int kRingBytes = 192 * 1024;
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = o.part < 0 ? 0 : o.part / tail;
         o.tile = tile_of(p.group_m, p.n_blocks, t - q * tail, m_blocks);
         // g walks the vocabulary backwards: the forward pass before left its end in L2
-        // (with dx before dw, step of 64 x 4096, 32768 tokens: 224 -> 218 us)
+        // (with dx before dw, 3 % of a step of 64 x 4096, 32768 tokens)
         if constexpr (MODE == kGrad) o.tile.nb = p.n_blocks - 1 - o.tile.nb;
         o.k0 = q * per_part;
         o.n_k = o.part < 0 ? k_tiles : min(per_part, k_tiles - o.k0);
@@ -1354,7 +1357,8 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxSize = INT32_MAX - 65536;
 constexpr int kMaxTop = 1024;
-// g of one piece of the vocabulary; a smaller workspace takes smaller pieces
+// g of one piece of the vocabulary, or 256 tokens of it where those are more; a smaller
+// workspace takes smaller pieces
 constexpr uint64_t kPieceBytes = uint64_t(1) << 30;
 constexpr int64_t kMinPiece = 256;
 

@@ -103,7 +103,7 @@ typedef enum {
     GLU_ERR_CUDA = -6,    /* the CUDA runtime refused a launch or copy; see glu_last_cuda_error() */
     GLU_ERR_WORKSPACE = -7, /* host-memory entry points, glu_mlp_fwd: workspace NULL or too small for one row;
                                glu_linear_*: too small */
-    GLU_ERR_VALUE = -8      /* an argument out of range: glu_add_rmsnorm_fwd's eps, or an
+    GLU_ERR_VALUE = -8      /* an argument out of range: glu_add_rmsnorm_fwd's eps, a temperature, or an
                                operand of a tensor-core entry point or glu_add_rmsnorm_bwd's
                                dgamma that is not in device memory */
 } glu_status_t;
@@ -698,8 +698,10 @@ size_t glu_mlp_q_workspace_bytes(int64_t M, int64_t I);
  *
  * x (N x H) are a model's rows behind its last norm, w (V x H) its output
  * projection (row v holds token v, the nn.Linear layout), and z = x w^T the
- * logits: products of 16-bit values, summed in fp32 on the tensor cores, reduced
- * in the product's epilogue and never stored.  A row that names no token (its
+ * logits: products of 16-bit values, summed in fp32 on the tensor cores and reduced
+ * in the product's epilogue.  Nothing of their size is kept between the passes; a
+ * backward call forms them again and stores their gradient in its workspace, in 16
+ * bits (N <= 64: 32), a piece of the vocabulary at a time.  A row that names no token (its
  * target, or every one of its entries, lies outside 0 .. V - 1) takes no part:
  * its loss, lse and dx are 0, it adds nothing to dw, and its x, dloss and lse
  * are not used (they may hold anything, NaN included).  Rows without a token
@@ -730,6 +732,8 @@ size_t glu_mlp_q_workspace_bytes(int64_t M, int64_t I);
  *
  *     lse[n] = log sum_v exp z[n, v],   loss[n] = lse[n] - z[n, target[n]]
  *
+ * loss is never negative, and beside the logits' own errors good relative to itself
+ * (some 2^-14) however small it is.
  *   target        N int64 in device memory; any value outside 0 .. V - 1 is none.
  * glu_last_launch reports path = 13.
  */
@@ -769,7 +773,8 @@ int glu_linear_ce_bwd(const float *dloss, const void *x, int64_t x_stride, const
  *     loss[n] = sum_k p[n, k] (log p[n, k] - z[n, index[n, k]] / T + lse[n])
  *
  * the divergence of the student's softmax at T (over the whole vocabulary) from
- * the teacher's (over its K tokens).  No factor T^2 is applied.
+ * the teacher's (over its K tokens).  No factor T^2 is applied.  loss is off by some
+ * 2^-23 of the sizes of the terms above: where they cancel it may be below 0 by that.
  *   index         N x K int64, index_stride >= K; an entry outside 0 .. V - 1 is
  *                 none, and so is one whose logit is -inf: it has no share of p.
  *                 A token may occur twice: its shares add up.
@@ -804,7 +809,9 @@ int glu_linear_distill_bwd(const float *dloss, const void *x, int64_t x_stride, 
                            void *workspace, size_t workspace_bytes, glu_stream_t stream);
 
 /* Workspace bytes of a forward (backward == 0) or backward call; 0 for invalid
- * arguments.  A backward call's pieces are of at most 1 GiB. */
+ * arguments.  A backward call's pieces take 1 GiB at most, or 256 tokens where those
+ * are more (N above 2^21).  4096 x 4096, 131072 tokens: 67 MB forward, 1300 MB backward
+ * (the logits in 16 bits: 1074 MB), 204 MB where the call is given no more. */
 size_t glu_linear_ce_workspace_bytes(int64_t N, int64_t H, int64_t V, int backward);
 size_t glu_linear_distill_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K, int backward);
 
