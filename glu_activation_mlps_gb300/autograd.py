@@ -446,7 +446,7 @@ class VocabLoss(nn.Module):
 
     @torch.no_grad()
     def logits(self, x):
-        return _gemm_nt(x, self.weight)
+        return _gemm_nt(_as_rows(x, 8), self.weight)
 
     def extra_repr(self):
         return f"{self.weight.shape[1]}, vocab={self.weight.shape[0]}"

@@ -236,3 +236,11 @@ def test_module_as_the_readme_has_it():
     head = ag.VocabLoss(64, 100, device="cuda")
     head(x, torch.randint(0, 100, (20,), device="cuda")).backward()
     assert x.grad.dtype == head.weight.grad.dtype == torch.bfloat16
+
+
+def test_logits_of_slices():
+    head = model()[3]
+    x = torch.randn(4, 7, H, device="cuda").bfloat16()
+    want = head.logits(x)
+    assert torch.equal(head.logits(x[:, :-1]), want[:, :-1])
+    assert torch.equal(head.logits(x.transpose(0, 1)), want.transpose(0, 1))
