@@ -1647,7 +1647,7 @@ Plan make_plan(const Call &c, int64_t piece)
 // Pieces of at most kPieceBytes of g, about equal, whole tiles.
 int64_t default_piece(int64_t N, int64_t V)
 {
-    int64_t most = int64_t(kPieceBytes / (2 * uint64_t(N))) / kMinPiece * kMinPiece;
+    int64_t most = int64_t(kPieceBytes / (2 * uint64_t(g_parts(N)) * uint64_t(N))) / kMinPiece * kMinPiece;
     if (most < kMinPiece) most = kMinPiece;
     const int64_t pieces = (V + most - 1) / most;
     return round_up((V + pieces - 1) / pieces, kMinPiece) < V ? round_up((V + pieces - 1) / pieces, kMinPiece) : V;

@@ -165,3 +165,11 @@ def test_forward_of_few_rows_has_no_room_for_x():
         assert glu.glu_linear_ce_workspace_bytes(n, 65536, 1000, 0) < n * 65536
         assert glu.glu_linear_distill_workspace_bytes(n, 65536, 1000, K, 0) < n * 65536 + 4096
     assert glu.glu_linear_ce_workspace_bytes(129, 65536, 1000, 0) > 2 * 129 * 65536
+
+
+def test_pieces_of_g():
+    """1 GiB of g at most, whatever its parts, or 256 tokens of it where those are more."""
+    for n in (1, 63, 64, 65, 4096):
+        assert glu.glu_linear_ce_workspace_bytes(n, 64, 1 << 30, 1) < (1 << 30) + (300 << 20)
+    n = 1 << 23
+    assert 512 * n < glu.glu_linear_ce_workspace_bytes(n, 8, 1 << 20, 1) < 512 * n + n * (128 + 64) + (300 << 20)
