@@ -107,8 +107,11 @@ struct Shape {
     static constexpr int kStageOut = is_gradient(MODE) ? kEpiWarps * kBoxBytes : 0;
     static constexpr int kCols = kTileN / 2;                            // columns of one epilogue thread
     // K slices summed in tensor memory before their sum goes to registers: fewer where
-    // that costs nothing, because w's bytes bound the few rows of one block
-    static constexpr int kSegment = is_gradient(MODE) ? 64 / kAParts : CTAS == 1 ? 4 : 16;
+    // that costs little, because w's bytes bound the few rows of one block (loss of one row, 1024 x
+    // 8192, median of 40 against 64 bits: segments of 256 products 1.6e-7 in 10.0 us, of 128 1.0e-7,
+    // as fp32 products, in 10.6; 64 rows, 4096 x 32768: 48.7 and 48.8 us)
+    static constexpr int kSegment =
+        is_gradient(MODE) ? 64 / kAParts : CTAS == 2 ? 16 : MODE == kStats ? 2 : 4;
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStageOut + kBars * 8 + 16;
     static_assert(BN % 32 == 0 && BN >= 32 && kTileN <= 256, "one MMA covers the tile's columns");
     static_assert(!kTransB || kBRows % 64 == 0, "MN-major operands come in chunks of 64 columns");
