@@ -106,12 +106,16 @@ struct Shape {
     static constexpr int kBars = 2 * kStages + 2 + 2 + 1;               // full, empty, acc_full, acc_empty, done
     static constexpr int kStageOut = is_gradient(MODE) ? kEpiWarps * kBoxBytes : 0;
     static constexpr int kCols = kTileN / 2;                            // columns of one epilogue thread
-    // K slices summed in tensor memory before their sum goes to registers: fewer where
-    // that costs little, because w's bytes bound the few rows of one block (loss of one row, 1024 x
-    // 8192, median of 40 against 64 bits: segments of 256 products 1.6e-7 in 10.0 us, of 128 1.0e-7,
-    // as fp32 products, in 10.6; 64 rows, 4096 x 32768: 48.7 and 48.8 us)
-    static constexpr int kSegment =
-        is_gradient(MODE) ? 64 / kAParts : CTAS == 2 ? 16 : MODE == kStats ? 2 : 4;
+    // K slices summed in tensor memory before their sum goes to registers.  The forward pass:
+    // 768 products, where the logits are off as much as fp32 products on the ordinary cores
+    // (1024 x 4096, 32768 tokens, 2-norm against 64 bits: segments of 1024 9.9e-7 in 161 us, of
+    // 768 7.0e-7 in 163, of 512 4.7e-7 in 165, fp32 6.1e-7; 4096 x 4096, 131072: 2268, 2302, 2336
+    // us).  For few rows, whose time is w's bytes, 128 (loss of one row, 1024 x 8192, median of 40:
+    // of 256 1.6e-7 in 10.0 us, of 128 1.0e-7 in 10.6, fp32 1.0e-7; 64 rows, 4096 x 32768: 48.7 and
+    // 48.8 us).  What is rounded to 16 bits takes longer ones.
+    static constexpr int kSegment = is_gradient(MODE) ? 64 / kAParts
+                                    : MODE == kStats  ? (CTAS == 2 ? 12 : 2)
+                                                      : (CTAS == 2 ? 16 : 4);
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStageOut + kBars * 8 + 16;
     static_assert(BN % 32 == 0 && BN >= 32 && kTileN <= 256, "one MMA covers the tile's columns");
     static_assert(!kTransB || kBRows % 64 == 0, "MN-major operands come in chunks of 64 columns");
