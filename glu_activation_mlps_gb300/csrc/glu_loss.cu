@@ -15,9 +15,9 @@
 //
 // g rounds to the inputs' type because one tensor-core product takes one type: half
 // a step, relative 2^-8 or 2^-11 an entry; up to 64 rows in two parts (g_parts, which
-// has the price of a second part and what one costs).  It is formed over the largest
-// |dloss| / T, which is put back in fp32: the share at a target is then within p of
-// -1 for p below half a step, whatever number of rows a mean divides by (8192 rows of
+// has the price of a second part and what one costs).  It is formed with the largest
+// |dloss| / T at a power of two, put back in fp32: the share at a target is then within
+// p of -1 of it for p below half a step, whatever number of rows a mean divides by (8192 rows of
 // which 3277 have a target, against 64 bits in the 2-norm: dx and dw off by 2.2e-3 ->
 // 1.85e-3, 1.7e-3 of it their own rounding), and shares of 1 / V are normal f16 numbers.
 //
@@ -840,7 +840,7 @@ struct ListParams {
     int64_t dx_stride;
     const float *dloss;         // backward
     float *scale;               // backward: what g is scaled by (and its inverse)
-    float level;                // f16, which holds 2^-24 .. 2^16: 2^13; bf16: 1
+    int f16;
     int copy;                   // copy the rows even if all take part
     float inv_t;
     Cut *cut;                   // backward: of dx's product, dw's, and dw's for the last piece
@@ -924,11 +924,21 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const ListParams p)
     if (blockIdx.x == 0 && tid == 0) {
         *p.count = total;
         if (p.scale) {
-            // g is formed with the largest |dloss| / T at `level`; one below 2^-107 stays as far
-            // below as 2^107 leaves it
-            const float a = __uint_as_float(s_amax), low = fmaxf(a, 0x1p-107f);
-            p.scale[0] = a == 0.0f ? 1.0f : p.level / low;
-            p.scale[1] = a == 0.0f ? 1.0f : low / p.level;
+            // f16, which holds 2^-24 .. 2^16: the largest |dloss| / T goes to 2^13 (one below 2^-107
+            // as high as 2^120 lifts it); bf16: to the next power of two, so that g stays where fp32 has it
+            const float a = __uint_as_float(s_amax);
+            float s = 1.0f, back = 1.0f;
+            if (a > 0.0f && p.f16) {
+                const float low = fmaxf(a, 0x1p-107f);
+                s = 0x1p13f / low;
+                back = low * 0x1p-13f;
+            } else if (a > 0.0f) {
+                int e;
+                back = frexpf(a, &e);
+                s = 1.0f / back;
+            }
+            p.scale[0] = s;
+            p.scale[1] = back;
         }
     }
     if (blockIdx.x == 0 && warp == 1 && p.cut) {
@@ -1823,7 +1833,7 @@ struct Run {
             l.dx_stride = c.dx_stride * 2;
             l.dloss = c.dloss;
             l.scale = scale();
-            l.level = bf16 ? 1.0f : 8192.0f;
+            l.f16 = !bf16;
             const int64_t n_blocks = (c.H + 2 * grad_bn(c.H) - 1) / (2 * grad_bn(c.H));
             l.cut = cuts();
             l.data_blocks = int(n_blocks);

@@ -748,10 +748,10 @@ int glu_linear_ce_fwd(const void *x, int64_t x_stride, const void *w, int64_t w_
  *     g[n, v] = dloss[n] (exp(z[n, v] - lse[n]) - [v = target[n]])
  *     dx = round(g w),   dw = round(g^T x)
  *
- * z is formed again from x and w.  g is formed over the largest |dloss| (put back
- * in fp32) and rounded to `dtype`, half a step an entry, or for N <= 64 to two
- * numbers of `dtype`, the second for what the first leaves; the products are summed
- * in fp32.  Where N > 64, dx and dw are so off by up to 1.4 times what their own
+ * z is formed again from x and w.  g is formed with the largest |dloss| at a power of
+ * two (2^13 in f16, the next one in bf16; put back in fp32) and rounded to `dtype`, half
+ * a step an entry, or for N <= 64 to two numbers of `dtype`, the second for what the
+ * first leaves; the products are summed in fp32.  Where N > 64, dx and dw are so off by up to 1.4 times what their own
  * rounding alone makes (2-norm).  In f16, entries with |dloss| |p - [v = target]|
  * below 2^-27 of the largest |dloss| are rounded to multiples of 2^-37 of it: the
  * softmax part of rows far below the largest dloss loses bits first (at p = 1 /

@@ -908,3 +908,18 @@ def test_very_large_projection_rows(N):
     got, want = step(x / big, w * big), step(x, w)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert torch.isfinite(got[2]).all() and torch.equal(got[2] / big, want[2])
+
+
+@pytest.mark.parametrize("N", [4, 80, 300])
+def test_bf16_shares_at_the_lower_end_of_its_range(N):
+    """Probabilities down to 2^-132 under a dloss of 100: g keeps bf16's steps where fp32 has them."""
+    H, V = 64, 500
+    x = torch.zeros(N, H, device="cuda").bfloat16()
+    x[:, 0], x[:, 1] = 5.75, 1.0
+    w = torch.zeros(V, H, device="cuda").bfloat16()
+    w[:, 0] = -(torch.arange(V, device="cuda") % 256) / 16
+    w[:, 2] = 1.0
+    t = torch.zeros(N, dtype=torch.int64, device="cuda")
+    dloss = torch.full((N,), 0.01, device="cuda")
+    dloss[:4] = torch.tensor([100.0, 50.0, 3.0, 0.1])
+    check_ce(x, w, t, dloss, exact=True)
